@@ -130,7 +130,7 @@ def _quantise(c, x):
         r = torch.where(d > 0, b / d, torch.zeros_like(b))
         return _e2m1_code(r).flatten(-2), s.view(torch.uint8)
     b = x.float().unflatten(-1, (-1, 32))
-    d = (b.abs().amax(-1).clamp(max=65504.0) / 127.0).half()
+    d = (b.abs().amax(-1).clamp(max=65024.0) / 127.0).half()
     f = d.float().unsqueeze(-1)
     r = torch.where(f > 0, b / f, torch.zeros_like(b))
     return r.round().clamp(-127, 127).to(torch.int8).flatten(-2), d
@@ -417,7 +417,7 @@ def _exact_codes(c, x):
     b = x.reshape(*x.shape[:-1], -1, n)
     top = b.abs().max(-1).values
     if c["fmt"] == Q8_0:
-        s = (top.clamp(max=65504.0) / 127.0).to(torch.float16).double()[..., None]
+        s = (top.clamp(max=65024.0) / 127.0).to(torch.float16).double()[..., None]
         return (torch.round(torch.nan_to_num(b / s)).clamp(-127, 127) * s).reshape(x.shape)
     s = (top / 6.0).clamp(max=448.0).float().to(torch.float8_e4m3fn).double()[..., None]
     r = torch.nan_to_num(b / s)
