@@ -375,6 +375,177 @@ moe_status moe_expert_hist(const moe_layer_desc* L, const moe_buckets* b, uint32
                            int32_t decay_shift, int32_t unit_shift, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* The layer's attention side: key/value cache and attention                 */
+/* ------------------------------------------------------------------------ */
+/*
+ * The pages' engine keeps a key/value cache for its 1 to 8 request slots beside
+ * the experts and lets its precision be chosen, because the two share GPU
+ * memory (aiopssre.com, "Concurrency divides context unless you pay for more
+ * cache"; devotd.net (en), "--parallel slots and KV cache allocation"); the
+ * pages give no layout.  Here the cache is paged and holds 16-bit values
+ * (MOE_FMT_BF16) or the block formats of the experts, NVFP4 (4.5 bits per
+ * value) and Q8_0 (8.5 bits per value), with blocks along the head size D.
+ *
+ * Page of page_tokens tokens (P below): for each key/value head in turn, four
+ * sections one after the other (o: token within the page, d: element):
+ *   NVFP4  K codes  u8 [P][D/2]       element d of token o in nibble d & 1
+ *          K scales E4M3 [P][D/16]
+ *          V codes  u8 [P/4][16][4][D/32]: token o, element d in byte
+ *                   (d % (D/16)) / 2 of [o/4][d/(D/16)][o%4], nibble d & 1
+ *          V scales E4M3 [D/16][P]
+ *   Q8_0   K codes  int8 [P][D];       K scales fp16 [P][D/32]
+ *          V codes  int8 [P/4][D][4]   token o, element d at [o/4][d][o%4]
+ *          V scales fp16 [D/32][P]
+ *   BF16   K [P][D];  V [P/4][D][4]    (no scales)
+ * Quantisation of a bf16 value x in a block whose largest magnitude is A, in
+ * fp32, divisions and conversions rounded to nearest even:
+ *   NVFP4  S = e4m3(min(A / (6 ts), 448)), code = e2m1(x / (S ts)) (0 when
+ *          S = 0), value code * S * ts; ts = k_scale or v_scale of the cache.
+ *   Q8_0   d = fp16(min(A, 65024) / 127), q = rint(x / d) within +-127 (0 when
+ *          d = 0), value q * d (65024 = 512 * 127, so every value fits fp16).
+ * A block that holds an infinity or a NaN gets a NaN scale, so all its values
+ * read as NaN.
+ */
+#define MOE_FMT_BF16 6  /* 16-bit cache values, as they are */
+
+/* Host struct: a layer's cache.  pool is device memory, 256-byte aligned, of
+ * n_pages * moe_kv_page_bytes(...) bytes; it needs no particular contents. */
+typedef struct moe_kv_cache {
+  int32_t fmt;          /* MOE_FMT_NVFP4, MOE_FMT_Q8_0 or MOE_FMT_BF16 */
+  int32_t n_kv;         /* key/value heads, 1..1024 */
+  int32_t D;            /* head size: 64, 128 or 256 */
+  int32_t page_tokens;  /* 32, 64, 128 or 256 */
+  int32_t n_pages;      /* pages in the pool, >= 1 */
+  float k_scale;        /* NVFP4 per-tensor scales, finite and > 0 (not read */
+  float v_scale;        /*   for the other formats) */
+  void* pool;
+} moe_kv_cache;
+
+/* Bytes of one page (a multiple of 256); 0 if unsupported. */
+size_t moe_kv_page_bytes(int32_t fmt, int32_t n_kv, int32_t D, int32_t page_tokens);
+
+/* Host struct holding device pointers: the sequences (request slots) of a
+ * step.  Sequence b has the packed rows row_start[b] .. row_start[b+1]-1 of
+ * the step's row arrays (none, one, or many), which are the last of its
+ * kv_len[b] tokens: row row_start[b] + i of n rows is token
+ * kv_len[b] - n + i.  Token j lies in page page_table[b][j / page_tokens].
+ * The arrays live on the device, so their contents are checked there: rows
+ * outside 0..T are not touched, a row before its sequence's first token
+ * (kv_len[b] < n) stores nothing and sees nothing, and a page outside
+ * 0..n_pages-1 (or a token past max_pages pages) is neither read nor written:
+ * whatever should have been read from it is NaN in the results. */
+typedef struct moe_seq_batch {
+  int32_t n_seq;              /* sequences, 0..65535 */
+  int32_t max_pages;          /* row length of page_table */
+  const int32_t* row_start;   /* [n_seq + 1], ascending */
+  const int32_t* kv_len;      /* [n_seq] */
+  const int32_t* page_table;  /* [n_seq][max_pages] */
+} moe_seq_batch;
+
+/* Host struct: what happens to a step's queries and keys before they are used. */
+typedef struct moe_qkv_desc {
+  int32_t n_q;             /* query heads, a multiple of n_kv, <= 1024 */
+  float eps;               /* of the norms, finite and >= 0 */
+  const float* q_norm;     /* device fp32 [D]: norm weights of the query heads, or NULL: no norm */
+  const float* k_norm;     /* the same for the key heads */
+  int32_t rot_dim;         /* rotated elements of a head, a multiple of 16 up to D; 0: none */
+  int32_t interleaved;     /* 1: pairs (2i, 2i+1); 0: pairs (i, i + rot_dim/2) */
+  const double* inv_freq;  /* device fp64 [rot_dim/2]: radians per position (moe_rope_freqs) */
+  float rope_scale;        /* factor of the cosines and sines (1, or moe_rope_freqs's) */
+} moe_qkv_desc;
+
+/* Frequencies of rotary positions, f_i = base^(-2i/rot_dim), stretched for
+ * contexts longer than the orig_len tokens a model was trained on by `factor`
+ * >= 1.  Host call, launches nothing; freqs: host fp64 [rot_dim/2].
+ *   MOE_ROPE_PLAIN   f_i (factor ignored)
+ *   MOE_ROPE_LINEAR  f_i / factor
+ *   MOE_ROPE_BASE    base * factor^(rot_dim/(rot_dim-2)) in place of base: the
+ *                    slowest pair is stretched by factor, the fastest not at all
+ *   MOE_ROPE_PARTS   by the turns t_i = orig_len f_i / 2 pi a pair makes over
+ *                    orig_len: f_i kept where t_i >= turns_hi, f_i / factor
+ *                    where t_i <= turns_lo, linear in the pair's index between
+ *                    (interpolation by parts); *scale = 0.1 ln(factor) + 1.
+ * scale: the value for rope_scale (1 for the other kinds). */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_BASE 2
+#define MOE_ROPE_PARTS 3
+moe_status moe_rope_freqs(int32_t kind, int32_t rot_dim, double base, double factor,
+                          double orig_len, double turns_lo, double turns_hi, double* freqs,
+                          float* scale);
+
+/* Norms of queries and keys per head, their rotation by position, and the
+ * cache's new tokens, in one pass over the projections' output:
+ *   qkv: bf16 rows of n_q query heads, n_kv key heads and n_kv value heads, D
+ *   each, qkv_stride elements apart.  For a query or key head x at position p:
+ *     z = x / sqrt(mean(x^2) + eps) * w     (with a norm weight w; else z = x)
+ *     (u, v) of pair i -> (u c - v s, v c + u s), c, s = rope_scale * cos, sin
+ *     of p * inv_freq[i],
+ *   in fp64, rounded to fp32 and then to bf16 once, so that the codes in the
+ *   cache do not depend on the order of a sum.
+ *   q_out: bf16 [T] rows of n_q * D, q_stride apart; k_out: the same with
+ *   n_kv * D, or NULL (for moe_attn_prompt, whose values may stay in qkv).
+ *   q_out and k_out may be the query and key parts of qkv itself (the same
+ *   addresses and stride); other overlaps are not allowed.
+ *   Keys and values go into the cache at the rows' tokens.  Rows at or behind
+ *   row_start[n_seq] are left as they are.  pos: device int32 [T], the rows'
+ *   rotary positions, or NULL: the token's index in its sequence.  The page
+ *   table decides where tokens go: two tokens of a call must not share a place.
+ * Strides: multiples of 8 elements, the row's width or more; pointers 16-byte
+ * aligned. */
+moe_status moe_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const moe_seq_batch* s,
+                         const uint16_t* qkv, int64_t qkv_stride, int64_t T, const int32_t* pos,
+                         uint16_t* q_out, int64_t q_stride, uint16_t* k_out, int64_t k_stride,
+                         hipStream_t stream);
+
+/* The cache read back as bf16 rows (rounded once where the format's values
+ * need it), for prompt chunks that attend to a cached prefix.  Token j of
+ * sequence b, first[b] <= j < kv_len[b], goes to row out_start[b] + j -
+ * first[b] of k_out and v_out (n_kv * D wide), as long as that row is below
+ * out_start[b+1] and R.  first: device int32 [n_seq], or NULL: 0.  out_start:
+ * device int32 [n_seq + 1], ascending.  k_out or v_out may be NULL.  row_start
+ * of the batch is not read. */
+moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int32_t* first,
+                       const int32_t* out_start, int64_t R, uint16_t* k_out, int64_t k_stride,
+                       uint16_t* v_out, int64_t v_stride, hipStream_t stream);
+
+/* Attention of a step's rows over the cache (their own tokens included): one
+ * row per sequence in a decode step, a few in a verification batch; any number
+ * is right.  Query head h uses key/value head h / (n_q / n_kv):
+ *   s_j = scale * q . k_j over the tokens j at or before the row's own,
+ *   out = sum_j softmax(s)_j v_j,
+ * sums and softmax in fp32; out bf16, zero for a row that sees no token.  The
+ * keys, values and softmax weights meet the matrix units as fp16 (block
+ * formats; the query rows scaled by a power of two each) or bf16 (16-bit
+ * cache).  What a row does not see has no influence on it, also if it is NaN or infinite.
+ * q, out: bf16 [T] rows of n_q * D (out may be q).  max_len: the longest
+ * kv_len expected; it decides how the work is split, never the result's
+ * validity (0: max_pages * page_tokens).  ws: moe_attn_workspace_bytes of the
+ * same arguments; nothing in it needs to start at zero.  Calls that may
+ * overlap need workspaces of their own. */
+size_t moe_attn_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_seq, int64_t T,
+                                int64_t max_len);
+moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_t n_q,
+                           const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
+                           float scale, uint16_t* out, int64_t out_stride, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
+
+/* Causal attention over whole prompts (or chunks of them), packed: sequence b
+ * has the query rows q_start[b] .. q_start[b+1]-1 and the key and value rows
+ * kv_start[b] .. kv_start[b+1]-1, the queries being the last of the keys'
+ * positions: query i of n sees keys j <= L - n + i of L.  The same formula,
+ * rounding and empty rows as moe_attn_decode, with bf16 operands.
+ * q_start, kv_start: device int32 [n_seq + 1], ascending; kv_start NULL: the
+ * queries' own.  q: bf16 [T] rows of n_q * D; k, v: bf16 [Tk] rows of n_kv * D;
+ * out: bf16 [T] rows of n_q * D (may be q, with the same stride).  Rows outside
+ * the sequences are left as they are; indices are held inside T and Tk. */
+moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
+                           const int32_t* q_start, const int32_t* kv_start, int64_t T, int64_t Tk,
+                           const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           int64_t k_stride, const uint16_t* v, int64_t v_stride, float scale,
+                           uint16_t* out, int64_t out_stride, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Optional cold-expert tier: pinned host RAM -> HBM slots                   */
 /* ------------------------------------------------------------------------ */
 /*

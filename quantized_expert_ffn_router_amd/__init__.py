@@ -28,10 +28,16 @@ MOE_FMT_Q6K = 2
 MOE_FMT_Q8_0 = 3
 MOE_FMT_IQ3G = 4
 MOE_FMT_IQ1G = 5
+MOE_FMT_BF16 = 6  # key/value cache only
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 
 MOE_NOALLOC_WORKSPACE_BYTES = 32 << 20
+
+MOE_ROPE_PLAIN = 0
+MOE_ROPE_LINEAR = 1
+MOE_ROPE_BASE = 2
+MOE_ROPE_PARTS = 3
 
 MOE_FFN_AUTO = 0
 MOE_FFN_GEMV = 1
@@ -78,6 +84,32 @@ class TierStats(ctypes.Structure):
                 ("hits", "misses", "h2d_bytes", "promotions", "prepares", "rebalances")]
 
 
+class KvCacheDesc(ctypes.Structure):
+    """moe_kv_cache: a layer's paged key/value cache."""
+    _fields_ = [("fmt", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("pool", ctypes.c_void_p)]
+
+
+class SeqBatch(ctypes.Structure):
+    """moe_seq_batch: a step's sequences (device pointers)."""
+    _fields_ = [("n_seq", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
+class QkvDesc(ctypes.Structure):
+    """moe_qkv_desc: norms and rotation of a step's queries and keys."""
+    _fields_ = [("n_q", ctypes.c_int32), ("eps", ctypes.c_float), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("rope_scale", ctypes.c_float)]
+
+
+assert ctypes.sizeof(KvCacheDesc) == 40
+assert ctypes.sizeof(SeqBatch) == 32
+assert ctypes.sizeof(QkvDesc) == 48
 assert ctypes.sizeof(ExpertRef) == 24
 assert ctypes.sizeof(TierDesc) == 64
 assert ctypes.sizeof(LayerDesc) == 56
@@ -87,6 +119,9 @@ assert ctypes.sizeof(Buckets) == 64
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _LP = ctypes.POINTER(LayerDesc)
 _BP = ctypes.POINTER(Buckets)
+_CP = ctypes.POINTER(KvCacheDesc)
+_SP = ctypes.POINTER(SeqBatch)
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "moe_abi_version": (ctypes.c_int, []),
     "moe_last_error": (ctypes.c_char_p, []),
@@ -108,6 +143,16 @@ SIGNATURES = {
                                           _i32, _vp, _i32, _vp, _sz, _vp]),
     "moe_route_bucket": (ctypes.c_int, [_LP, _vp, _i64, _vp, _vp, _vp, _BP, _vp, _sz, _vp, _i32,
                                          _i32, _vp]),
+    "moe_kv_page_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_rope_freqs": (ctypes.c_int, [_i32, _i32, _f64, _f64, _f64, _f64, _f64, _vp, _vp]),
+    "moe_kv_append": (ctypes.c_int, [_CP, ctypes.POINTER(QkvDesc), _SP, _vp, _i64, _i64, _vp, _vp,
+                                     _i64, _vp, _i64, _vp]),
+    "moe_kv_read": (ctypes.c_int, [_CP, _SP, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "moe_attn_workspace_bytes": (_sz, [_CP, _i32, _i32, _i64, _i64]),
+    "moe_attn_decode": (ctypes.c_int, [_CP, _SP, _i32, _vp, _i64, _i64, _i64, _f32, _vp, _i64, _vp,
+                                       _sz, _vp]),
+    "moe_attn_prompt": (ctypes.c_int, [_i32, _i32, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp,
+                                       _i64, _vp, _i64, _f32, _vp, _i64, _vp]),
     "moe_tier_create": (ctypes.c_int, [ctypes.POINTER(TierDesc), ctypes.POINTER(ctypes.c_void_p)]),
     "moe_tier_prepare": (ctypes.c_int, [_vp, _i32, _BP, _vp, _vp]),
     "moe_tier_prepare_async": (ctypes.c_int, [_vp, _i32, _BP, _vp, _vp]),
@@ -242,6 +287,48 @@ def moe_layer_forward(desc, x, T, residual, out, logits, topk_idx, topk_w, bucke
                                    _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
                                    ctypes.byref(buckets), _ptr(hist), decay_shift, unit_shift,
                                    _ptr(y), y_dtype, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_kv_page_bytes(fmt, n_kv, D, page_tokens) -> int:
+    return lib().moe_kv_page_bytes(fmt, n_kv, D, page_tokens)
+
+
+def moe_rope_freqs(kind, rot_dim, base, factor=1.0, orig_len=0.0, turns_lo=1.0, turns_hi=32.0):
+    """(frequencies float64 [rot_dim/2], rope_scale) of rotary positions."""
+    f, scale = np.zeros(max(rot_dim // 2, 1), np.float64), ctypes.c_float()
+    _check(lib().moe_rope_freqs(kind, rot_dim, base, factor, orig_len, turns_lo, turns_hi,
+                                f.ctypes.data, ctypes.addressof(scale)))
+    return f, scale.value
+
+
+def moe_kv_append(cache, qkv_desc, seqs, qkv, qkv_stride, T, pos, q_out, q_stride, k_out=None,
+                  k_stride=0, stream=None):
+    _check(lib().moe_kv_append(ctypes.byref(cache), ctypes.byref(qkv_desc), ctypes.byref(seqs),
+                               _ptr(qkv), qkv_stride, T, _ptr(pos), _ptr(q_out), q_stride,
+                               _ptr(k_out), k_stride, _stream(stream)))
+
+
+def moe_kv_read(cache, seqs, first, out_start, R, k_out, k_stride, v_out, v_stride, stream=None):
+    _check(lib().moe_kv_read(ctypes.byref(cache), ctypes.byref(seqs), _ptr(first), _ptr(out_start),
+                             R, _ptr(k_out), k_stride, _ptr(v_out), v_stride, _stream(stream)))
+
+
+def moe_attn_workspace_bytes(cache, n_q, n_seq, T, max_len=0) -> int:
+    return lib().moe_attn_workspace_bytes(ctypes.byref(cache), n_q, n_seq, T, max_len)
+
+
+def moe_attn_decode(cache, seqs, n_q, q, q_stride, T, max_len, scale, out, out_stride, ws, ws_bytes,
+                    stream=None):
+    _check(lib().moe_attn_decode(ctypes.byref(cache), ctypes.byref(seqs), n_q, _ptr(q), q_stride, T,
+                                 max_len, scale, _ptr(out), out_stride, _ptr(ws), ws_bytes,
+                                 _stream(stream)))
+
+
+def moe_attn_prompt(n_q, n_kv, D, n_seq, q_start, kv_start, T, Tk, q, q_stride, k, k_stride, v,
+                    v_stride, scale, out, out_stride, stream=None):
+    _check(lib().moe_attn_prompt(n_q, n_kv, D, n_seq, _ptr(q_start), _ptr(kv_start), T, Tk, _ptr(q),
+                                 q_stride, _ptr(k), k_stride, _ptr(v), v_stride, scale, _ptr(out),
+                                 out_stride, _stream(stream)))
 
 
 def moe_tier_create(desc: TierDesc) -> int:

@@ -1,11 +1,13 @@
 // api.hip -- the extern "C" entry points of libmoe: argument validation
 // (before any launch), error reporting and kernel dispatch.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
 #include <mutex>
 
+#include "attn_common.h"
 #include "gemv_common.h"
 
 // Workspace of moe_expert_ffn_noalloc: one copy per GPU, held until the
@@ -533,6 +535,267 @@ moe_status moe_expert_hist(const moe_layer_desc* L, const moe_buckets* b, uint32
     return fail(MOE_ERR_INVALID_ARG, "%s: shifts (%d, %d) must be in [0, 31]", W, decay_shift,
                 unit_shift);
   return hip_status(W, moe::launch_hist(b->counts, L->E, hist, decay_shift, unit_shift, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- attention side
+
+namespace {
+
+moe_status check_head(int D, const char* where) {
+  if (D != 64 && D != 128 && D != 256)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: D=%d (64, 128 or 256)", where, D);
+  return MOE_OK;
+}
+
+moe_status check_cache_shape(int fmt, int n_kv, int D, int P, const char* where) {
+  if (fmt != MOE_FMT_NVFP4 && fmt != MOE_FMT_Q8_0 && fmt != MOE_FMT_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: cache format %d", where, fmt);
+  if (n_kv < 1 || n_kv > 1024)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: n_kv=%d must be in 1..1024", where, n_kv);
+  if (P != 32 && P != 64 && P != 128 && P != 256)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: page_tokens=%d (32, 64, 128 or 256)", where, P);
+  return check_head(D, where);
+}
+
+moe_status check_aligned(const void* p, const char* name, const char* where) {
+  if ((uintptr_t)p % 16 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", where, name);
+  return MOE_OK;
+}
+
+moe_status check_rows(const void* p, int64_t stride, int64_t width, const char* name,
+                      const char* where) {
+  if (!p) return fail(MOE_ERR_INVALID_ARG, "%s: %s is NULL", where, name);
+  if (stride < width || stride % 8 != 0)
+    return fail(MOE_ERR_INVALID_ARG,
+                "%s: %s stride %lld must be a multiple of 8 and at least %lld", where, name,
+                (long long)stride, (long long)width);
+  return check_aligned(p, name, where);
+}
+
+moe_status check_cache(const moe_kv_cache* c, const char* where) {
+  CHECK_PTR(c, where);
+  moe_status st = check_cache_shape(c->fmt, c->n_kv, c->D, c->page_tokens, where);
+  if (st != MOE_OK) return st;
+  if (c->n_pages < 1) return fail(MOE_ERR_INVALID_ARG, "%s: n_pages=%d", where, c->n_pages);
+  if (c->fmt == MOE_FMT_NVFP4 &&
+      !(c->k_scale > 0.0f && isfinite(c->k_scale) && c->v_scale > 0.0f && isfinite(c->v_scale)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: k_scale=%g v_scale=%g must be finite and > 0", where,
+                (double)c->k_scale, (double)c->v_scale);
+  if (!c->pool) return fail(MOE_ERR_INVALID_ARG, "%s: pool is NULL", where);
+  if ((uintptr_t)c->pool % moe::kAlign != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: pool not 256-byte aligned", where);
+  return MOE_OK;
+}
+
+moe_status check_seqs(const moe_seq_batch* s, bool rows, const char* where) {
+  CHECK_PTR(s, where);
+  if (s->n_seq < 0 || s->n_seq > 65535)
+    return fail(s->n_seq < 0 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED,
+                "%s: n_seq=%d must be in 0..65535", where, s->n_seq);
+  if (s->n_seq == 0) return MOE_OK;
+  if (s->max_pages < 1) return fail(MOE_ERR_INVALID_ARG, "%s: max_pages=%d", where, s->max_pages);
+  if (rows && !s->row_start) return fail(MOE_ERR_INVALID_ARG, "%s: row_start is NULL", where);
+  if (!s->kv_len) return fail(MOE_ERR_INVALID_ARG, "%s: kv_len is NULL", where);
+  if (!s->page_table) return fail(MOE_ERR_INVALID_ARG, "%s: page_table is NULL", where);
+  return MOE_OK;
+}
+
+// Query heads against key/value heads, and the launch sizes they give.
+moe_status check_heads(int n_q, int n_kv, int64_t T, int64_t n_seq, const char* where) {
+  if (n_q < 1 || n_q > 1024 || n_kv < 1 || n_q % n_kv != 0)
+    return fail(n_q > 1024 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG,
+                "%s: n_q=%d must be a multiple of n_kv=%d, at most 1024", where, n_q, n_kv);
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T=%lld < 0", where, (long long)T);
+  if (T > kMaxT || T * n_q > ((int64_t)1 << 26) || n_seq * n_q > ((int64_t)1 << 22))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T=%lld, n_seq=%lld with n_q=%d is too large", where,
+                (long long)T, (long long)n_seq, n_q);
+  return MOE_OK;
+}
+
+moe_status check_scale(float scale, const char* where) {
+  if (!(scale > 0.0f && isfinite(scale)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: scale=%g must be finite and > 0", where, (double)scale);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_kv_page_bytes(int32_t fmt, int32_t n_kv, int32_t D, int32_t page_tokens) {
+  if (check_cache_shape(fmt, n_kv, D, page_tokens, "moe_kv_page_bytes") != MOE_OK) return 0;
+  return (size_t)n_kv * moe::kv_layout(fmt, D, page_tokens).head;
+}
+
+moe_status moe_rope_freqs(int32_t kind, int32_t rot_dim, double base, double factor,
+                          double orig_len, double turns_lo, double turns_hi, double* freqs,
+                          float* scale) {
+  const char* W = "moe_rope_freqs";
+  const double kTwoPi = 6.283185307179586;
+  if (kind < MOE_ROPE_PLAIN || kind > MOE_ROPE_PARTS)
+    return fail(MOE_ERR_INVALID_ARG, "%s: kind=%d", W, kind);
+  if (rot_dim < 16 || rot_dim > 256 || rot_dim % 16 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: rot_dim=%d must be a multiple of 16 in 16..256", W, rot_dim);
+  if (!(base > 1.0 && isfinite(base))) return fail(MOE_ERR_INVALID_ARG, "%s: base=%g", W, base);
+  if (kind != MOE_ROPE_PLAIN && !(factor >= 1.0 && isfinite(factor)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: factor=%g must be >= 1", W, factor);
+  if (kind == MOE_ROPE_PARTS && !(orig_len > 0.0 && turns_lo > 0.0 && turns_hi > turns_lo && isfinite(orig_len) && isfinite(turns_hi)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: orig_len=%g, turns %g..%g", W, orig_len, turns_lo, turns_hi);
+  CHECK_PTR(freqs, W);
+  CHECK_PTR(scale, W);
+  const int half = rot_dim / 2;
+  if (kind == MOE_ROPE_BASE) base *= pow(factor, rot_dim / (rot_dim - 2.0));
+  // the pair index whose frequency makes `turns` turns over orig_len
+  const auto index_of = [&](double turns) {
+    return rot_dim * log(orig_len / (turns * kTwoPi)) / (2.0 * log(base));
+  };
+  double lo = 0.0, hi = 0.0;
+  if (kind == MOE_ROPE_PARTS) {
+    lo = index_of(turns_hi);
+    hi = index_of(turns_lo);
+  }
+  for (int i = 0; i < half; ++i) {
+    const double f = pow(base, -2.0 * i / rot_dim);
+    if (kind == MOE_ROPE_LINEAR) {
+      freqs[i] = f / factor;
+    } else if (kind == MOE_ROPE_PARTS) {
+      double r = (i - lo) / (hi - lo);  // 0: kept, 1: stretched
+      r = r < 0.0 ? 0.0 : r > 1.0 ? 1.0 : r;
+      freqs[i] = f * (1.0 - r) + f / factor * r;
+    } else {
+      freqs[i] = f;
+    }
+  }
+  *scale = kind == MOE_ROPE_PARTS ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  return MOE_OK;
+}
+
+moe_status moe_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const moe_seq_batch* s,
+                         const uint16_t* qkv, int64_t qkv_stride, int64_t T, const int32_t* pos,
+                         uint16_t* q_out, int64_t q_stride, uint16_t* k_out, int64_t k_stride,
+                         hipStream_t stream) {
+  const char* W = "moe_kv_append";
+  moe_status st = check_cache(c, W);
+  if (st != MOE_OK) return st;
+  CHECK_PTR(p, W);
+  if ((st = check_seqs(s, true, W)) != MOE_OK) return st;
+  if ((st = check_heads(p->n_q, c->n_kv, T, s->n_seq, W)) != MOE_OK) return st;
+  if (!(p->eps >= 0.0f && isfinite(p->eps)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g", W, (double)p->eps);
+  if (p->rot_dim < 0 || p->rot_dim > c->D || p->rot_dim % 16 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: rot_dim=%d must be a multiple of 16 in 0..%d", W,
+                p->rot_dim, c->D);
+  if (p->interleaved != 0 && p->interleaved != 1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: interleaved=%d must be 0 or 1", W, p->interleaved);
+  if (p->rot_dim > 0 && (!p->inv_freq || !isfinite(p->rope_scale)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: inv_freq is NULL or rope_scale=%g", W,
+                (double)p->rope_scale);
+  if (T == 0 || s->n_seq == 0) return MOE_OK;
+  const int64_t D = c->D, qw = p->n_q * D, kw = c->n_kv * D;
+  if ((st = check_rows(qkv, qkv_stride, qw + 2 * kw, "qkv", W)) != MOE_OK) return st;
+  if ((st = check_rows(q_out, q_stride, qw, "q_out", W)) != MOE_OK) return st;
+  if (k_out && (st = check_rows(k_out, k_stride, kw, "k_out", W)) != MOE_OK) return st;
+  if ((st = check_aligned(p->q_norm, "q_norm", W)) != MOE_OK) return st;
+  if ((st = check_aligned(p->k_norm, "k_norm", W)) != MOE_OK) return st;
+  return hip_status(W, moe::launch_kv_append(c, p, s, qkv, qkv_stride, T, pos, q_out, q_stride,
+                                             k_out, k_stride, stream));
+}
+
+moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int32_t* first,
+                       const int32_t* out_start, int64_t R, uint16_t* k_out, int64_t k_stride,
+                       uint16_t* v_out, int64_t v_stride, hipStream_t stream) {
+  const char* W = "moe_kv_read";
+  moe_status st = check_cache(c, W);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(s, false, W)) != MOE_OK) return st;
+  if (R < 0) return fail(MOE_ERR_INVALID_ARG, "%s: R=%lld < 0", W, (long long)R);
+  if (R > (int64_t)1 << 28)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: R=%lld too large", W, (long long)R);
+  if (R == 0 || s->n_seq == 0 || (!k_out && !v_out)) return MOE_OK;
+  CHECK_PTR(out_start, W);
+  const int64_t kw = (int64_t)c->n_kv * c->D;
+  if (k_out && (st = check_rows(k_out, k_stride, kw, "k_out", W)) != MOE_OK) return st;
+  if (v_out && (st = check_rows(v_out, v_stride, kw, "v_out", W)) != MOE_OK) return st;
+  return hip_status(W, moe::launch_kv_read(c, s, first, out_start, R, k_out, k_stride, v_out,
+                                           v_stride, stream));
+}
+
+size_t moe_attn_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_seq, int64_t T,
+                                int64_t max_len) {
+  const char* W = "moe_attn_workspace_bytes";
+  if (!c) {
+    fail(MOE_ERR_INVALID_ARG, "%s: c is NULL", W);
+    return 0;
+  }
+  if (check_cache_shape(c->fmt, c->n_kv, c->D, c->page_tokens, W) != MOE_OK) return 0;
+  if (check_heads(n_q, c->n_kv, T, n_seq, W) != MOE_OK) return 0;
+  if (n_seq < 0 || max_len < 0) {
+    fail(MOE_ERR_INVALID_ARG, "%s: n_seq=%d max_len=%lld", W, n_seq, (long long)max_len);
+    return 0;
+  }
+  // max_len 0 stands for the page table's capacity, which is not known here:
+  // the longest cache gives the largest split
+  return moe::attn_decode_ws_bytes(c->n_kv, c->D, n_q, n_seq, T, max_len ? max_len : INT32_MAX);
+}
+
+moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_t n_q,
+                           const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
+                           float scale, uint16_t* out, int64_t out_stride, void* ws,
+                           size_t ws_bytes, hipStream_t stream) {
+  const char* W = "moe_attn_decode";
+  moe_status st = check_cache(c, W);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(s, true, W)) != MOE_OK) return st;
+  if ((st = check_heads(n_q, c->n_kv, T, s->n_seq, W)) != MOE_OK) return st;
+  if ((st = check_scale(scale, W)) != MOE_OK) return st;
+  if (max_len < 0) return fail(MOE_ERR_INVALID_ARG, "%s: max_len=%lld < 0", W, (long long)max_len);
+  if (T == 0 || s->n_seq == 0) return MOE_OK;
+  const int64_t qw = (int64_t)n_q * c->D;
+  if ((st = check_rows(q, q_stride, qw, "q", W)) != MOE_OK) return st;
+  if ((st = check_rows(out, out_stride, qw, "out", W)) != MOE_OK) return st;
+  if (max_len == 0) max_len = (int64_t)s->max_pages * c->page_tokens;
+  const size_t need = moe::attn_decode_ws_bytes(c->n_kv, c->D, n_q, s->n_seq, T, max_len);
+  if (need > 0) {
+    CHECK_PTR(ws, W);
+    if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu", W, ws_bytes, need);
+    if ((st = check_aligned(ws, "ws", W)) != MOE_OK) return st;
+  }
+  return hip_status(W, moe::launch_attn_decode(c, s, n_q, q, q_stride, T, max_len, scale, out,
+                                               out_stride, ws, stream));
+}
+
+moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
+                           const int32_t* q_start, const int32_t* kv_start, int64_t T, int64_t Tk,
+                           const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           int64_t k_stride, const uint16_t* v, int64_t v_stride, float scale,
+                           uint16_t* out, int64_t out_stride, hipStream_t stream) {
+  const char* W = "moe_attn_prompt";
+  moe_status st = check_head(D, W);
+  if (st != MOE_OK) return st;
+  if (n_seq < 0 || n_seq > 65535)
+    return fail(n_seq < 0 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED,
+                "%s: n_seq=%d must be in 0..65535", W, n_seq);
+  if ((st = check_heads(n_q, n_kv, T, n_seq, W)) != MOE_OK) return st;
+  if ((st = check_scale(scale, W)) != MOE_OK) return st;
+  if (Tk < 0) return fail(MOE_ERR_INVALID_ARG, "%s: Tk=%lld < 0", W, (long long)Tk);
+  if (!kv_start && Tk < T)
+    return fail(MOE_ERR_INVALID_ARG, "%s: Tk=%lld < T=%lld without kv_start", W, (long long)Tk,
+                (long long)T);
+  if (T == 0 || n_seq == 0) return MOE_OK;
+  CHECK_PTR(q_start, W);
+  const int64_t qw = (int64_t)n_q * D, kw = (int64_t)n_kv * D;
+  if ((st = check_rows(q, q_stride, qw, "q", W)) != MOE_OK) return st;
+  if ((st = check_rows(out, out_stride, qw, "out", W)) != MOE_OK) return st;
+  if (Tk > 0) {
+    if ((st = check_rows(k, k_stride, kw, "k", W)) != MOE_OK) return st;
+    if ((st = check_rows(v, v_stride, kw, "v", W)) != MOE_OK) return st;
+  }
+  return hip_status(W, moe::launch_attn_prompt(n_q, n_kv, D, n_seq, q_start, kv_start, T, Tk, q,
+                                               q_stride, k, k_stride, v, v_stride, scale, out,
+                                               out_stride, stream));
 }
 
 }  // extern "C"

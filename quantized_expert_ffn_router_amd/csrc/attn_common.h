@@ -1,0 +1,80 @@
+// attn_common.h -- pieces shared by the key/value cache and attention kernels.
+//
+// The pages' engine keeps a key/value cache per request slot and trades its
+// precision against the experts' memory (aiopssre.com, "Concurrency divides
+// context unless you pay for more cache").  The cache layout is chosen for the
+// reader: one (page, head) block is contiguous, keys are rows of D values (a
+// lane of the score product takes a quarter of one token's row), values are
+// laid out in quads of tokens (a lane of the output product takes D/16 elements
+// of four tokens), so every fragment of a 16-token step is one vector load.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+// Byte offsets inside one (page, head) block; head = bytes of the block.
+struct KvLayout {
+  uint32_t ks, vq, vs, head;
+};
+
+__host__ __device__ constexpr KvLayout kv_layout(int fmt, int D, int P) {
+  const uint32_t codes = fmt == MOE_FMT_NVFP4 ? (uint32_t)(P * D / 2)
+                         : fmt == MOE_FMT_Q8_0 ? (uint32_t)(P * D)
+                                               : (uint32_t)(2 * P * D);
+  const uint32_t scales = fmt == MOE_FMT_BF16 ? 0u : (uint32_t)(P * D / 16);
+  return KvLayout{codes, codes + scales, 2 * codes + scales, 2 * (codes + scales)};
+}
+
+// A step's sequences as the kernels take them (device pointers).
+struct SeqView {
+  const int32_t* row_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int n_seq, max_pages, n_pages, log2P;
+};
+
+// Sequence of packed row t: the number of sequences that end at or before it.
+// Every lane of the wave takes part and gets the same answer; n_seq when the
+// row lies behind the last sequence.  Up to 64 sequences cost one load.
+__device__ __forceinline__ int find_seq(const int32_t* __restrict__ start, int n_seq, int64_t t) {
+  int b = 0;
+  for (int i0 = 0; i0 < n_seq; i0 += 64) {
+    const int i = i0 + lane_id();
+    const bool before = i < n_seq && (int64_t)start[i + 1] <= t;
+    b += __popcll(__ballot(before));
+  }
+  return b;
+}
+
+// Page of token j of sequence b, or -1 when the table or the pool has none.
+__device__ __forceinline__ int page_of(const SeqView& s, int b, int64_t j) {
+  const int64_t n = j >> s.log2P;
+  if (j < 0 || n >= s.max_pages) return -1;
+  const int p = s.page_table[(int64_t)b * s.max_pages + n];
+  return (unsigned)p < (unsigned)s.n_pages ? p : -1;
+}
+
+}  // namespace moe
+
+namespace moe {
+
+hipError_t launch_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const moe_seq_batch* s,
+                            const uint16_t* qkv, int64_t qkv_stride, int64_t T, const int32_t* pos,
+                            uint16_t* q_out, int64_t q_stride, uint16_t* k_out, int64_t k_stride,
+                            hipStream_t stream);
+hipError_t launch_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int32_t* first,
+                          const int32_t* out_start, int64_t R, uint16_t* k_out, int64_t k_stride,
+                          uint16_t* v_out, int64_t v_stride, hipStream_t stream);
+size_t attn_decode_ws_bytes(int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len);
+hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int n_q,
+                              const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
+                              float scale, uint16_t* out, int64_t out_stride, void* ws,
+                              hipStream_t stream);
+hipError_t launch_attn_prompt(int n_q, int n_kv, int D, int n_seq, const int32_t* q_start,
+                              const int32_t* kv_start, int64_t T, int64_t Tk, const uint16_t* q,
+                              int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                              const uint16_t* v, int64_t v_stride, float scale, uint16_t* out,
+                              int64_t out_stride, hipStream_t stream);
+
+}  // namespace moe
