@@ -537,7 +537,8 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
  * rounding and empty rows as moe_attn_decode, with bf16 operands.
  * q_start, kv_start: device int32 [n_seq + 1], ascending; kv_start NULL: the
  * queries' own.  q: bf16 [T] rows of n_q * D; k, v: bf16 [Tk] rows of n_kv * D;
- * out: bf16 [T] rows of n_q * D (may be q, with the same stride).  Rows outside
+ * out: bf16 [T] rows of n_q * D (may be q, with the same stride).  k_stride and
+ * v_stride: at most 2^24.  Rows outside
  * the sequences are left as they are; indices are held inside T and Tk. */
 moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
                            const int32_t* q_start, const int32_t* kv_start, int64_t T, int64_t Tk,

@@ -792,6 +792,9 @@ moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
   if (Tk > 0) {
     if ((st = check_rows(k, k_stride, kw, "k", W)) != MOE_OK) return st;
     if ((st = check_rows(v, v_stride, kw, "v", W)) != MOE_OK) return st;
+    // a tile of 64 rows is read with 32-bit byte offsets
+    if (k_stride > (1 << 24) || v_stride > (1 << 24))
+      return fail(MOE_ERR_UNSUPPORTED, "%s: k and v strides are at most 2^24 elements", W);
   }
   return hip_status(W, moe::launch_attn_prompt(n_q, n_kv, D, n_seq, q_start, kv_start, T, Tk, q,
                                                q_stride, k, k_stride, v, v_stride, scale, out,

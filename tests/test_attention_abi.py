@@ -112,7 +112,7 @@ def test_read_decode_and_prompt_refusals():
             (prompt, dict(n_kv=0), BAD, "n_kv=0"), (prompt, dict(n_q=12, n_kv=5), BAD, "n_q=12"), (prompt, dict(scale=-1.0), BAD, "scale"),
             (prompt, dict(Tk=-1), BAD, "Tk=-1"), (prompt, dict(Tk=3), BAD, "without kv_start"), (prompt, dict(qs=None), BAD, "q_start"),
             (prompt, dict(x=None), BAD, "q is NULL"), (prompt, dict(k=None), BAD, "k is NULL"), (prompt, dict(vst=250), BAD, "v stride"),
-            (prompt, dict(out=A + 4), BAD, "out is not"), (prompt, dict(T=1 << 24), UNSUP, "too large")]:
+            (prompt, dict(out=A + 4), BAD, "out is not"), (prompt, dict(kst=(1 << 24) + 8), UNSUP, "strides"), (prompt, dict(T=1 << 24), UNSUP, "too large")]:
         assert call(**kw) == status, (call.__name__, kw, q.last_error())
         assert msg in q.last_error(), (call.__name__, kw, q.last_error())
     c, p, s = cache(), qkv(), seqs()

@@ -440,6 +440,22 @@ def test_prompt_unseen_tokens_have_no_influence(D, val):
             assert np.isnan(ref.bf16_val(got[70])).any() or val == math.inf
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prompt_scores_far_above_the_first_keys(D):
+    """The first tile's keys are small and later ones large: weights relative to
+    the first tile's maximum leave every range, and the rows have to be done
+    again with a running maximum; also keys that only get smaller."""
+    rng = np.random.default_rng(D)
+    for first, rest in ((0.01, 40.0), (0.01, 6.0), (20.0, 0.01)):
+        mag = np.where(np.arange(190) < 64, first, rest)[:, None]
+        qv = ref.bf16_bits(rng.standard_normal((190, 2 * D)))
+        kv = ref.bf16_bits(rng.standard_normal((190, D)) * mag)
+        vv = ref.bf16_bits(rng.standard_normal((190, D)))
+        print("prompt far", D, first, rest, flush=True)
+        got = run_prompt(2, 1, D, [0, 190], None, 190, 190, qv, kv, vv)
+        check_prompt(2, 1, D, [0, 190], None, qv, kv, vv, got, [0, 63, 64, 65, 100, 127, 128, 189])
+
+
 def test_prompt_bad_ranges_give_nan():
     """Keys that reach past Tk are not read: their sequence is NaN."""
     rng = np.random.default_rng(3)
