@@ -738,7 +738,7 @@ size_t moe_attn_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_se
   }
   // max_len 0 stands for the page table's capacity, which is not known here:
   // the longest cache gives the largest split
-  return moe::attn_decode_ws_bytes(c->n_kv, c->D, n_q, n_seq, T, max_len ? max_len : INT32_MAX);
+  return moe::attn_decode_ws_bytes(c->fmt, c->n_kv, c->D, n_q, n_seq, T, max_len ? max_len : INT32_MAX);
 }
 
 moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_t n_q,
@@ -757,7 +757,7 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
   if ((st = check_rows(q, q_stride, qw, "q", W)) != MOE_OK) return st;
   if ((st = check_rows(out, out_stride, qw, "out", W)) != MOE_OK) return st;
   if (max_len == 0) max_len = (int64_t)s->max_pages * c->page_tokens;
-  const size_t need = moe::attn_decode_ws_bytes(c->n_kv, c->D, n_q, s->n_seq, T, max_len);
+  const size_t need = moe::attn_decode_ws_bytes(c->fmt, c->n_kv, c->D, n_q, s->n_seq, T, max_len);
   if (need > 0) {
     CHECK_PTR(ws, W);
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu", W, ws_bytes, need);

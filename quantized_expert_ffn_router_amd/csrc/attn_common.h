@@ -34,17 +34,28 @@ struct SeqView {
   int n_seq, max_pages, n_pages, log2P;
 };
 
-// Sequence of packed row t: the number of sequences that end at or before it.
-// Every lane of the wave takes part and gets the same answer; n_seq when the
-// row lies behind the last sequence.  Up to 64 sequences cost one load.
-__device__ __forceinline__ int find_seq(const int32_t* __restrict__ start, int n_seq, int64_t t) {
-  int b = 0;
-  for (int i0 = 0; i0 < n_seq; i0 += 64) {
-    const int i = i0 + lane_id();
-    const bool before = i < n_seq && (int64_t)start[i + 1] <= t;
-    b += __popcll(__ballot(before));
+// Sequence of packed row t, with its first row, row count and length; b = -1
+// when the row belongs to none.  Every lane of the wave takes part and gets the
+// same answer.  Up to 64 sequences cost one round of loads.
+struct RowSeq {
+  int b, r0, len;
+  int64_t rows;
+};
+__device__ __forceinline__ RowSeq find_row(const SeqView& s, int64_t t) {
+  RowSeq r{-1, 0, 0, 0};
+  for (int i0 = 0; i0 < s.n_seq; i0 += 64) {
+    const int i = min(i0 + lane_id(), s.n_seq - 1);
+    const int start = s.row_start[i], end = s.row_start[i + 1], len = s.kv_len[i];
+    const uint64_t behind = __ballot(i0 + lane_id() < s.n_seq && (int64_t)end > t);
+    if (!behind) continue;
+    const int l = __ffsll((unsigned long long)behind) - 1;
+    r.r0 = __builtin_amdgcn_readlane(start, l);
+    r.rows = (int64_t)__builtin_amdgcn_readlane(end, l) - r.r0;
+    r.len = __builtin_amdgcn_readlane(len, l);
+    if (r.r0 <= t) r.b = i0 + l;
+    break;
   }
-  return b;
+  return r;
 }
 
 // Page of token j of sequence b, or -1 when the table or the pool has none.
@@ -66,7 +77,7 @@ hipError_t launch_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const 
 hipError_t launch_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int32_t* first,
                           const int32_t* out_start, int64_t R, uint16_t* k_out, int64_t k_stride,
                           uint16_t* v_out, int64_t v_stride, hipStream_t stream);
-size_t attn_decode_ws_bytes(int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len);
+size_t attn_decode_ws_bytes(int fmt, int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len);
 hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int n_q,
                               const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
                               float scale, uint16_t* out, int64_t out_stride, void* ws,

@@ -27,6 +27,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
+constexpr int kStreamed = 2;         // cache policy of loads that are read once
 constexpr float kNone = -3.0e38f;   // running maximum before any token
 constexpr float kGrow = 8.0f;       // log2 headroom before the accumulators are rescaled
 
@@ -42,22 +43,22 @@ struct DecodeArgs {
   float scale_log2, v_ts;
 };
 
-// What one tile of 16 query rows (row r = i * G + g: packed row i, head g of
+// What one tile of `size` query rows (row r = i * G + g: packed row i, head g of
 // the group) of a sequence sees, and how its 32-token units are split.
 struct TilePlan {
   int64_t hi;  // last token that any row of the tile sees (-1: none)
   int64_t lo;  // last token that all of them see
-  int units, per_split, n_split;
+  int units, per_split;
 };
-__device__ __forceinline__ TilePlan tile_plan(int64_t len, int64_t rows, int G, int64_t tile, int S) {
+__device__ __forceinline__ TilePlan tile_plan(int len, int rows, int inside, int G, int tile,
+                                              int size, int S) {
   TilePlan p;
-  const int64_t last = min((tile * 16 + 15) / G, rows - 1);
-  p.hi = max(len - rows + last, (int64_t)-1);
-  p.lo = len - rows + (tile * 16) / G;
+  const int last = min((int)((uint32_t)(tile * size + size - 1) / (uint32_t)G), inside - 1);
+  p.hi = max((int64_t)len - rows + last, (int64_t)-1);
+  p.lo = (int64_t)len - rows + (int)((uint32_t)(tile * size) / (uint32_t)G);
   p.units = (int)((p.hi + 32) >> 5);
-  const int even = (p.units + S - 1) / S;
+  const int even = (int)((uint32_t)(p.units + S - 1) / (uint32_t)S);
   p.per_split = max((even + kWaves - 1) / kWaves * kWaves, kWaves);
-  p.n_split = (p.units + p.per_split - 1) / p.per_split;
   return p;
 }
 
@@ -97,75 +98,130 @@ __device__ __forceinline__ float groups_sum(float v) {
   return v + __shfl_xor(v, 16);
 }
 
-// The cache bytes of one lane for a unit of 32 tokens (two tiles of 16): a
-// quarter of one token's key per tile, D/16 elements of four tokens' values.
+// The cache bytes of one lane for a unit of 32 tokens (two tiles of 16): of one
+// token's key per tile, D/4 elements, and of four tokens' values, D/16 elements
+// each.  A lane's bytes come in chunks of one load (16 bytes; 8 for 64 elements
+// of 4 bits), spread so that a load of the wave covers whole pieces of 64 bytes
+// and more: chunk i of group g of a key starts at byte 64 i + 16 g of its row,
+// chunk i of lane n of a value quad at byte 256 i + 16 n.  Which elements those
+// are does not matter to the products, as long as the query row is cut the same
+// way and the output is put back.
 template <int FMT, int D>
 struct Unit {
   static constexpr int W = FMT == MOE_FMT_NVFP4 ? D / 32 : FMT == MOE_FMT_Q8_0 ? D / 16 : D / 8;
+  static constexpr int CW = W < 4 ? W : 4;   // words of a chunk
+  static constexpr int NC = W / CW;          // chunks of a lane and tile
+  static constexpr int EK = D / 4 / NC;      // key elements of a chunk
+  // value elements of a chunk (NVFP4: all of a lane's, for one or two tokens)
+  static constexpr int JC = FMT == MOE_FMT_NVFP4 ? D / 16 : D / 16 / NC;
+  static constexpr int NS = FMT == MOE_FMT_BF16 ? 1 : FMT == MOE_FMT_Q8_0 ? NC : 1;
   uint32_t k[2][W], v[2][W];
-  uint32_t ks[2];     // NVFP4: D/64 E4M3 bytes; Q8_0: D/128 (at least one) fp16
-  uint32_t vs[2][2];  // scales of the 4 tokens: E4M3 bytes in [0], or 4 fp16
+  uint32_t ks[2][NC];      // scales of a key chunk: one or two E4M3 bytes, or an fp16
+  uint32_t vs[2][NS][2];   // of the 4 tokens: E4M3 bytes in [0], or 4 fp16 for each chunk
 
-  __device__ __forceinline__ static void words(uint32_t* d, const uint8_t* p) {
-    if constexpr (W == 2) {
-      typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-      const v2u x = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(p));
-      d[0] = x.x; d[1] = x.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < W / 4; ++i) {
-        const v4u x = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p) + i);
-        d[4 * i] = x.x; d[4 * i + 1] = x.y; d[4 * i + 2] = x.z; d[4 * i + 3] = x.w;
-      }
-    }
+  // First key element of step s (8 elements) of group g.
+  __device__ __forceinline__ static int key_dim(int s, int g) {
+    return (s * 8 / EK) * (4 * EK) + g * EK + s * 8 % EK;
   }
+  // Element of value fragment j in row m of its product.
+  __device__ __forceinline__ static int value_dim(int m, int j) {
+    return (j / JC) * (16 * JC) + m * JC + j % JC;
+  }
+
+  // Byte offsets of a lane inside the sections of a 16-token tile.
+  struct Lane {
+    uint32_t k, v, ks, vs;
+    __device__ __forceinline__ Lane(int n, int g, int P) {
+      k = n * (16 * W) + g * (4 * CW);
+      v = FMT == MOE_FMT_NVFP4 ? (g * 16 + n) * (4 * W) : g * (64 * W) + n * 16;
+      ks = FMT == MOE_FMT_NVFP4 ? n * (D / 16) + g * (EK / 16) : 2 * (n * (D / 32) + g / 2);
+      vs = FMT == MOE_FMT_NVFP4 ? (n * D / 256) * P + 4 * g : 2 * (n / 8 * P + 4 * g);
+    }
+  };
 
   // blk: the (page, head) block; o: the unit's first token within the page.
-  __device__ __forceinline__ void load(const uint8_t* blk, const KvLayout lay, int P, int o, int n,
-                                       int g) {
+  // Both are the same for the whole wave: a descriptor of the block and scalar
+  // offsets of the sections, so that a lane's own offsets never change.  Keys and
+  // values take 16 W bytes a token; they are not kept in the caches (read once).
+  // bytes: readable bytes of the block; with 0 the loads come back at once, as
+  // zeros.
+  template <typename R>
+  __device__ __forceinline__ static void words(R rsrc, uint32_t* d, uint32_t lane, uint32_t base) {
+#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass does not know the builtins)
+    if constexpr (CW == 2) {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, lane, base, kStreamed);
+      d[0] = x[0]; d[1] = x[1];
+    } else {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, base, kStreamed);
+      d[0] = x[0]; d[1] = x[1]; d[2] = x[2]; d[3] = x[3];
+    }
+#endif
+  }
+  __device__ __forceinline__ void load_keys(const uint8_t* blk, const KvLayout lay, int bytes, int o, const Lane& at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(blk), 0, bytes, 0x00020000);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int tok = o + 16 * t + n, quad = ((o + 16 * t) >> 2) + g;
-      words(k[t], blk + (tok * 4 + g) * (4 * W));
-      words(v[t], blk + lay.vq + (quad * 16 + n) * (4 * W));
-      if constexpr (FMT == MOE_FMT_NVFP4) {
-        const uint8_t* s = blk + lay.ks + tok * (D / 16) + g * (D / 64);
-        if constexpr (D == 64) ks[t] = *s;
-        if constexpr (D == 128) ks[t] = *reinterpret_cast<const uint16_t*>(s);
-        if constexpr (D == 256) ks[t] = *reinterpret_cast<const uint32_t*>(s);
-        vs[t][0] = *reinterpret_cast<const uint32_t*>(blk + lay.vs + (n * D / 256) * P + o + 16 * t + 4 * g);
-      } else if constexpr (FMT == MOE_FMT_Q8_0) {
-        const uint8_t* s = blk + lay.ks + 2 * (tok * (D / 32) + g * D / 128);
-        if constexpr (D == 256) ks[t] = *reinterpret_cast<const uint32_t*>(s);
-        else ks[t] = *reinterpret_cast<const uint16_t*>(s);
-        const uint2 x = *reinterpret_cast<const uint2*>(blk + lay.vs + 2 * ((n * D / 512) * P + o + 16 * t + 4 * g));
-        vs[t][0] = x.x; vs[t][1] = x.y;
+      const uint32_t tok = o + 16 * t;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        words(rsrc, k[t] + i * CW, at.k + 64 * i, tok * (16 * W));
+        if constexpr (FMT == MOE_FMT_NVFP4) {
+          const uint32_t s = lay.ks + tok * (D / 16);
+          if constexpr (EK == 16) ks[t][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rsrc, at.ks + 8 * i, s, 0);
+          else ks[t][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, at.ks + 8 * i, s, 0);
+        } else if constexpr (FMT == MOE_FMT_Q8_0) {
+          ks[t][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, at.ks + 4 * i, lay.ks + 2 * tok * (D / 32), 0);
+        }
       }
     }
+#endif
+  }
+  __device__ __forceinline__ void load_values(const uint8_t* blk, const KvLayout lay, int bytes, int P, int o, const Lane& at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(blk), 0, bytes, 0x00020000);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t tok = o + 16 * t;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        words(rsrc, v[t] + i * CW, at.v + (FMT == MOE_FMT_NVFP4 ? 16 : 256) * i, lay.vq + tok * (16 * W));
+      if constexpr (FMT == MOE_FMT_NVFP4) {
+        vs[t][0][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at.vs, lay.vs + tok, 0);
+      } else if constexpr (FMT == MOE_FMT_Q8_0) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const auto x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, at.vs, lay.vs + 2 * (tok + 2 * i * P), 0);
+          vs[t][i][0] = x[0]; vs[t][i][1] = x[1];
+        }
+      }
+    }
+#endif
   }
 
-  // Key fragment s (elements g * D/4 + 8 s ..) of tile t, as 4 words.
+  // Key fragment s (8 elements of the lane's) of tile t, as 4 words.
   __device__ __forceinline__ v4u key(int t, int s) const {
     v4u r;
+    const int i = s * 8 / EK;
     if constexpr (FMT == MOE_FMT_NVFP4) {
-      const v2h sp = fp8_pair(ks[t], s >> 2);
-      const v2h sc = (s >> 1) & 1 ? v2h{sp.y, sp.y} : v2h{sp.x, sp.x};
+      const v2h sp = fp8_pair(ks[t][i], 0);
+      const v2h sc = (s * 8 % EK) / 16 ? v2h{sp.y, sp.y} : v2h{sp.x, sp.x};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = bits(fp4_pair(k[t][s], i) * sc);
+      for (int q = 0; q < 4; ++q) r[q] = bits(fp4_pair(k[t][s], q) * sc);
     } else if constexpr (FMT == MOE_FMT_Q8_0) {
-      const v2h sp = halves(ks[t]);
-      const v2h sc = s >> 2 ? v2h{sp.y, sp.y} : v2h{sp.x, sp.x};
+      const v2h sp = halves(ks[t][i]);
+      const v2h sc = {sp.x, sp.x};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = bits(i8_pair(k[t][2 * s + (i >> 1)] ^ 0x80808080u, i & 1) * sc);
+      for (int q = 0; q < 4; ++q) r[q] = bits(i8_pair(k[t][2 * s + (q >> 1)] ^ 0x80808080u, q & 1) * sc);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = k[t][4 * s + i];
+      for (int q = 0; q < 4; ++q) r[q] = k[t][4 * s + q];
     }
     return r;
   }
 
-  // Value fragment of element n * D/16 + j: tokens 4g.. of tile 0, then of
-  // tile 1 (the order of the score accumulators).
+  // Value fragment j: tokens 4g.. of tile 0, then of tile 1 (the order of the
+  // score accumulators).
   __device__ __forceinline__ v4u value(int j) const {
     v4u r;
 #pragma unroll
@@ -183,9 +239,9 @@ struct Unit {
           // nibbles, odd ones from the high nibbles
           const uint32_t w = j & 1 ? ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u)
                                    : (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
-          r[2 * t + h] = bits(fp4_pair(w, (j & 7) >> 1) * fp8_pair(vs[t][0], h));
+          r[2 * t + h] = bits(fp4_pair(w, (j & 7) >> 1) * fp8_pair(vs[t][0][0], h));
         } else if constexpr (FMT == MOE_FMT_Q8_0) {
-          r[2 * t + h] = bits(i8_pair(v[t][j] ^ 0x80808080u, h) * halves(vs[t][h]));
+          r[2 * t + h] = bits(i8_pair(v[t][j] ^ 0x80808080u, h) * halves(vs[t][j / JC][h]));
         } else {
           r[2 * t + h] = v[t][2 * j + h];
         }
@@ -194,25 +250,35 @@ struct Unit {
     return r;
   }
 
-  // Zeroes the values of this lane's tokens from the `left`-th of the unit on
-  // (left: tokens of the unit that some row sees), whatever they hold.
+  // Zeroes the values of this lane's tokens from the `left`-th of the unit on,
+  // whatever they hold.
   __device__ __forceinline__ void cut(int left, int g) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int n = min(max(left - 16 * t - 4 * g, 0), 4);
+      const uint32_t m0 = n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
+      const uint32_t m1 = n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
       if constexpr (FMT == MOE_FMT_NVFP4) {
-        vs[t][0] = n >= 4 ? vs[t][0] : vs[t][0] & ((1u << (8 * n)) - 1u);
-      } else {
-        const uint32_t m0 = n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
-        const uint32_t m1 = n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
-        if constexpr (FMT == MOE_FMT_Q8_0) {
-          vs[t][0] &= m0; vs[t][1] &= m1;
-        } else {
+        vs[t][0][0] = n >= 4 ? vs[t][0][0] : vs[t][0][0] & ((1u << (8 * n)) - 1u);
+      } else if constexpr (FMT == MOE_FMT_Q8_0) {
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) { v[t][2 * j] &= m0; v[t][2 * j + 1] &= m1; }
-        }
+        for (int i = 0; i < NC; ++i) { vs[t][i][0] &= m0; vs[t][i][1] &= m1; }
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) { v[t][2 * j] &= m0; v[t][2 * j + 1] &= m1; }
       }
     }
+  }
+
+  // Keeps what is decoded from the value bytes from being computed ahead of a
+  // rare loop, where it would take registers all along.
+  __device__ __forceinline__ void pin() {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < W; ++i) asm("" : "+v"(v[t][i]));
+#endif
   }
 
   // Whether any of this lane's values is infinite or NaN (in the block
@@ -223,11 +289,13 @@ struct Unit {
     for (int t = 0; t < 2; ++t) {
       if constexpr (FMT == MOE_FMT_NVFP4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) any |= ((vs[t][0] >> (8 * i)) & 0x7fu) == 0x7fu;
+        for (int i = 0; i < 4; ++i) any |= ((vs[t][0][0] >> (8 * i)) & 0x7fu) == 0x7fu;
       } else if constexpr (FMT == MOE_FMT_Q8_0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          any |= ((vs[t][i >> 1] >> (16 * (i & 1))) & 0x7c00u) == 0x7c00u;
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            any |= (vs[t][c][i] & 0x7c00u) == 0x7c00u || (vs[t][c][i] & 0x7c000000u) == 0x7c000000u;
       } else {
 #pragma unroll
         for (int j = 0; j < W; ++j)
@@ -249,254 +317,434 @@ __device__ __forceinline__ v4f mma(v4u a, v4u b, v4f c) {
 }
 
 // Two softmax weights as a pair of the product's operand type, rounded to
-// nearest even: at most half a step of weights between 0 and 2^kGrow.
+// nearest even (half a step of weights between 0 and 2^kGrow), and their sum
+// added to l: of the rounded weights, so that rounding does not shift the mean.
 template <int FMT>
-__device__ __forceinline__ uint32_t weight_pair(float a, float b) {
+__device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
   if constexpr (FMT == MOE_FMT_BF16) {
     typedef __bf16 v2b __attribute__((ext_vector_type(2)));
-    const v2b r = {(__bf16)a, (__bf16)b};
+    const v2b r = {(__bf16)a, (__bf16)b}, one = {(__bf16)1.0f, (__bf16)1.0f};
+    *l = __builtin_amdgcn_fdot2_f32_bf16(r, one, *l, false);
     return __builtin_bit_cast(uint32_t, r);
   } else {
-    const v2h r = {(_Float16)a, (_Float16)b};
+    const v2h r = {(_Float16)a, (_Float16)b}, one = {(_Float16)1.0f, (_Float16)1.0f};
+    *l = __builtin_amdgcn_fdot2(r, one, *l, false);
     return bits(r);
   }
 }
 
-template <int FMT, int D>
-__global__ __launch_bounds__(64 * kWaves) void k_attn_decode(DecodeArgs a) {
+// What a wave carries for one tile of NT * 16 query rows (a lane column is one
+// row of each 16): running maximum, sum, and the weighted values.
+template <int FMT, int D, int NT>
+struct Carry {
+  static constexpr int KS = D / 32, NJ = D / 16;
+  v4u qf[NT][KS];
+  v4f o[NT][NJ];
+  float m[NT], l[NT], qs[NT];
+  int64_t limit[NT];  // last token the lane's row sees
+
+  __device__ __forceinline__ void scores(const Unit<FMT, D>& c, v4f (&x)[NT][2]) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const v4u k = c.key(t, s);
+#pragma unroll
+        for (int r = 0; r < NT; ++r)
+          x[r][t] = mma<FMT>(k, qf[r][s], s ? x[r][t] : v4f{0.f, 0.f, 0.f, 0.f});
+        __builtin_amdgcn_sched_barrier(0);  // one fragment decoded at a time
+      }
+    }
+  }
+  __device__ __forceinline__ void weights(v4f (&x)[NT][2], v4u (&p)[NT]) {
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      float mx = fmaxf(fmaxf(x[r][0][0], x[r][0][1]), fmaxf(x[r][0][2], x[r][0][3]));
+      mx = fmaxf(mx, fmaxf(fmaxf(x[r][1][0], x[r][1][1]), fmaxf(x[r][1][2], x[r][1][3])));
+      mx = groups_max(mx) * qs[r];
+      if (__any(mx > m[r] + kGrow)) {
+        const float mn = fmaxf(m[r], mx), al = __builtin_amdgcn_exp2f(m[r] - mn);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[r][j][i] *= al;
+        l[r] *= al;
+        m[r] = mn;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[r][t][i] = __builtin_amdgcn_exp2f(fmaf(x[r][t][i], qs[r], -m[r]));
+        }
+        p[r][2 * t] = weight_pair<FMT>(x[r][t][0], x[r][t][1], &l[r]);
+        p[r][2 * t + 1] = weight_pair<FMT>(x[r][t][2], x[r][t][3], &l[r]);
+      }
+    }
+  }
+  __device__ __forceinline__ void gather(const Unit<FMT, D>& c, const v4u (&p)[NT]) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const v4u v = c.value(j);
+#pragma unroll
+      for (int r = 0; r < NT; ++r) o[r][j] = mma<FMT>(v, p[r], o[r][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  __device__ __forceinline__ void mask(v4f (&x)[NT][2], int64_t t0, int g) const {
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      const int seen = (int)min(max(limit[r] - t0, (int64_t)-1), (int64_t)32) - 4 * g;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * t + i > seen) x[r][t][i] = -__builtin_inff();
+    }
+  }
+
+  // One unit of 32 tokens from t0 on.  edge: not every row sees all of it;
+  // left: its tokens that some row sees.  The unit's bytes make room for the next
+  // one's as they are used: next_keys and next_values start those loads.
+  // Returns whether the values are left to wild_values.
+  template <typename FK, typename FV>
+  __device__ __forceinline__ bool unit(Unit<FMT, D>& c, bool edge, int64_t t0, int left, int g,
+                                       FK next_keys, FV next_values) {
+    v4f x[NT][2];
+    v4u p[NT];
+    bool wild = false;
+    scores(c, x);
+    next_keys();
+    __builtin_amdgcn_sched_barrier(0);
+    if (edge) mask(x, t0, g);
+    weights(x, p);
+    if (edge) {
+      c.cut(left, g);
+      wild = __any(c.wild());
+      if (wild) c.cut(0, g);
+    }
+    gather(c, p);
+    next_values();
+    __builtin_amdgcn_sched_barrier(0);
+    return wild;
+  }
+
+  // The weighted values of a unit with infinities or NaN among them that some row
+  // may not see, for rows t, added to out (this lane's row of D sums in LDS).  A
+  // zero weight would not silence them: the rows by what they see, each with the
+  // values behind its last token cut off.
+  __device__ __forceinline__ void wild_values(Unit<FMT, D>& c, int t, int64_t t0, int left, int g,
+                                              float* out) const {
+    v4f x[NT][2];
+    v4u p;
+    scores(c, x);
+    mask(x, t0, g);
+    c.cut(left, g);
+    if (!__any(c.wild())) return;
+    float none = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(fmaf(x[t][h][i], qs[t], -m[t]));
+        const float e1 = __builtin_amdgcn_exp2f(fmaf(x[t][h][i + 1], qs[t], -m[t]));
+        p[2 * h + i / 2] = weight_pair<FMT>(e0, e1, &none);
+      }
+#pragma unroll 1
+    for (int k = 0; k < 32; ++k) {
+      const bool mine = min(limit[t] - t0, (int64_t)31) == k;
+      if (!__any(mine)) continue;
+      Unit<FMT, D> seen = c;
+      seen.pin();
+      seen.cut(k + 1, g);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const v4f add = mma<FMT>(seen.value(j), p, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (mine) out[Unit<FMT, D>::value_dim(4 * g + i, j)] += add[i];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void store_row(uint16_t* d, const float (&v)[N]) {
+  uint32_t w[N < 2 ? 1 : N / 2];
+  if constexpr (N == 1) {
+    *d = f32_to_bf16_rne(v[0]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j)
+    w[j] = (uint32_t)f32_to_bf16_rne(v[2 * j]) | ((uint32_t)f32_to_bf16_rne(v[2 * j + 1]) << 16);
+  if constexpr (N == 2) *reinterpret_cast<uint32_t*>(d) = w[0];
+  if constexpr (N == 4) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+  if constexpr (N >= 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (N == 16) *reinterpret_cast<uint4*>(d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Waves per SIMD that the register use allows: the accumulators (NT * D / 4), the
+// query fragments (half of that) and a unit's bytes.
+constexpr int kDecodeOcc(int fmt, int D, int NT) {
+  const int regs = NT * D / 4 * 3 / 2 + D * (fmt == MOE_FMT_NVFP4 ? 4 : fmt == MOE_FMT_Q8_0 ? 8 : 16) / 32;
+  return regs <= 64 ? 4 : regs <= 80 ? 3 : regs <= 160 ? 2 : 1;
+}
+
+// One workgroup: a tile of NT * 16 query rows of one key/value head, and one
+// split of the sequence's units, which its waves take in turn, the next unit's
+// bytes on their way while one is worked on.
+template <int FMT, int D, int NT>
+__global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_decode(DecodeArgs a) {
   constexpr int KS = D / 32, NJ = D / 16, LD = D + 4;
+  constexpr int E = 16 * D / (64 * kWaves);  // elements of a thread in the join
   __shared__ __align__(16) float o_s[kWaves][16][LD];
   __shared__ float m_s[kWaves][16], l_s[kWaves][16];
-  const int wave = threadIdx.x >> 6, lane = lane_id(), n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   uint32_t id = blockIdx.x;
   const int sp = (int)(id % a.S); id /= a.S;
   const int kvh = (int)(id % a.n_kv); id /= a.n_kv;
   const int zt = (int)(id % a.ztiles);
-  const int b = (int)(id / a.ztiles);
+  const int b = (int)(id / a.ztiles);  // (scalar arithmetic all along)
 
-  const int64_t r0 = a.s.row_start[b], rows = (int64_t)a.s.row_start[b + 1] - r0;
-  const int64_t len = a.s.kv_len[b];
-  if (rows <= 0 || r0 < 0) return;
+  const int r0 = a.s.row_start[b], len = a.s.kv_len[b];
+  const int rows = (int)min((int64_t)a.s.row_start[b + 1] - r0, (int64_t)INT32_MAX);
+  if (r0 < 0 || r0 >= a.T || rows <= 0) return;
+  const int inside = (int)min((int64_t)rows, a.T - r0);  // (inside * G is below 2^31)
   const int P = 1 << a.s.log2P;
   const KvLayout lay = kv_layout(FMT, D, P);
   const size_t page_bytes = (size_t)a.n_kv * lay.head;
   const uint8_t* heads = a.pool + (size_t)kvh * lay.head;
+  const typename Unit<FMT, D>::Lane at(n, g, P);
 
-  for (int64_t tile = zt; tile * 16 < rows * a.G; tile += a.ztiles) {
-    if (r0 + tile * 16 / a.G >= a.T) break;
-    const TilePlan plan = tile_plan(len, rows, a.G, tile, a.S);
+  for (int tile = zt; tile * (16 * NT) < inside * a.G; tile += a.ztiles) {
+    const TilePlan plan = tile_plan(len, rows, inside, a.G, tile, 16 * NT, a.S);
     const int u_begin = sp * plan.per_split, u_end = min(plan.units, u_begin + plan.per_split);
-    if (sp > 0 && u_begin >= u_end) continue;  // split 0 also answers rows that see nothing
-
-    // this lane's query row, its last visible token and its fragments
-    const int64_t r = tile * 16 + n;
-    const int64_t row = r0 + r / a.G;
-    const int head = kvh * a.G + (int)(r % a.G);
-    const bool live = r < rows * a.G && row < a.T;
-    const int64_t limit = live ? len - rows + r / a.G : -1;
-    v4u qf[KS];
-    const uint16_t* qp = a.q + (live ? row : r0) * a.q_stride + (size_t)(live ? head : kvh * a.G) * D + g * (D / 4);
-    float qs = a.scale_log2;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const v4u*>(qp + 8 * s);
-    if constexpr (FMT != MOE_FMT_BF16) {
-      // bf16 -> fp16, scaled by the power of two that puts the row's largest
-      // magnitude into [2^14, 2^15): exact for values above 2^-29 of it
-      uint32_t top = 0;
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(qf[s][i] & 0x7fffu, (qf[s][i] >> 16) & 0x7fffu));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-      const int e = min(max(141 - (int)(top >> 7), -113), 126);
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      qs *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const v2h p = {(_Float16)(__uint_as_float(qf[s][i] << 16) * up),
-                         (_Float16)(__uint_as_float(qf[s][i] & 0xffff0000u) * up)};
-          qf[s][i] = bits(p);
-        }
+    if (sp > 0 && u_begin >= u_end) {  // (split 0 also answers rows that see nothing)
+      const int rr = tile * (16 * NT) + threadIdx.x, i = (int)((uint32_t)rr / (uint32_t)a.G);
+      if (threadIdx.x < 16 * NT && rr < inside * a.G)
+        a.part_ml[((int64_t)(r0 + i) * a.n_q + kvh * a.G + rr - i * a.G) * a.S + sp] = make_float2(kNone, 0.0f);
+      continue;
     }
 
-    v4f o[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) o[j] = v4f{0.f, 0.f, 0.f, 0.f};
-    float m = kNone, l = 0.0f;
+    Unit<FMT, D> c;
+    // Entries of the page table, by scalar loads (a wave's units are its own); a
+    // unit past the table's end has none.
+    const int* const row = a.s.page_table + (int64_t)b * a.s.max_pages;
+    const auto page_at = [&](int u) {
+      const int i = (int)(((int64_t)u * 32) >> a.s.log2P);
+      const int p = *(const int __attribute__((address_space(4)))*)(uintptr_t)(row + min(i, a.s.max_pages - 1));
+      return i < a.s.max_pages ? p : -1;
+    };
+    const auto block = [&](int page) {  // page 0 stands in for one that is not there
+      return heads + (size_t)((unsigned)page < (unsigned)a.s.n_pages ? page : 0) * page_bytes;
+    };
+    int u = u_begin + wave, page = 0, next = 0;
+    if (u < u_end) {
+      page = page_at(u);
+      next = page_at(min(u + kWaves, u_end - 1));
+      c.load_keys(block(page), lay, lay.head, (u * 32) & (P - 1), at);
+      c.load_values(block(page), lay, lay.head, P, (u * 32) & (P - 1), at);
+    }
 
-    for (int u = u_begin + wave; u < u_end; u += kWaves) {
-      const int64_t t0 = (int64_t)u * 32;
-      const int page = page_of(a.s, b, t0);
-      if (page < 0) {  // nothing to read: whoever sees a token of it has no answer
-        if (limit >= t0) l = __uint_as_float(0x7fc00000u);
-        continue;
-      }
-      Unit<FMT, D> c;
-      c.load(heads + (size_t)page * page_bytes, lay, P, (int)(t0 & (P - 1)), n, g);
-
-      v4f x[2];
+    // this lane's query rows, their last visible tokens and their fragments
+    Carry<FMT, D, NT> w;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        x[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t) {
+      const int r = (tile * NT + t) * 16 + n, i = (int)((uint32_t)r / (uint32_t)a.G);
+      const int row = r0 + i, head = kvh * a.G + r - i * a.G;
+      const bool live = r < inside * a.G;
+      w.limit[t] = live ? (int64_t)len - rows + i : -1;
+      const uint16_t* qp = a.q + (live ? row : r0) * a.q_stride + (size_t)(live ? head : kvh * a.G) * D;
+      w.qs[t] = a.scale_log2;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) x[t] = mma<FMT>(c.key(t, s), qf[s], x[t]);
-      }
-      const bool edge = t0 + 31 > plan.lo;  // some row does not see all of it
-      float mx = kNone;
+      for (int s = 0; s < KS; ++s) w.qf[t][s] = *reinterpret_cast<const v4u*>(qp + Unit<FMT, D>::key_dim(s, g));
+      if constexpr (FMT != MOE_FMT_BF16) {
+        // bf16 -> fp16, scaled by the power of two that puts the row's largest
+        // magnitude into [2^14, 2^15): exact for values above 2^-29 of it
+        uint32_t top = 0;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[t][i] *= qs;
-          if (edge && t0 + 16 * t + 4 * g + i > limit) x[t][i] = -__builtin_inff();
-          mx = fmaxf(mx, x[t][i]);
-        }
-      mx = groups_max(mx);
-      if (__any(mx > m + kGrow)) {
-        const float mn = fmaxf(m, mx), al = __builtin_amdgcn_exp2f(m - mn);
+          for (int i = 0; i < 4; ++i)
+            top = max(top, max(w.qf[t][s][i] & 0x7fffu, (w.qf[t][s][i] >> 16) & 0x7fffu));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+        const int e = min(max(141 - (int)(top >> 7), -113), 126);
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        w.qs[t] *= __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] *= al;
-        l *= al;
-        m = mn;
-      }
-      v4u p;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[t][i] = __builtin_amdgcn_exp2f(x[t][i] - m);
-          l += x[t][i];
-        }
-        p[2 * t] = weight_pair<FMT>(x[t][0], x[t][1]);
-        p[2 * t + 1] = weight_pair<FMT>(x[t][2], x[t][3]);
-      }
-      if (edge) {
-        const int64_t left = plan.hi + 1 - t0;
-        if (left < 32) c.cut((int)left, g);
-        if (__any(c.wild())) {
-          // A zero weight would not silence an infinity or a NaN: take the
-          // tokens one at a time and add each only to the rows that see it.
-          for (int tk = 0; tk < 32; ++tk) {
-            const bool mine = g == ((tk & 15) >> 2), seen = t0 + tk <= limit;
-            const int w = 2 * (tk >> 4) + ((tk & 3) >> 1);
-            const uint32_t keep = mine ? 0xffffu << (16 * (tk & 1)) : 0u;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              v4u f = c.value(j);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[i] = i == w ? f[i] & keep : 0u;
-              const v4f add = mma<FMT>(f, p, v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[j][i] += seen ? add[i] : 0.0f;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const v2h p = {(_Float16)(__uint_as_float(w.qf[t][s][i] << 16) * up),
+                           (_Float16)(__uint_as_float(w.qf[t][s][i] & 0xffff0000u) * up)};
+            w.qf[t][s][i] = bits(p);
           }
-          continue;
-        }
       }
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) o[j] = mma<FMT>(c.value(j), p, o[j]);
+      for (int j = 0; j < NJ; ++j) w.o[t][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      w.m[t] = kNone;
+      w.l[t] = 0.0f;
     }
-    l = groups_sum(l);
+
+    // The loads of the next unit are not conditional (after a wave's last one they
+    // read nothing): a load that may or may not be there would have to be waited
+    // for with the others.
+    bool wild = false;
+#pragma unroll 1
+    for (; u < u_end; u += kWaves) {
+      const int64_t t0 = (int64_t)u * 32;
+      const bool more = u + kWaves < u_end;
+      const int o = ((u + kWaves) * 32) & (P - 1), bytes = more ? (int)lay.head : 0;
+      const uint8_t* blk = block(next);
+      if ((unsigned)page >= (unsigned)a.s.n_pages) {
+        // nothing to read: rows that see a token of it have no answer
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (w.limit[t] >= t0) w.l[t] = __uint_as_float(0x7fc00000u);
+      }
+      page = next;
+      next = page_at(min(u + 2 * kWaves, u_end - 1));
+      wild |= w.unit(c, t0 + 31 > plan.lo, t0, (int)min(plan.hi + 1 - t0, (int64_t)32), g,
+             [&] { c.load_keys(blk, lay, bytes, o, at); },
+                     [&] { c.load_values(blk, lay, bytes, P, o, at); });
+    }
 
     // join the waves' parts
-    __syncthreads();  // a former tile's parts have been read
-    if (g == 0) { m_s[wave][n] = m; l_s[wave][n] = l; }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float* d = &o_s[wave][n][(4 * g + i) * NJ];
+    for (int t = 0; t < NT; ++t) {
+      const float l = groups_sum(w.l[t]);
+      __syncthreads();  // former parts have been read
+      if (g == 0) { m_s[wave][n] = w.m[t]; l_s[wave][n] = l; }
+      float* const part = o_s[wave][n];
 #pragma unroll
-      for (int j = 0; j < NJ; j += 4)
-        *reinterpret_cast<float4*>(d + j) = make_float4(o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]);
-    }
-    __syncthreads();
-    const int qr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * NJ;
-    const int64_t rr = tile * 16 + qr;
-    const int64_t orow = r0 + rr / a.G;
-    if (rr < rows * a.G && orow < a.T) {
-      float M = kNone, L = 0.0f, acc[NJ];
+      for (int i = 0; i < 4; ++i) {
+        constexpr int JC = Unit<FMT, D>::JC;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, m_s[w][qr]);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[j] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(m_s[w][qr] - M);
-        L += f * l_s[w][qr];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[j] += f * o_s[w][qr][d0 + j];
+        for (int j = 0; j < NJ; j += JC < 4 ? 2 : 4) {
+          float* e = part + Unit<FMT, D>::value_dim(4 * g + i, j);
+          if constexpr (JC < 4)
+            *reinterpret_cast<float2*>(e) = make_float2(w.o[t][j][i], w.o[t][j + 1][i]);
+          else
+            *reinterpret_cast<float4*>(e) =
+                make_float4(w.o[t][j][i], w.o[t][j + 1][i], w.o[t][j + 2][i], w.o[t][j + 3][i]);
+        }
       }
-      const int64_t h = kvh * a.G + rr % a.G;
-      if (plan.n_split <= 1) {
-        const float inv = len - rows + rr / a.G < 0 ? 0.0f : a.v_ts / L;
-        uint32_t w[NJ / 2];
+      if (wild) {
+        for (int v = u_begin + wave; v < u_end; v += kWaves) {
+          const int64_t t0 = (int64_t)v * 32;
+          const int pg = page_at(v);
+          if (t0 + 31 <= plan.lo || (unsigned)pg >= (unsigned)a.s.n_pages) continue;
+          c.load_keys(block(pg), lay, lay.head, (v * 32) & (P - 1), at);
+          c.load_values(block(pg), lay, lay.head, P, (v * 32) & (P - 1), at);
+          w.wild_values(c, t, t0, (int)min(plan.hi + 1 - t0, (int64_t)32), g, part);
+        }
+      }
+      __syncthreads();
+      const int qr = threadIdx.x / (D / E), d0 = (threadIdx.x % (D / E)) * E;
+      float M = kNone, L = 0.0f, acc[E];
 #pragma unroll
-        for (int j = 0; j < NJ / 2; ++j)
-          w[j] = (uint32_t)f32_to_bf16_rne(acc[2 * j] * inv) | ((uint32_t)f32_to_bf16_rne(acc[2 * j + 1] * inv) << 16);
-        uint16_t* d = a.out + orow * a.out_stride + h * D + d0;
-        if constexpr (NJ == 4) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
-        if constexpr (NJ >= 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-        if constexpr (NJ == 16) *reinterpret_cast<uint4*>(d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      for (int i = 0; i < kWaves; ++i) M = fmaxf(M, m_s[i][qr]);
+#pragma unroll
+      for (int j = 0; j < E; ++j) acc[j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        const float f = __builtin_amdgcn_exp2f(m_s[i][qr] - M);
+        L += f * l_s[i][qr];
+#pragma unroll
+        for (int j = 0; j < E; ++j) acc[j] += f * o_s[i][qr][d0 + j];
+      }
+      const int rr = (tile * NT + t) * 16 + qr, i = (int)((uint32_t)rr / (uint32_t)a.G);
+      const int64_t orow = r0 + i, h = kvh * a.G + rr - i * a.G;
+      if (rr >= inside * a.G) continue;
+      if (a.S == 1) {
+        const float inv = (int64_t)len - rows + i < 0 ? 0.0f : a.v_ts / L;
+#pragma unroll
+        for (int j = 0; j < E; ++j) acc[j] *= inv;
+        store_row<E>(a.out + orow * a.out_stride + h * D + d0, acc);
       } else {
         const int64_t at = (orow * a.n_q + h) * a.S + sp;
         if (d0 == 0) a.part_ml[at] = make_float2(M, L);
         float* d = a.part_o + at * D + d0;
 #pragma unroll
-        for (int j = 0; j < NJ; j += 4)
+        for (int j = 0; j < E; j += 4)
           *reinterpret_cast<float4*>(d + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
       }
     }
   }
 }
 
-// Joins the splits of one (row, head): weights exp2(m_s - M), in the order of
-// the splits, so the result does not depend on scheduling.
-template <int D>
+// Joins the splits of EL elements of one (row, head): weights exp2(m_s - M),
+// added in a fixed order, so the result does not depend on scheduling.  EL / 4
+// lanes hold the elements and 1024 / EL groups of them the splits, at most PER
+// each, and a split without units says so itself: all loads are on their way at
+// once, beside the search for the row's sequence.
+constexpr int kMaxSplit = 256;
+
+template <int D, int EL, int PER>
 __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
-  constexpr int LW = D / 4, NG = 256 / LW;  // lanes of a row, splits at a time
-  __shared__ __align__(16) float4 acc_s[NG][LW];
-  __shared__ float l_s[NG];
-  const int64_t t = blockIdx.x / a.n_q;
-  const int h = (int)(blockIdx.x % a.n_q);
-  const int b = find_seq(a.s.row_start, a.s.n_seq, t);
-  if (b >= a.s.n_seq) return;
-  const int64_t r0 = a.s.row_start[b], rows = (int64_t)a.s.row_start[b + 1] - r0;
-  if (t < r0 || r0 < 0) return;
-  const int64_t tile = ((t - r0) * a.G + h % a.G) / 16;
-  const int ns = tile_plan(a.s.kv_len[b], rows, a.G, tile, a.S).n_split;
-  if (ns <= 1) return;
-  const int64_t at = (t * a.n_q + h) * a.S;
-  const int lane = lane_id();
+  constexpr int LW = EL / 4, NG = 256 / LW;
+  __shared__ __align__(16) float4 acc_s[4][LW];
+  __shared__ float l_s[4];
+  const uint32_t id = blockIdx.x / (D / EL);
+  const int x = (int)(blockIdx.x % (D / EL)) * LW + threadIdx.x % LW, grp = threadIdx.x / LW;
+  const int t = (int)(id / (uint32_t)a.n_q), h = (int)(id % (uint32_t)a.n_q);
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int64_t at = ((int64_t)t * a.n_q + h) * a.S;
+  float2 ml[PER];
+  float4 v[PER];
   float M = kNone, L = 0.0f;
-  for (int s = lane; s < ns; s += 64) M = fmaxf(M, a.part_ml[at + s].x);
 #pragma unroll
-  for (int d = 32; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
-  const int grp = threadIdx.x / LW, x = threadIdx.x % LW;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = grp; s < ns; s += NG) {
-    const float2 ml = a.part_ml[at + s];
-    const float f = __builtin_amdgcn_exp2f(ml.x - M);
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (at + s) * D + 4 * x);
-    o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
-    L += f * ml.y;
+  for (int i = 0; i < PER; ++i) {
+    const int s = grp + NG * i;
+    ml[i] = make_float2(kNone, 0.0f);
+    if (s < a.S) {
+      ml[i] = a.part_ml[at + s];
+      v[i] = *reinterpret_cast<const float4*>(a.part_o + (at + s) * D + 4 * x);
+    }
   }
-  acc_s[grp][x] = o;
-  if (x == 0) l_s[grp] = L;
+  const RowSeq q = find_row(a.s, t);
+  if (q.b < 0) return;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) M = fmaxf(M, ml[i].x);
+#pragma unroll
+  for (int d = LW; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
+  if (lane == 0) l_s[wave] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) M = fmaxf(M, l_s[i]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (ml[i].x == kNone && ml[i].y == 0.0f) continue;  // nothing there
+    const float f = __builtin_amdgcn_exp2f(ml[i].x - M);
+    o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
+    L += f * ml[i].y;
+  }
+#pragma unroll
+  for (int d = LW; d < 64; d <<= 1) {
+    o.x += __shfl_xor(o.x, d); o.y += __shfl_xor(o.y, d);
+    o.z += __shfl_xor(o.z, d); o.w += __shfl_xor(o.w, d);
+    L += __shfl_xor(L, d);
+  }
+  __syncthreads();
+  if (lane < LW) acc_s[wave][lane] = o;
+  if (lane == 0) l_s[wave] = L;
   __syncthreads();
   if (threadIdx.x < LW) {
-    o = acc_s[0][x];
+    o = acc_s[0][lane];
     L = l_s[0];
 #pragma unroll
-    for (int i = 1; i < NG; ++i) {
-      const float4 v = acc_s[i][x];
-      o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+    for (int i = 1; i < 4; ++i) {
+      const float4 w = acc_s[i][lane];
+      o.x += w.x; o.y += w.y; o.z += w.z; o.w += w.w;
       L += l_s[i];
     }
-    const float inv = a.s.kv_len[b] - rows + (t - r0) < 0 ? 0.0f : a.v_ts / L;
+    const float inv = (int64_t)q.len - q.rows + (t - q.r0) < 0 ? 0.0f : a.v_ts / L;
     uint16_t* d = a.out + t * a.out_stride + (int64_t)h * D + 4 * x;
     *reinterpret_cast<uint2*>(d) =
         make_uint2((uint32_t)f32_to_bf16_rne(o.x * inv) | ((uint32_t)f32_to_bf16_rne(o.y * inv) << 16),
@@ -504,31 +752,66 @@ __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
   }
 }
 
-struct Split {
-  int S, ztiles;
+// Up to 32 splits a whole head in one workgroup; more, 32 elements in each.
+template <int D>
+void launch_join(const DecodeArgs& a, hipStream_t stream) {
+  const unsigned heads = (unsigned)(a.T * a.n_q);
+  if (a.S <= 32) k_attn_join<D, D, 32 * D / 1024><<<heads, 256, 0, stream>>>(a);
+  else if (a.S <= 64) k_attn_join<D, 32, 2><<<heads * (D / 32), 256, 0, stream>>>(a);
+  else k_attn_join<D, 32, kMaxSplit / 32><<<heads * (D / 32), 256, 0, stream>>>(a);
+}
+
+// Launch shape: query rows of a tile, tiles side by side for a sequence (more
+// are taken in turn), splits of a sequence's cache.
+struct Shape {
+  int tile, ztiles, S;
 };
-// Splits of a sequence's cache: enough workgroups for every CU to hold four
-// (the resident number at this register use), none shorter than one round of
-// the four waves.
-Split split_of(int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) {
+// Split rule, measured on one MI355X with 32 query and 4 key/value heads of 128
+// (us, graph replay, NVFP4 unless said otherwise):
+//   - 16 query rows to a tile, 32 when a sequence has more (the cache is read
+//     once for them: 4 rows of 8 slots at 16 K tokens 30 against 38);
+//   - up to 12 units (384 tokens) no split, so no joining launch: 300 tokens 7.2
+//     against 8.3, but 700 tokens 9.4 against 8.3;
+//   - splits of at least 4 units for each wave (8 slots at 8 K tokens 17.7, at
+//     one unit 20), unless workgroups for 192 CUs need shorter ones (one slot at
+//     700 tokens);
+//   - at most 4 workgroups a CU where the registers allow them (8 slots at 28 K
+//     tokens 32, with 2 a CU 35, with 1 46), 2 for the wider formats, which have
+//     enough bytes on their way with those (Q8_0, 8 x 16 K: 32, with 3 35; bf16
+//     75, with 4 92).
+Shape shape_of(int fmt, int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) {
   const int G = n_q / n_kv;
   const int64_t per_seq = (T + n_seq - 1) / n_seq;
-  Split r;
-  r.ztiles = (int)((per_seq * G + 15) / 16);
-  const int64_t base = (int64_t)n_seq * n_kv * r.ztiles;
-  int64_t S = (1024 + base - 1) / base;
-  const int64_t most = (max_len + 32 * kWaves - 1) / (32 * kWaves);
+  Shape r;
+  r.tile = per_seq * G > 16 && D <= 128 ? 32 : 16;
+  r.ztiles = (int)((per_seq * G + r.tile - 1) / r.tile);
+  const int64_t base = (int64_t)n_seq * n_kv * r.ztiles, units = (max_len + 31) / 32;
+  const int per_cu = fmt == MOE_FMT_NVFP4 && r.tile == 16 && D <= 128 ? 4 : 2;
+  int64_t S = units / (4 * kWaves);
+  if (S < 192 / base) S = 192 / base;
+  if (S > 256 * per_cu / base) S = 256 * per_cu / base;
+  const int64_t most = (units + kWaves - 1) / kWaves;
   if (S > most) S = most;
-  if (S > 256) S = 256;
-  r.S = S < 1 ? 1 : (int)S;
+  if (S > kMaxSplit) S = kMaxSplit;
+  r.S = S < 1 || units <= 3 * kWaves ? 1 : (int)S;
   return r;
+}
+
+template <int FMT>
+void launch_decode(const DecodeArgs& a, int D, int tile, unsigned grid, hipStream_t stream) {
+  constexpr int N = 64 * kWaves;
+  if (D == 64 && tile == 16) k_attn_decode<FMT, 64, 1><<<grid, N, 0, stream>>>(a);
+  else if (D == 64) k_attn_decode<FMT, 64, 2><<<grid, N, 0, stream>>>(a);
+  else if (D == 128 && tile == 16) k_attn_decode<FMT, 128, 1><<<grid, N, 0, stream>>>(a);
+  else if (D == 128) k_attn_decode<FMT, 128, 2><<<grid, N, 0, stream>>>(a);
+  else k_attn_decode<FMT, 256, 1><<<grid, N, 0, stream>>>(a);
 }
 
 }  // namespace
 
-size_t attn_decode_ws_bytes(int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len) {
+size_t attn_decode_ws_bytes(int fmt, int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len) {
   if (n_seq < 1 || T < 1) return 0;
-  const Split sp = split_of(n_kv, n_q, n_seq, T, max_len);
+  const Shape sp = shape_of(fmt, D, n_kv, n_q, n_seq, T, max_len);
   if (sp.S == 1) return 0;
   const size_t n = (size_t)T * n_q * sp.S;
   return align_up(n * D * sizeof(float)) + align_up(n * sizeof(float2));
@@ -538,7 +821,7 @@ hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int
                               const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
                               float scale, uint16_t* out, int64_t out_stride, void* ws,
                               hipStream_t stream) {
-  const Split sp = split_of(c->n_kv, n_q, s->n_seq, T, max_len);
+  const Shape sp = shape_of(c->fmt, c->D, c->n_kv, n_q, s->n_seq, T, max_len);
   int l2 = 0;
   while ((1 << l2) < c->page_tokens) ++l2;
   const bool fp4 = c->fmt == MOE_FMT_NVFP4;
@@ -549,25 +832,17 @@ hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int
                n_q, c->n_kv, n_q / c->n_kv, sp.S, sp.ztiles,
                scale * 1.4426950408889634f * (fp4 ? c->k_scale : 1.0f), fp4 ? c->v_scale : 1.0f};
   const unsigned grid = (unsigned)((int64_t)sp.S * c->n_kv * sp.ztiles * s->n_seq);
-#define MOE_DECODE(FMT)                                                              \
-  switch (c->D) {                                                                    \
-    case 64: k_attn_decode<FMT, 64><<<grid, 64 * kWaves, 0, stream>>>(a); break;     \
-    case 128: k_attn_decode<FMT, 128><<<grid, 64 * kWaves, 0, stream>>>(a); break;   \
-    default: k_attn_decode<FMT, 256><<<grid, 64 * kWaves, 0, stream>>>(a);           \
-  }
   switch (c->fmt) {
-    case MOE_FMT_NVFP4: MOE_DECODE(MOE_FMT_NVFP4) break;
-    case MOE_FMT_Q8_0: MOE_DECODE(MOE_FMT_Q8_0) break;
-    default: MOE_DECODE(MOE_FMT_BF16)
+    case MOE_FMT_NVFP4: launch_decode<MOE_FMT_NVFP4>(a, c->D, sp.tile, grid, stream); break;
+    case MOE_FMT_Q8_0: launch_decode<MOE_FMT_Q8_0>(a, c->D, sp.tile, grid, stream); break;
+    default: launch_decode<MOE_FMT_BF16>(a, c->D, sp.tile, grid, stream);
   }
-#undef MOE_DECODE
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.S == 1) return e;
-  const unsigned heads = (unsigned)(T * n_q);
   switch (c->D) {
-    case 64: k_attn_join<64><<<heads, 256, 0, stream>>>(a); break;
-    case 128: k_attn_join<128><<<heads, 256, 0, stream>>>(a); break;
-    default: k_attn_join<256><<<heads, 256, 0, stream>>>(a);
+    case 64: launch_join<64>(a, stream); break;
+    case 128: launch_join<128>(a, stream); break;
+    default: launch_join<256>(a, stream);
   }
   return hipGetLastError();
 }

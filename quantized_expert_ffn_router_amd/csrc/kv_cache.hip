@@ -152,12 +152,10 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
   const int wave = threadIdx.x >> 6, lane = lane_id();
   const int64_t t = (int64_t)blockIdx.x * kRows + wave;
   if (t >= a.T) return;
-  const int b = find_seq(a.s.row_start, a.s.n_seq, t);
-  if (b >= a.s.n_seq) return;
-  const int64_t r0 = a.s.row_start[b], r1 = a.s.row_start[b + 1];
-  if (t < r0) return;
-  const int64_t tok = (int64_t)a.s.kv_len[b] - (r1 - r0) + (t - r0);
-  const int page = page_of(a.s, b, tok);
+  const RowSeq q = find_row(a.s, t);
+  if (q.b < 0) return;
+  const int64_t tok = (int64_t)q.len - q.rows + (t - q.r0);
+  const int page = page_of(a.s, q.b, tok);
   const int P = 1 << a.s.log2P, o = (int)(tok & (P - 1));
   const KvLayout lay = kv_layout(FMT, D, P);
   uint8_t* page_p = a.pool + (size_t)max(page, 0) * ((size_t)a.n_kv * lay.head);
@@ -217,9 +215,9 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
         xb = make_uint2(bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7]));
       }
       if (live && is_q) {
-        uint16_t* q = a.q_out + t * a.q_stride + (size_t)h * D;
-        *reinterpret_cast<uint2*>(q + a0) = xa;
-        *reinterpret_cast<uint2*>(q + b0) = xb;
+        uint16_t* d = a.q_out + t * a.q_stride + (size_t)h * D;
+        *reinterpret_cast<uint2*>(d + a0) = xa;
+        *reinterpret_cast<uint2*>(d + b0) = xb;
       } else if (live && !is_v && a.k_out) {
         uint16_t* k = a.k_out + t * a.k_stride + (size_t)(h - a.n_q) * D;
         *reinterpret_cast<uint2*>(k + a0) = xa;

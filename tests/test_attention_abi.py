@@ -40,7 +40,7 @@ def read(c=None, s=None, first=None, start=A, R=4, ko=A, ks=256, vo=A, vs=256):
     return q.lib().moe_kv_read(ctypes.byref(c), ctypes.byref(s), first, start, R, ko, ks, vo, vs, None)
 
 
-def decode(c=None, s=None, n_q=8, x=A, xs=1024, T=2, max_len=256, scale=0.1, out=A, os=1024, ws=A,
+def decode(c=None, s=None, n_q=8, x=A, xs=1024, T=2, max_len=8192, scale=0.1, out=A, os=1024, ws=A,
            wb=1 << 30):
     c, s = c or cache(), s or seqs()
     return q.lib().moe_attn_decode(ctypes.byref(c), ctypes.byref(s), n_q, x, xs, T, max_len, scale, out,
