@@ -58,6 +58,46 @@ __device__ __forceinline__ RowSeq find_row(const SeqView& s, int64_t t) {
   return r;
 }
 
+// The unit-th aligned quad of tokens that rows inside 0..T belong to, over all
+// sequences: its sequence (b = -1: there are not so many), the first and last
+// such row of the sequence, and the row of the quad's first token (which may lie
+// before the first row).
+__device__ __forceinline__ RowSeq find_quad(const SeqView& s, int64_t T, int unit, int64_t* first,
+                                            int64_t* last, int64_t* row) {
+  RowSeq r{-1, 0, 0, 0};
+  int before = 0;
+  for (int i0 = 0; i0 < s.n_seq; i0 += 64) {
+    const int i = min(i0 + lane_id(), s.n_seq - 1);
+    const int start = s.row_start[i], end = s.row_start[i + 1], len = s.kv_len[i];
+    const int64_t lo = max(start, 0), hi = min((int64_t)end, T);
+    const int64_t tok = (int64_t)len - ((int64_t)end - start) + (lo - start);
+    int sum = i0 + lane_id() < s.n_seq && hi > lo ? (int)(((tok + hi - lo - 1) >> 2) - (tok >> 2)) + 1 : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(sum, d);
+      if (lane_id() >= d) sum += v;
+    }
+    const uint64_t past = __ballot(before + sum > unit);
+    if (!past) {
+      before += __builtin_amdgcn_readlane(sum, 63);
+      continue;
+    }
+    const int l = __ffsll((unsigned long long)past) - 1;
+    if (l > 0) before += __builtin_amdgcn_readlane(sum, l - 1);
+    r.r0 = __builtin_amdgcn_readlane(start, l);
+    const int e = __builtin_amdgcn_readlane(end, l);
+    r.rows = (int64_t)e - r.r0;
+    r.len = __builtin_amdgcn_readlane(len, l);
+    r.b = i0 + l;
+    *first = max(r.r0, 0);
+    *last = min((int64_t)e, T) - 1;
+    const int64_t t0 = r.len - r.rows + (*first - r.r0);  // token of the first row
+    *row = *first + (((t0 >> 2) + unit - before) << 2) - t0;
+    break;
+  }
+  return r;
+}
+
 // Page of token j of sequence b, or -1 when the table or the pool has none.
 __device__ __forceinline__ int page_of(const SeqView& s, int b, int64_t j) {
   const int64_t n = j >> s.log2P;

@@ -24,9 +24,36 @@ __device__ __forceinline__ void wave_lds_fence() {
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// fp64 -> fp32 -> bf16, each rounded to nearest even.
-__device__ __forceinline__ uint32_t bf16_pair(double a, double b) {
-  return (uint32_t)f32_to_bf16_rne((float)a) | ((uint32_t)f32_to_bf16_rne((float)b) << 16);
+// Two values as bf16, rounded to nearest even.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  const v2b r = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// Sum over groups of N lanes (8, 16 or 32): within a row of 16 by lane
+// permutations of the adder's operand.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int i = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const int lo = (int)u, hi = (int)(u >> 32);
+  const uint32_t l = __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xf, 0xf, true);
+  const uint32_t h = __builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, ((uint64_t)h << 32) | l);
+}
+template <int N, typename T>
+__device__ __forceinline__ T group_sum(T v) {
+  v += dpp<0xb1>(v);   // lane ^ 1
+  v += dpp<0x4e>(v);   // lane ^ 2
+  v += dpp<0x141>(v);  // mirrored in 8: the other four
+  if constexpr (N >= 16) v += dpp<0x140>(v);  // mirrored in 16: the other eight
+  if constexpr (N >= 32) v += __shfl_xor(v, 16);
+  return v;
 }
 
 // The largest magnitude of 8 bf16 values, as bits (so that an infinity or a
@@ -37,6 +64,29 @@ __device__ __forceinline__ uint32_t top_bits(uint4 x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
   return m;
+}
+
+// The 8-bit codes and the scale of 8 values of a block of 32 (4 lanes).
+__device__ __forceinline__ uint2 q8_codes(uint4 x, uint16_t* scale) {
+  uint32_t top = top_bits(x);
+  top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+  top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+  const float v[8] = {lo16(x.x), hi16(x.x), lo16(x.y), hi16(x.y),
+                      lo16(x.z), hi16(x.z), lo16(x.w), hi16(x.w)};
+  const _Float16 d = top >= 0x7f80u
+                         ? __builtin_bit_cast(_Float16, (uint16_t)0x7e00)
+                         : (_Float16)(fminf(__uint_as_float(top << 16), 65024.0f) / 127.0f);
+  const float df = (float)d;
+  uint32_t q[2] = {0, 0};
+  if (df > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = (int)fminf(fmaxf(rintf(v[i] / df), -127.0f), 127.0f);
+      q[i >> 2] |= (uint32_t)(c & 0xff) << (8 * (i & 3));
+    }
+  }
+  *scale = __builtin_bit_cast(uint16_t, d);
+  return make_uint2(q[0], q[1]);
 }
 
 // Quantises 8 values (elements 8n..8n+7 of token o) of a key or value head and
@@ -62,9 +112,23 @@ __device__ __forceinline__ void store_token(uint8_t* __restrict__ blk, const KvL
     }
     return;
   }
+  if constexpr (FMT == MOE_FMT_Q8_0) {
+    uint16_t d;
+    const uint2 q = q8_codes(x, &d);
+    if (!store) return;
+    if (!is_v) {
+      *reinterpret_cast<uint2*>(blk + o * D + 8 * n) = q;
+      if (!(n & 3)) *reinterpret_cast<uint16_t*>(blk + lay.ks + 2 * (o * (D / 32) + (n >> 2))) = d;
+    } else {
+      uint8_t* p = blk + lay.vq + ((o >> 2) * D + 8 * n) * 4 + (o & 3);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[4 * i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+      if (!(n & 3)) *reinterpret_cast<uint16_t*>(blk + lay.vs + 2 * ((n >> 2) * P + o)) = d;
+    }
+    return;
+  }
   uint32_t top = top_bits(x);
   top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-  if constexpr (FMT == MOE_FMT_Q8_0) top = max(top, (uint32_t)__shfl_xor((int)top, 2));
   if (!store) return;
   const float amax = __uint_as_float(top << 16);
   const bool bad = top >= 0x7f80u;
@@ -97,29 +161,29 @@ __device__ __forceinline__ void store_token(uint8_t* __restrict__ blk, const KvL
       }
       if (!(n & 1)) blk[lay.vs + (n >> 1) * P + o] = (uint8_t)sb;
     }
-  } else {
-    const _Float16 d = bad ? __builtin_bit_cast(_Float16, (uint16_t)0x7e00)
-                           : (_Float16)(fminf(amax, 65024.0f) / 127.0f);
-    const float df = (float)d;
-    uint32_t q[2] = {0, 0};
-    if (df > 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (int)fminf(fmaxf(rintf(v[i] / df), -127.0f), 127.0f);
-        q[i >> 2] |= (uint32_t)(c & 0xff) << (8 * (i & 3));
-      }
-    }
-    const uint16_t db = __builtin_bit_cast(uint16_t, d);
-    if (!is_v) {
-      *reinterpret_cast<uint2*>(blk + o * D + 8 * n) = make_uint2(q[0], q[1]);
-      if (!(n & 3)) *reinterpret_cast<uint16_t*>(blk + lay.ks + 2 * (o * (D / 32) + (n >> 2))) = db;
-    } else {
-      uint8_t* p = blk + lay.vq + ((o >> 2) * D + 8 * n) * 4 + (o & 3);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[4 * i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
-      if (!(n & 3)) *reinterpret_cast<uint16_t*>(blk + lay.vs + 2 * ((n >> 2) * P + o)) = db;
-    }
   }
+}
+
+// Sine and cosine of an angle in fp64: reduced by multiples of pi/2 held in two
+// parts (the products are exact inside the fused operations, so positions up to
+// 2^31 lose nothing), then the Taylor series to x^15 and x^16, whose remainders
+// are below 2^-54 for |x| <= pi/4.
+__device__ __forceinline__ void sin_cos(double a, double* s, double* c) {
+  const double n = rint(a * 0.63661977236758134);
+  const double x = fma(-n, 6.123233995736766e-17, fma(-n, 1.5707963267948966, a)), z = x * x;
+  double p = -1.0 / 1307674368000.0, q = 1.0 / 20922789888000.0;
+  p = fma(p, z, 1.0 / 6227020800.0);  q = fma(q, z, -1.0 / 87178291200.0);
+  p = fma(p, z, -1.0 / 39916800.0);   q = fma(q, z, 1.0 / 479001600.0);
+  p = fma(p, z, 1.0 / 362880.0);      q = fma(q, z, -1.0 / 3628800.0);
+  p = fma(p, z, -1.0 / 5040.0);       q = fma(q, z, 1.0 / 40320.0);
+  p = fma(p, z, 1.0 / 120.0);         q = fma(q, z, -1.0 / 720.0);
+  p = fma(p, z, -1.0 / 6.0);          q = fma(q, z, 1.0 / 24.0);
+  p = fma(p * z, x, x);               q = fma(q, z, -0.5);
+  q = fma(q, z, 1.0);
+  const int k = (int)(long long)n & 3;  // quarter turns
+  const double u = k & 1 ? q : p, v = k & 1 ? p : q;
+  *s = k & 2 ? -u : u;
+  *c = (k + 1) & 2 ? -v : v;
 }
 
 struct AppendArgs {
@@ -137,103 +201,233 @@ struct AppendArgs {
   float eps, rope_scale, k_ts, v_ts;
 };
 
-// One wave per row, D/8 lanes per head, 64/(D/8) heads at a time.  The row's
-// angles are taken once, in fp64 (a far position times a frequency needs more
-// than 24 bits), and kept in the wave's LDS.  A lane holds 4 rotation pairs of
-// its head (elements a0.., b0..: both halves of a pair, so no lane needs
-// another's value), norms and rotates them in fp64 -- on this chip as many
-// fp64 as plain fp32 operations run per cycle -- and rounds once.  Keys then go
-// through LDS into 8 consecutive elements a lane, the unit of quantisation.
-template <int FMT, int D>
+// 8 elements of a head: z * w / rms(z), then the rotation of the lane's four
+// pairs: (z[i], z[i + 4]) where the lane holds both halves' elements, neighbours
+// otherwise.  T: float for queries (a few 2^-24, against the 2^-9 of the
+// rounding to bf16), double for keys.
+template <int LPH, int D, typename T>
+__device__ __forceinline__ void norm_turn(T (&z)[8], const float (&w)[8], bool normed, float eps,
+                                          bool halves, bool turn, const T (&cs)[8]) {
+  if (normed) {
+    T ss = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fma(z[i], z[i], ss);
+    ss = group_sum<LPH>(ss);
+    const T r = rsqrt(ss / (T)D + (T)eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = z[i] * r * (T)w[i];
+  }
+  if (turn) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const T zu = halves ? z[i] : z[2 * i], zv = halves ? z[i + 4] : z[2 * i + 1];
+      const T nu = zu * cs[2 * i] - zv * cs[2 * i + 1], nv = zv * cs[2 * i] + zu * cs[2 * i + 1];
+      z[halves ? i : 2 * i] = nu;
+      z[halves ? i + 4 : 2 * i + 1] = nv;
+    }
+  }
+}
+
+// One wave per row, D/8 lanes per head, 64/(D/8) heads at a time: the row's
+// queries, then its keys, then its values, the next group's elements on their way
+// while one is worked on.  The row's angles are taken once, in fp64 (a far
+// position times a frequency needs more than 24 bits), and kept in the wave's
+// LDS.  Queries are normed and rotated in fp32.  Keys are in fp64 (as many fp64
+// as plain fp32 operations run per cycle here), so that the codes in the cache do
+// not hang on the order of a sum: they go through LDS into 8 consecutive elements
+// a lane, the unit of quantisation.
+// HALVES: the rotation pairs elements of the head's two halves (i, i + rot/2).
+//
+// QUADS (the formats that keep four tokens' values side by side): the four waves
+// take the tokens of one aligned quad of a sequence, so that the quad's values
+// are written as whole pieces, put together in LDS; a quad that is not whole in
+// this call is written value by value.  16384 rows (bf16 cache) 97 us without, 72
+// with it.
+template <int FMT, int D, bool HALVES>
 __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
   constexpr int LPH = D / 8, HPW = 64 / LPH;
+  constexpr bool QUADS = FMT != MOE_FMT_NVFP4;
+  constexpr int VB = FMT == MOE_FMT_BF16 ? 2 : 1;  // bytes of a value
   __shared__ double2 cs_s[kRows][128];
   __shared__ __align__(16) uint16_t k_s[kRows][HPW][D];
-  const int wave = threadIdx.x >> 6, lane = lane_id();
-  const int64_t t = (int64_t)blockIdx.x * kRows + wave;
-  if (t >= a.T) return;
-  const RowSeq q = find_row(a.s, t);
-  if (q.b < 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+  int64_t t = (int64_t)blockIdx.x * kRows + wave;  // row
+  RowSeq q;
+  bool mine = true, whole = false;  // there is such a row; all rows of the quad are there
+  if constexpr (QUADS) {
+    int64_t first, last;
+    q = find_quad(a.s, a.T, blockIdx.x, &first, &last, &t);
+    if (q.b < 0) return;
+    whole = t >= first && t + 3 <= last;
+    t += wave;
+    mine = t >= first && t <= last;
+  } else if (t >= a.T) {
+    return;
+  }
+  const int n = lane % LPH, g = lane / LPH;
+  const int q_groups = (a.n_q + HPW - 1) / HPW, kv_groups = (a.n_kv + HPW - 1) / HPW;
+  const int groups = q_groups + 2 * kv_groups, step = gridDim.y;
+  const uint16_t* row = a.qkv + t * a.qkv_stride;
+  // places of the lane's 8 elements in a query or key head: 4 pairs
+  const bool split = HALVES && n < a.rot / 8;
+  const bool turn = HALVES ? split : 8 * n < a.rot;
+  const int a0 = split ? 4 * n : 8 * n, b0 = split ? a.rot / 2 + 4 * n : 8 * n + 4;
+
+  // head of this lane in a group (of its kind), -1: none
+  const auto head_of = [&](int u) {
+    const int k = u < q_groups ? u : u < q_groups + kv_groups ? u - q_groups : u - q_groups - kv_groups;
+    const int h = k * HPW + g;
+    return h < (u < q_groups ? a.n_q : a.n_kv) ? h : -1;
+  };
+  const auto fetch = [&](int u, uint2& xa, uint2& xb) {
+    const int h = head_of(u);
+    if (h < 0) return;
+    const bool v = u >= q_groups + kv_groups;
+    const uint16_t* p = row + (size_t)(h + (u < q_groups ? 0 : v ? a.n_q + a.n_kv : a.n_q)) * D;
+    xa = *reinterpret_cast<const uint2*>(p + (v ? 8 * n : a0));
+    xb = *reinterpret_cast<const uint2*>(p + (v ? 8 * n + 4 : b0));
+  };
+  int u = mine ? blockIdx.y : groups;
+  uint2 xa = make_uint2(0, 0), xb = make_uint2(0, 0);
+  if (u < groups) fetch(u, xa, xb);
+
+  if constexpr (!QUADS) {
+    q = find_row(a.s, t);
+    if (q.b < 0) return;
+  }
   const int64_t tok = (int64_t)q.len - q.rows + (t - q.r0);
   const int page = page_of(a.s, q.b, tok);
   const int P = 1 << a.s.log2P, o = (int)(tok & (P - 1));
   const KvLayout lay = kv_layout(FMT, D, P);
   uint8_t* page_p = a.pool + (size_t)max(page, 0) * ((size_t)a.n_kv * lay.head);
 
-  const double p = (double)(a.pos ? (int64_t)a.pos[t] : tok);
+  const double p = (double)(a.pos && mine ? (int64_t)a.pos[t] : tok);
   for (int i = lane; i < a.rot / 2; i += 64) {
     double s, c;
-    sincos(p * a.inv_freq[i], &s, &c);
+    sin_cos(p * a.inv_freq[i], &s, &c);
     cs_s[wave][i] = make_double2(c * (double)a.rope_scale, s * (double)a.rope_scale);
   }
   wave_lds_fence();
+  const auto weights = [&](const float* w, float (&out)[8]) {
+    if (!w) return;
+    const float4 wa = *reinterpret_cast<const float4*>(w + a0), wb = *reinterpret_cast<const float4*>(w + b0);
+    out[0] = wa.x; out[1] = wa.y; out[2] = wa.z; out[3] = wa.w;
+    out[4] = wb.x; out[5] = wb.y; out[6] = wb.z; out[7] = wb.w;
+  };
+  // the cache's part of a group: x, 8 consecutive elements of a lane
+  const auto store = [&](int h, bool is_v, uint4 x) {
+    store_token<FMT, D>(page_p + (size_t)max(h, 0) * lay.head, lay, P, o, n, is_v,
+                        is_v ? a.v_ts : a.k_ts, x, h >= 0 && page >= 0);
+  };
 
-  const int n = lane % LPH, g = lane / LPH;
-  const int NH = a.n_q + 2 * a.n_kv;
-  const uint16_t* row = a.qkv + t * a.qkv_stride;
-  const bool split = !a.interleaved && n < a.rot / 8;  // holds pairs (i, i + rot/2)
-  const bool turn = split || (a.interleaved && 8 * n < a.rot);
-
-  for (int h0 = blockIdx.y * HPW; h0 < NH; h0 += gridDim.y * HPW) {
-    const int h = h0 + g;
-    const bool live = h < NH, is_q = h < a.n_q, is_v = h >= a.n_q + a.n_kv;
-    const bool sp = split && !is_v;
-    const int a0 = sp ? 4 * n : 8 * n, b0 = sp ? a.rot / 2 + 4 * n : 8 * n + 4;
-    uint2 xa = make_uint2(0, 0), xb = make_uint2(0, 0);
-    if (live) {
-      xa = *reinterpret_cast<const uint2*>(row + (size_t)h * D + a0);
-      xb = *reinterpret_cast<const uint2*>(row + (size_t)h * D + b0);
-    }
-    if (h0 < a.n_q + a.n_kv) {  // some head of this group is a query or a key
-      double z[8] = {lo16(xa.x), hi16(xa.x), lo16(xa.y), hi16(xa.y),
-                     lo16(xb.x), hi16(xb.x), lo16(xb.y), hi16(xb.y)};
-      const float* w = is_q ? a.q_norm : a.k_norm;
-      double ss = 0.0;
+  if (u < q_groups) {
+    float w[8], cs[8];
+    weights(a.q_norm, w);
+    if (turn) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fma(z[i], z[i], ss);
-#pragma unroll
-      for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor(ss, m);
-      if (w && !is_v) {
-        const double r = rsqrt(ss / D + (double)a.eps);
-        const float4 wa = *reinterpret_cast<const float4*>(w + a0);
-        const float4 wb = *reinterpret_cast<const float4*>(w + b0);
-        const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = z[i] * r * (double)ww[i];
+      for (int i = 0; i < 4; ++i) {
+        const double2 c = cs_s[wave][4 * n + i];
+        cs[2 * i] = (float)c.x;
+        cs[2 * i + 1] = (float)c.y;
       }
-      if (turn && !is_v) {
+    }
+    for (; u < q_groups; u += step) {
+      const int h = head_of(u);
+      float z[8] = {lo16(xa.x), hi16(xa.x), lo16(xa.y), hi16(xa.y),
+                    lo16(xb.x), hi16(xb.x), lo16(xb.y), hi16(xb.y)};
+      if (u + step < groups) fetch(u + step, xa, xb);
+      norm_turn<LPH, D>(z, w, a.q_norm != nullptr, a.eps, split, turn, cs);
+      if (h < 0) continue;
+      uint16_t* d = a.q_out + t * a.q_stride + (size_t)h * D;
+      *reinterpret_cast<uint2*>(d + a0) = make_uint2(bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]));
+      *reinterpret_cast<uint2*>(d + b0) = make_uint2(bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7]));
+    }
+  }
+  for (; u < q_groups + kv_groups; u += step) {
+    const int h = head_of(u);
+    double z[8] = {lo16(xa.x), hi16(xa.x), lo16(xa.y), hi16(xa.y),
+                   lo16(xb.x), hi16(xb.x), lo16(xb.y), hi16(xb.y)};
+    if (u + step < groups) fetch(u + step, xa, xb);
+    float w[8];
+    double cs[8];
+    weights(a.k_norm, w);
+    if (turn) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const double2 c = cs_s[wave][4 * n + i];
+        cs[2 * i] = c.x;
+        cs[2 * i + 1] = c.y;
+      }
+    }
+    norm_turn<LPH, D>(z, w, a.k_norm != nullptr, a.eps, split, turn, cs);
+    uint32_t y[4];  // fp64 -> fp32 -> bf16 (the compiler makes one rounding of two conversions)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i] = (uint32_t)f32_to_bf16_rne((float)z[2 * i]) | ((uint32_t)f32_to_bf16_rne((float)z[2 * i + 1]) << 16);
+    const uint2 ya = make_uint2(y[0], y[1]), yb = make_uint2(y[2], y[3]);
+    if (h >= 0 && a.k_out) {
+      uint16_t* k = a.k_out + t * a.k_stride + (size_t)h * D;
+      *reinterpret_cast<uint2*>(k + a0) = ya;
+      *reinterpret_cast<uint2*>(k + b0) = yb;
+    }
+    uint16_t* st = k_s[wave][g];
+    *reinterpret_cast<uint2*>(st + a0) = ya;
+    *reinterpret_cast<uint2*>(st + b0) = yb;
+    wave_lds_fence();
+    const uint4 x = *reinterpret_cast<const uint4*>(st + 8 * n);
+    wave_lds_fence();
+    store(h, false, x);
+  }
+  if (!QUADS || !whole) {
+    for (; u < groups; u += step) {
+      const int h = head_of(u);
+      const uint4 x = make_uint4(xa.x, xa.y, xb.x, xb.y);
+      if (u + step < groups) fetch(u + step, xa, xb);
+      store(h, true, x);
+    }
+    return;
+  }
+  // a whole quad: each wave's token into LDS, then a thread's two elements of all
+  // four tokens to their place
+  if constexpr (QUADS) {
+    uint8_t* const v_s = reinterpret_cast<uint8_t*>(k_s);  // [token][head of the group][D]
+    const int tg = threadIdx.x / (D / 2), td = 2 * (threadIdx.x % (D / 2));
+    __syncthreads();  // the keys' part has been read
+    for (; u < groups; u += step) {
+      const int h = head_of(u);
+      const uint4 x = make_uint4(xa.x, xa.y, xb.x, xb.y);
+      if (u + step < groups) fetch(u + step, xa, xb);
+      uint8_t* const mine_s = v_s + ((wave * HPW + g) * D + 8 * n) * VB;
+      if constexpr (FMT == MOE_FMT_BF16) {
+        *reinterpret_cast<uint4*>(mine_s) = x;
+      } else {
+        uint16_t d;
+        *reinterpret_cast<uint2*>(mine_s) = q8_codes(x, &d);
+        if (h >= 0 && page >= 0 && tok >= 0 && !(n & 3))
+          *reinterpret_cast<uint16_t*>(page_p + (size_t)h * lay.head + lay.vs + 2 * ((n >> 2) * P + o)) = d;
+      }
+      __syncthreads();
+      const int th = (u - q_groups - kv_groups) * HPW + tg;
+      if (th < a.n_kv && page >= 0) {
+        uint8_t* dst = page_p + (size_t)th * lay.head + lay.vq + ((o >> 2) * D + td) * 4 * VB;
+        uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const double2 cs = cs_s[wave][4 * n + i];
-          const double zu = sp ? z[i] : z[2 * i], zv = sp ? z[i + 4] : z[2 * i + 1];
-          const double nu = zu * cs.x - zv * cs.y, nv = zv * cs.x + zu * cs.y;
-          if (sp) { z[i] = nu; z[i + 4] = nv; } else { z[2 * i] = nu; z[2 * i + 1] = nv; }
+          const uint8_t* p = v_s + ((i * HPW + tg) * D + td) * VB;
+          w[i] = VB == 2 ? *reinterpret_cast<const uint32_t*>(p) : (uint32_t)*reinterpret_cast<const uint16_t*>(p);
+        }
+        if constexpr (FMT == MOE_FMT_BF16) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(
+              __builtin_amdgcn_perm(w[1], w[0], 0x05040100u), __builtin_amdgcn_perm(w[3], w[2], 0x05040100u),
+              __builtin_amdgcn_perm(w[1], w[0], 0x07060302u), __builtin_amdgcn_perm(w[3], w[2], 0x07060302u));
+        } else {
+          const uint32_t l = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);  // a0 b0 a1 b1
+          const uint32_t r = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(__builtin_amdgcn_perm(r, l, 0x05040100u),
+                                                      __builtin_amdgcn_perm(r, l, 0x07060302u));
         }
       }
-      if (!is_v) {
-        xa = make_uint2(bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]));
-        xb = make_uint2(bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7]));
-      }
-      if (live && is_q) {
-        uint16_t* d = a.q_out + t * a.q_stride + (size_t)h * D;
-        *reinterpret_cast<uint2*>(d + a0) = xa;
-        *reinterpret_cast<uint2*>(d + b0) = xb;
-      } else if (live && !is_v && a.k_out) {
-        uint16_t* k = a.k_out + t * a.k_stride + (size_t)(h - a.n_q) * D;
-        *reinterpret_cast<uint2*>(k + a0) = xa;
-        *reinterpret_cast<uint2*>(k + b0) = xb;
-      }
-    }
-    if (h0 + HPW > a.n_q) {  // some head of this group goes into the cache
-      uint16_t* st = k_s[wave][g];
-      *reinterpret_cast<uint2*>(st + a0) = xa;
-      *reinterpret_cast<uint2*>(st + b0) = xb;
-      wave_lds_fence();
-      const uint4 x = *reinterpret_cast<const uint4*>(st + 8 * n);
-      wave_lds_fence();
-      const int kvh = is_v ? h - a.n_q - a.n_kv : max(h - a.n_q, 0);
-      store_token<FMT, D>(page_p + (size_t)kvh * lay.head, lay, P, o, n, is_v,
-                          is_v ? a.v_ts : a.k_ts, x, live && !is_q && page >= 0);
+      __syncthreads();
     }
   }
 }
@@ -250,147 +444,166 @@ struct ReadArgs {
   float k_ts, v_ts;
 };
 
-// Tokens first.. of sequence b that are read, in units of 16 aligned tokens.
-__device__ __forceinline__ void read_span(const ReadArgs& a, int b, int64_t* f, int64_t* end,
-                                          int64_t* units) {
-  *f = a.first ? max((int64_t)a.first[b], (int64_t)0) : 0;
-  const int64_t room = (int64_t)a.out_start[b + 1] - a.out_start[b];
-  *end = min((int64_t)a.s.kv_len[b], *f + room);
-  *units = *end > *f ? ((*end - 1) >> 4) - (*f >> 4) + 1 : 0;
-}
-
 constexpr uint32_t kNanPair = 0x7fc07fc0u;
 
-// One wave per 16 aligned tokens of a sequence and head: both halves are bound
-// by writing bf16 rows, so a lane takes what it writes as one vector: 8
-// consecutive elements of a key, D/16 of a value (its quad layout).
+__device__ __forceinline__ float e4m3_scale(uint32_t b) {  // (0x7f, 0xff: NaN)
+  return (b & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : e4m3_to_f32(b);
+}
+
+// Eight E2M1 codes of a word times a block's scale and the tensor's, as bf16.
+__device__ __forceinline__ uint4 fp4_values(uint32_t q, float s, float ts) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0);
+  const f2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1);
+  const f2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
+  const f2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
+  return make_uint4(bf16_pair(p0.x * s * ts, p0.y * s * ts), bf16_pair(p1.x * s * ts, p1.y * s * ts),
+                    bf16_pair(p2.x * s * ts, p2.y * s * ts), bf16_pair(p3.x * s * ts, p3.y * s * ts));
+}
+__device__ __forceinline__ uint32_t i8_values(uint32_t q, int i, float s) {  // bytes i, i + 1
+  return bf16_pair((float)(int8_t)(q >> (8 * i)) * s, (float)(int8_t)(q >> (8 * i + 8)) * s);
+}
+
+// One wave per 16 aligned tokens of a sequence and head.  What it reads is a
+// third of what it writes or less (4 bits): every load of the wave is on its way
+// before the first value is worked on, each in the order of the cache, and a
+// lane writes consecutive elements of a row.
 template <int FMT, int D>
 __global__ __launch_bounds__(256) void k_kv_read(ReadArgs a) {
-  const int lane = lane_id();
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int h = blockIdx.y;
-  // the sequence that holds this unit: a running sum over the sequences
-  int64_t base = 0;
-  int b = -1;
-  int64_t u = 0;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = (int)blockIdx.x * 4 + wave, h = blockIdx.y;
+  // the sequence that holds this unit: tokens f.. and units of its span, summed
+  int before = 0, u = -1, b = -1;
+  int64_t f = 0, end = 0, out = 0;
   for (int i0 = 0; i0 < a.s.n_seq; i0 += 64) {
-    int64_t f, e, m = 0;
-    if (i0 + lane < a.s.n_seq) read_span(a, i0 + lane, &f, &e, &m);
-    int64_t sum = m;
+    const int i = min(i0 + lane, a.s.n_seq - 1);
+    const int from = a.first ? max(a.first[i], 0) : 0, len = a.s.kv_len[i];
+    const int o0 = a.out_start[i], o1 = a.out_start[i + 1];
+    const int64_t stop = min((int64_t)len, from + max((int64_t)o1 - o0, (int64_t)0));
+    int sum = i0 + lane < a.s.n_seq && stop > from ? (int)((stop - 1) >> 4) - (from >> 4) + 1 : 0;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int64_t v = __shfl_up(sum, d);
+      const int v = __shfl_up(sum, d);
       if (lane >= d) sum += v;
     }
-    const uint64_t past = __ballot(base + sum > unit);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      b = i0 + l;
-      u = unit - (base + __shfl(sum, l) - __shfl(m, l));
-      break;
+    const uint64_t past = __ballot(before + sum > unit);
+    if (!past) {
+      before += __builtin_amdgcn_readlane(sum, 63);
+      continue;
     }
-    base += __shfl(sum, 63);
+    const int l = __ffsll((unsigned long long)past) - 1;
+    if (l > 0) before += __builtin_amdgcn_readlane(sum, l - 1);
+    b = i0 + l;
+    f = __builtin_amdgcn_readlane(from, l);
+    out = __builtin_amdgcn_readlane(o0, l);
+    end = min((int64_t)__builtin_amdgcn_readlane(len, l), f + __builtin_amdgcn_readlane(o1, l) - out);
+    u = unit - before;
+    break;
   }
   if (b < 0) return;
-  int64_t f, end, units;
-  read_span(a, b, &f, &end, &units);
   const int64_t t0 = ((f >> 4) + u) << 4;  // first token of the unit
   const int page = page_of(a.s, b, t0);
-  const int P = 1 << a.s.log2P, o0 = (int)(t0 & (P - 1));
+  const int P = 1 << a.s.log2P, o = (int)(t0 & (P - 1));
   const KvLayout lay = kv_layout(FMT, D, P);
   const uint8_t* blk = a.pool + (size_t)max(page, 0) * ((size_t)a.n_kv * lay.head) + (size_t)h * lay.head;
-  const int64_t row0 = (int64_t)a.out_start[b] + t0 - f;
+  const int64_t row0 = out + t0 - f;
+  const auto wanted = [&](int j) {  // token j of the unit
+    return t0 + j >= f && t0 + j < end && row0 + j >= 0 && row0 + j < a.R;
+  };
 
+  // keys: 8 elements of a token a lane
+  constexpr int LPT = D / 8, TPI = 64 / LPT, KI = 16 / TPI;  // lanes of a token, tokens at a time
+  const int kn = lane % LPT, kj = lane / LPT;
+  uint4 kq[KI];
+  uint32_t kscale[KI];
   if (a.k_out) {
-    constexpr int LPT = D / 8, TPI = 64 / LPT;  // lanes per token, tokens at a time
-    const int n = lane % LPT;
 #pragma unroll
-    for (int i = 0; i < 16 / TPI; ++i) {
-      const int j = i * TPI + lane / LPT, o = o0 + j;
-      const int64_t row = row0 + j;
-      if (t0 + j < f || t0 + j >= end || row < 0 || row >= a.R) continue;
-      uint4 x;
-      if (page < 0) {
-        x = make_uint4(kNanPair, kNanPair, kNanPair, kNanPair);
-      } else if constexpr (FMT == MOE_FMT_BF16) {
-        x = *reinterpret_cast<const uint4*>(blk + 2 * (o * D + 8 * n));
+    for (int i = 0; i < KI; ++i) {
+      const int tok = o + i * TPI + kj;
+      if constexpr (FMT == MOE_FMT_BF16) {
+        kq[i] = *reinterpret_cast<const uint4*>(blk + 2 * (tok * D + 8 * kn));
+      } else if constexpr (FMT == MOE_FMT_Q8_0) {
+        const uint2 x = *reinterpret_cast<const uint2*>(blk + tok * D + 8 * kn);
+        kq[i].x = x.x; kq[i].y = x.y;
+        kscale[i] = *reinterpret_cast<const uint16_t*>(blk + lay.ks + 2 * (tok * (D / 32) + (kn >> 2)));
       } else {
-        float v[8], s;
-        if constexpr (FMT == MOE_FMT_NVFP4) {
-          const uint32_t q = *reinterpret_cast<const uint32_t*>(blk + o * (D / 2) + 4 * n);
-          const uint32_t sb = blk[lay.ks + o * (D / 16) + (n >> 1)];
-          s = (sb & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : e4m3_to_f32(sb);
-          typedef float f2 __attribute__((ext_vector_type(2)));
-          const f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0);
-          const f2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1);
-          const f2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
-          const f2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
-          v[0] = p0.x; v[1] = p0.y; v[2] = p1.x; v[3] = p1.y;
-          v[4] = p2.x; v[5] = p2.y; v[6] = p3.x; v[7] = p3.y;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = v[k] * s * a.k_ts;
-        } else {
-          const uint2 q = *reinterpret_cast<const uint2*>(blk + o * D + 8 * n);
-          s = f16_to_f32(*reinterpret_cast<const uint16_t*>(blk + lay.ks + 2 * (o * (D / 32) + (n >> 2))));
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            v[k] = (float)(int8_t)((k < 4 ? q.x : q.y) >> (8 * (k & 3))) * s;
-        }
-        x.x = (uint32_t)f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16);
-        x.y = (uint32_t)f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16);
-        x.z = (uint32_t)f32_to_bf16_rne(v[4]) | ((uint32_t)f32_to_bf16_rne(v[5]) << 16);
-        x.w = (uint32_t)f32_to_bf16_rne(v[6]) | ((uint32_t)f32_to_bf16_rne(v[7]) << 16);
+        kq[i].x = *reinterpret_cast<const uint32_t*>(blk + tok * (D / 2) + 4 * kn);
+        kscale[i] = blk[lay.ks + tok * (D / 16) + (kn >> 1)];
       }
-      *reinterpret_cast<uint4*>(a.k_out + row * a.k_stride + (size_t)h * D + 8 * n) = x;
     }
   }
+  // values: NVFP4: D/16 elements of one token; the others: 16 bytes, four tokens'
+  constexpr int GE = D / 16;                              // elements (NVFP4)
+  constexpr int DC = FMT == MOE_FMT_BF16 ? 2 : 4;         // elements of a chunk (others)
+  constexpr int VI = FMT == MOE_FMT_NVFP4 ? 4 : D / (16 * DC);
+  const uint8_t* vq = blk + lay.vq;
+  uint4 vv[VI];
+  uint2 vscale[VI];
   if (a.v_out) {
-    constexpr int GE = D / 16;  // elements of a lane: group n of the quad's token bq
-    const int n = lane >> 2, bq = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = 4 * i + bq, o = o0 + j;
-      const int64_t row = row0 + j;
-      if (t0 + j < f || t0 + j >= end || row < 0 || row >= a.R) continue;
-      uint32_t x[GE / 2];
-      const uint8_t* vq = blk + lay.vq;
-      if (page < 0) {
-#pragma unroll
-        for (int k = 0; k < GE / 2; ++k) x[k] = kNanPair;
+    for (int i = 0; i < VI; ++i) {
+      if constexpr (FMT == MOE_FMT_NVFP4) {
+        const uint8_t* p = vq + ((o / 4 + i) * 64 + lane) * (GE / 2);
+        if constexpr (GE == 4) vv[i].x = *reinterpret_cast<const uint16_t*>(p);
+        if constexpr (GE == 8) vv[i].x = *reinterpret_cast<const uint32_t*>(p);
+        if constexpr (GE == 16) { const uint2 x = *reinterpret_cast<const uint2*>(p); vv[i].x = x.x; vv[i].y = x.y; }
+        vscale[i].x = blk[lay.vs + ((lane >> 2) * GE / 16) * P + o + 4 * i + (lane & 3)];
       } else {
-        uint16_t e[GE];
-        if constexpr (FMT == MOE_FMT_BF16) {
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(vq) + ((o >> 2) * D + n * GE) * 4 + bq;
-#pragma unroll
-          for (int k = 0; k < GE; ++k) e[k] = src[4 * k];
-        } else if constexpr (FMT == MOE_FMT_Q8_0) {
-          const int8_t* src = reinterpret_cast<const int8_t*>(vq) + ((o >> 2) * D + n * GE) * 4 + bq;
-          const float s = f16_to_f32(*reinterpret_cast<const uint16_t*>(blk + lay.vs + 2 * ((n * GE / 32) * P + o)));
-#pragma unroll
-          for (int k = 0; k < GE; ++k) e[k] = f32_to_bf16_rne((float)src[4 * k] * s);
-        } else {
-          const uint32_t sb = blk[lay.vs + (n * GE / 16) * P + o];
-          const float s = (sb & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : e4m3_to_f32(sb);
-          const uint8_t* src = vq + (((o >> 2) * 16 + n) * 4 + bq) * (GE / 2);
-          uint32_t q[2] = {0, 0};
-          if constexpr (GE == 4) q[0] = *reinterpret_cast<const uint16_t*>(src);
-          if constexpr (GE == 8) q[0] = *reinterpret_cast<const uint32_t*>(src);
-          if constexpr (GE == 16) { const uint2 t = *reinterpret_cast<const uint2*>(src); q[0] = t.x; q[1] = t.y; }
-#pragma unroll
-          for (int k = 0; k < GE; ++k) {
-            const uint32_t c = (q[k >> 3] >> (4 * (k & 7))) & 15u;
-            const uint32_t ex = (c >> 1) & 3u, m = c & 1u;
-            const float mag = ex ? __uint_as_float(((ex + 126u) << 23) | (m << 22)) : 0.5f * (float)m;
-            e[k] = f32_to_bf16_rne(((c & 8u) ? -mag : mag) * s * a.v_ts);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < GE / 2; ++k) x[k] = (uint32_t)e[2 * k] | ((uint32_t)e[2 * k + 1] << 16);
+        const int c = i * 64 + lane, quad = c / (D / DC), d = c % (D / DC) * DC;
+        vv[i] = *reinterpret_cast<const uint4*>(vq + (o / 4 * (D / DC) + c) * 16);
+        if constexpr (FMT == MOE_FMT_Q8_0)
+          vscale[i] = *reinterpret_cast<const uint2*>(blk + lay.vs + 2 * ((d / 32) * P + o + 4 * quad));
       }
-      uint16_t* dst = a.v_out + row * a.v_stride + (size_t)h * D + n * GE;
-      if constexpr (GE == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(x[0], x[1]);
-      if constexpr (GE >= 8) *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
-      if constexpr (GE == 16) *reinterpret_cast<uint4*>(dst + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+  }
+
+  if (a.k_out) {
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const int j = i * TPI + kj;
+      uint4 x = kq[i];
+      if constexpr (FMT == MOE_FMT_NVFP4) x = fp4_values(kq[i].x, e4m3_scale(kscale[i]), a.k_ts);
+      if constexpr (FMT == MOE_FMT_Q8_0) {
+        const float s = f16_to_f32((uint16_t)kscale[i]);
+        x = make_uint4(i8_values(kq[i].x, 0, s), i8_values(kq[i].x, 2, s), i8_values(kq[i].y, 0, s),
+                       i8_values(kq[i].y, 2, s));
+      }
+      if (page < 0) x = make_uint4(kNanPair, kNanPair, kNanPair, kNanPair);
+      if (wanted(j))
+        *reinterpret_cast<uint4*>(a.k_out + (row0 + j) * a.k_stride + (size_t)h * D + 8 * kn) = x;
+    }
+  }
+  if (!a.v_out) return;
+#pragma unroll
+  for (int i = 0; i < VI; ++i) {
+    if constexpr (FMT == MOE_FMT_NVFP4) {
+      const int j = 4 * i + (lane & 3), n = lane >> 2;
+      const float s = page < 0 ? __uint_as_float(0x7fc00000u) : e4m3_scale(vscale[i].x);
+      const uint4 x = fp4_values(vv[i].x, s, a.v_ts);
+      if (!wanted(j)) continue;
+      uint16_t* dst = a.v_out + (row0 + j) * a.v_stride + (size_t)h * D + n * GE;
+      if constexpr (GE == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(x.x, x.y);
+      if constexpr (GE >= 8) *reinterpret_cast<uint4*>(dst) = x;
+      if constexpr (GE == 16) *reinterpret_cast<uint4*>(dst + 8) = fp4_values(vv[i].y, s, a.v_ts);
+    } else {
+      const int c = i * 64 + lane, quad = c / (D / DC), d = c % (D / DC) * DC;
+      const uint32_t w[4] = {vv[i].x, vv[i].y, vv[i].z, vv[i].w};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int j = 4 * quad + t;
+        uint16_t* dst = a.v_out + (row0 + j) * a.v_stride + (size_t)h * D + d;
+        if constexpr (FMT == MOE_FMT_BF16) {  // w: two tokens of an element each
+          const uint32_t x = __builtin_amdgcn_perm(w[2 + t / 2], w[t / 2], t & 1 ? 0x07060302u : 0x05040100u);
+          if (wanted(j)) *reinterpret_cast<uint32_t*>(dst) = page < 0 ? kNanPair : x;
+        } else {  // w: four tokens of an element each
+          const float s = page < 0 ? __uint_as_float(0x7fc00000u)
+                                   : f16_to_f32((uint16_t)((t < 2 ? vscale[i].x : vscale[i].y) >> (16 * (t & 1))));
+          float e[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k] = (float)(int8_t)(w[k] >> (8 * t)) * s;
+          if (wanted(j)) *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(e[0], e[1]), bf16_pair(e[2], e[3]));
+        }
+      }
     }
   }
 }
@@ -427,13 +640,17 @@ hipError_t launch_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const 
                qkv_stride, q_stride, k_stride, T, seq_view(c, s), p->n_q, c->n_kv, p->rot_dim,
                p->interleaved, p->eps, p->rope_scale, c->k_scale, c->v_scale};
   const int per_wave = 64 / (c->D / 8);
-  const int groups = (p->n_q + 2 * c->n_kv + per_wave - 1) / per_wave;
-  const int64_t wgs = (T + kRows - 1) / kRows;
-  // few rows: the heads of a row spread over workgroups
-  int hs = (int)((2048 + wgs - 1) / wgs);
+  const int groups = (p->n_q + per_wave - 1) / per_wave + 2 * ((c->n_kv + per_wave - 1) / per_wave);
+  // (quads: n rows of a sequence lie in at most n/4 + 2 of them)
+  const int64_t wgs = c->fmt == MOE_FMT_NVFP4 ? (T + kRows - 1) / kRows : T / 4 + 2 * (int64_t)s->n_seq;
+  // few rows: the heads of a row spread over workgroups (each takes the row's
+  // angles again: 4096 rows 19.2 us over 1024 workgroups, 22 over 4096)
+  int hs = (int)((1024 + wgs - 1) / wgs);
   hs = hs < 1 ? 1 : hs > groups ? groups : hs;
   return by_format(c->fmt, c->D, [&](auto F, auto DD) {
-    k_kv_append<F(), DD()><<<dim3((unsigned)wgs, (unsigned)hs), 64 * kRows, 0, stream>>>(a);
+    const dim3 grid((unsigned)wgs, (unsigned)hs);
+    if (a.interleaved) k_kv_append<F(), DD(), false><<<grid, 64 * kRows, 0, stream>>>(a);
+    else k_kv_append<F(), DD(), true><<<grid, 64 * kRows, 0, stream>>>(a);
     return hipGetLastError();
   });
 }

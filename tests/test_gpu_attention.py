@@ -282,6 +282,25 @@ def test_append_matches_reference(fmt, D, P, rot, inter, normed):
     assert (got_k[int(s.start[-1]):] == ref.bf16_bits([7.0])[0]).all()
 
 
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("D,n_kv", [(64, 3), (64, 9), (128, 5), (256, 3)])
+def test_append_whole_and_part_quads(fmt, D, n_kv):
+    """Tokens are written four at a time where a call holds all four: prompts
+    that start and end inside a quad and cross pages, more than 64 sequences
+    before them, fewer tokens than rows."""
+    n_q = n_kv
+    lens = [1] * 66 + [13, 43, 3, 8]
+    rows = [1] * 30 + [0] * 36 + [13, 38, 5, 8]
+    s = Setup(fmt, n_kv, D, 32, lens, rows, seed=D + n_kv, v_ts=1.5, pad_rows=1)
+    qkv = append_inputs(s, n_q, 6)
+    norm = [np.ones(D, np.float32)] * 2
+    freq, _ = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 32, 10000.0)
+    print("append quads", FMT[fmt], D, n_kv, flush=True)
+    got_q, got_k, _ = run_append(s, n_q, qkv, norm, 32, 0, freq, 1.0)
+    check_append(s, n_q, qkv, norm, 32, 0, freq, 1.0, got_q, got_k)
+    assert (got_q[int(s.start[-1]):] == ref.bf16_bits([7.0])[0]).all()
+
+
 def test_append_far_positions_scaled_and_given():
     """Positions near 2^31 given by the caller, frequencies interpolated by
     parts with their factor on cosines and sines; queries and keys written in
