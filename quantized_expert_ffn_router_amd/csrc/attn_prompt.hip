@@ -53,6 +53,14 @@ __device__ __forceinline__ int swz(int row, int chunk) {
   else return chunk ^ (((row & 3) << 2) | ((row >> 2) & 3));
 }
 
+// Waits until at most N of the wave's loads are on their way (its newest ones).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0f70);
+#endif
+}
+
 // One head's key or value rows of a sequence, as tiles of 64 rows that go
 // straight from global memory into LDS: lane i of a load fills the 16 bytes at
 // slot i and reads the chunk that belongs there.  Buffer loads: the lanes'
@@ -244,7 +252,7 @@ __device__ __forceinline__ void careful_pass(Rows<D>& w, uint8_t* kt, uint8_t* v
     __syncthreads();
     K.load(kt, it, wave);
     V.load(vt, it, wave);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    wait_loads<0>();
     __syncthreads();
     const int64_t t0 = (int64_t)it * kBN;
     v16f x[2];
@@ -391,10 +399,15 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
   const Tiles<D, WAVES> V(a.v + k0 * a.v_stride + (int64_t)(head / a.G) * D, a.v_stride, len, wave, lane);
 
   if (n_tiles > 0) {
+    constexpr int N = Tiles<D, WAVES>::LOADS;
     K.load(k_even, 0, wave);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     V.load(v_even, 0, wave);
-    if (n_tiles > 1) K.load(k_odd, 1, wave);
+    if (n_tiles > 1) {
+      K.load(k_odd, 1, wave);
+      wait_loads<2 * N>();
+    } else {
+      wait_loads<N>();
+    }
     __syncthreads();
     v16f x[2];
     w.scores(k_even, x);
@@ -406,7 +419,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
     // variables of their own and named statically, so that no read waits for
     // a load into another one.
     const auto arrive = [&](int it, uint8_t* k0, uint8_t* v1) {
-      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's parts of the tiles
+      wait_loads<0>();  // this wave's parts of the tiles
       __syncthreads();
       if (it + 2 < n_tiles) K.load(k0, it + 2, wave);
       if (it + 1 < n_tiles) V.load(v1, it + 1, wave);
