@@ -479,3 +479,72 @@ def layer_forward(layer: DeviceLayer, buf: StepBuffers, x, T: int, residual=None
     if hist_shifts is not None and not fused_gating:
         moe_expert_hist(d, buf.buckets, buf.hist, hist_shifts[0], hist_shifts[1], stream)
     return buf.out
+
+
+class KvCache:
+    """A layer's paged key/value cache in HBM (n_pages pages of page_tokens
+    tokens; fmt MOE_FMT_NVFP4, _Q8_0 or _BF16), with the norm weights and rotary
+    frequencies of its layer: q_norm, k_norm float32 [D] or None, rope a pair
+    (frequencies, scale) as moe_rope_freqs returns it, or None."""
+
+    def __init__(self, fmt, n_q, n_kv, D, page_tokens, n_pages, q_norm=None, k_norm=None, rope=None,
+                 interleaved=0, eps=1e-6, k_scale=1.0, v_scale=1.0, device="cuda"):
+        import torch
+        dev = torch.device(device)
+        self.n_q, self.n_kv, self.D = n_q, n_kv, D
+        self.page_bytes = moe_kv_page_bytes(fmt, n_kv, D, page_tokens)
+        if self.page_bytes == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
+        self.pool = torch.empty(n_pages * self.page_bytes, dtype=torch.uint8, device=dev)
+        t = lambda a, dt: None if a is None else torch.as_tensor(a, dtype=dt, device=dev).contiguous()  # noqa: E731
+        self.q_norm, self.k_norm = t(q_norm, torch.float32), t(k_norm, torch.float32)
+        freqs, scale = (None, 1.0) if rope is None else rope
+        self.inv_freq = t(freqs, torch.float64)
+        rot = 0 if freqs is None else 2 * len(freqs)
+        self.desc = KvCacheDesc(fmt, n_kv, D, page_tokens, n_pages, k_scale, v_scale,
+                                self.pool.data_ptr())
+        self.qkv_desc = QkvDesc(n_q, eps, _ptr(self.q_norm), _ptr(self.k_norm), rot, interleaved,
+                                _ptr(self.inv_freq), scale)
+
+
+class AttnBuffers:
+    """Per-step device buffers for up to T_max rows of n_seq sequences with page
+    tables of max_pages pages; the host fills row_start, kv_len and page_table
+    (int32 device tensors) before a step."""
+
+    def __init__(self, cache: KvCache, n_seq: int, T_max: int, max_pages: int, device="cuda"):
+        import torch
+        dev = torch.device(device)
+        self.T_max = T_max
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)  # noqa: E731
+        bf16 = lambda heads: torch.empty((T_max, heads * cache.D), dtype=torch.bfloat16, device=dev)  # noqa: E731
+        self.row_start, self.kv_len, self.page_table = i32(n_seq + 1), i32(n_seq), i32(n_seq, max_pages)
+        self.seqs = SeqBatch(n_seq, max_pages, self.row_start.data_ptr(), self.kv_len.data_ptr(),
+                             self.page_table.data_ptr())
+        self.max_len = max_pages * cache.desc.page_tokens
+        self.q, self.k, self.out = bf16(cache.n_q), bf16(cache.n_kv), bf16(cache.n_q)
+        self.ws_bytes = moe_attn_workspace_bytes(cache.desc, cache.n_q, n_seq, T_max, self.max_len)
+        self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=dev)
+
+
+def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: float, prompt=None,
+                      max_len=0, stream=None):
+    """One layer's attention over the step's rows qkv (bf16 [T][n_q + 2 n_kv][D],
+    the projections' output): norms, rotation and cache write, then attention
+    over the cache.  prompt: None for decode and verification steps; for
+    prompts kv_start (int32 device [n_seq + 1], the running sum of kv_len), the
+    total Tk and buffers k, v (bf16 [Tk][n_kv][D]) as a tuple: the keys and
+    values, those cached earlier included, are read back into k, v first, so
+    that every chunk of a prompt attends to what the cache holds."""
+    c, D = cache.desc, cache.D
+    qw, kw = cache.n_q * D, cache.n_kv * D
+    moe_kv_append(c, cache.qkv_desc, buf.seqs, qkv, qw + 2 * kw, T, None, buf.q, qw, buf.k, kw, stream)
+    if prompt is None:
+        moe_attn_decode(c, buf.seqs, cache.n_q, buf.q, qw, T, max_len, scale, buf.out, qw, buf.ws,
+                        buf.ws_bytes, stream)
+    else:
+        kv_start, Tk, k, v = prompt
+        moe_kv_read(c, buf.seqs, None, kv_start, Tk, k, kw, v, kw, stream)
+        moe_attn_prompt(cache.n_q, cache.n_kv, D, buf.seqs.n_seq, buf.row_start, kv_start, T, Tk,
+                        buf.q, qw, k, kw, v, kw, scale, buf.out, qw, stream)
+    return buf.out

@@ -582,3 +582,46 @@ def test_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_attention_forward_then_layer_forward():
+    """The binding's path: two layers of attention and experts over a prompt in
+    two chunks and two decode steps give the rows of the same tokens taken in one
+    chunk, up to roundings: every chunk attends to what the cache holds."""
+    import moegen
+    n_q, n_kv, D, P = 8, 2, 64, 32
+    w = moegen.Workload(name="attn_stack", E=8, k=2, H=512, I=128, T=64)
+    rope = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 64, 10000.0)
+    layers = [q.DeviceLayer(moegen.make_layer(w)) for _ in range(2)]
+    gen = torch.Generator(device=dev).manual_seed(1)
+    proj = [torch.randn(512, (n_q + 2 * n_kv) * D, generator=gen, device=dev) / 20 for _ in range(2)]
+    x_all = torch.randn(1, 60, 512, generator=gen, device=dev).bfloat16()
+
+    def run(steps):
+        caches = [q.KvCache(NVFP4, n_q, n_kv, D, P, 4, np.ones(D), np.ones(D), rope) for _ in layers]
+        buf = q.AttnBuffers(caches[0], 1, 64, 2)
+        sb = q.StepBuffers(layers[0], 64)
+        buf.page_table.copy_(i32([[3, 1]]))
+        out, at = [], 0
+        for n, prompt in steps:
+            buf.row_start.copy_(i32([0, n]))
+            buf.kv_len.copy_(i32([at + n]))
+            x = x_all[0, at:at + n].clone()
+            at += n
+            kv = [torch.empty(at, n_kv * D, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+            for cache, layer, pj in zip(caches, layers, proj):
+                qkv = (x.float() @ pj).bfloat16()
+                o = q.attention_forward(cache, buf, qkv, n, 0.125, (i32([0, at]), at, *kv) if prompt else None)
+                x = (x.float() + o[:n].float()).bfloat16()
+                x = q.layer_forward(layer, sb, x, n, x)[:n].view(torch.bfloat16).clone()
+            out.append(x)
+        torch.cuda.synchronize()
+        return torch.cat(out), caches
+
+    whole, c1 = run([(60, True)])
+    parts, c2 = run([(37, True), (20, True), (1, False), (2, False)])
+    assert torch.isfinite(whole.float()).all()
+    err = (whole.float() - parts.float()).norm() / whole.float().norm()
+    # a decode row's weights are fp16 and a prompt's bf16 (2^-8), the row itself
+    # is rounded to bf16 a few times over in each of the two layers
+    assert err < 8 * 2.0 ** -8, float(err)
