@@ -4,7 +4,8 @@
  * router logits, softmax top-k gating, token-to-expert bucketing, block-
  * quantized (NVFP4, Q6_K-style, Q8_0, IQ3-style) SwiGLU expert FFNs with the dequantization
  * fused into the matmuls, the gate-weighted combine, and the per-step expert
- * usage histogram that decides which experts stay resident.
+ * usage histogram that decides which experts stay resident; and of the same
+ * layer's attention over a paged key/value cache.
  *
  * What the pages fix, and where:
  *   - each token uses a few experts chosen from many; the busiest experts stay
@@ -52,7 +53,7 @@
  *
  * Supported shapes: 1 <= k <= min(E, 64), E <= 1024, H % 128 == 0,
  * 128 <= H <= 8192, I % 128 == 0 (NVFP4, Q8_0) or I % 256 == 0 (Q6_K, IQ3G, IQ1G),
- * I <= 8192.
+ * I <= 8192.  The attention side states its own (moe_kv_cache, moe_qkv_desc).
  */
 #ifndef MOE_H
 #define MOE_H
@@ -481,8 +482,9 @@ moe_status moe_rope_freqs(int32_t kind, int32_t rot_dim, double base, double fac
  *     z = x / sqrt(mean(x^2) + eps) * w     (with a norm weight w; else z = x)
  *     (u, v) of pair i -> (u c - v s, v c + u s), c, s = rope_scale * cos, sin
  *     of p * inv_freq[i],
- *   in fp64, rounded to fp32 and then to bf16 once, so that the codes in the
- *   cache do not depend on the order of a sum.
+ *   keys in fp64, rounded to fp32 and then to bf16, so that the codes in the
+ *   cache do not depend on the order of a sum; queries, which meet the matrix
+ *   units anyway, in fp32 (sine and cosine from fp64), rounded to bf16 once.
  *   q_out: bf16 [T] rows of n_q * D, q_stride apart; k_out: the same with
  *   n_kv * D, or NULL (for moe_attn_prompt, whose values may stay in qkv).
  *   q_out and k_out may be the query and key parts of qkv itself (the same
