@@ -14,6 +14,8 @@
 // lanes, and a row's maximum needs two lane swaps.
 #include <type_traits>
 
+#include <algorithm>
+
 #include "attn_common.h"
 
 namespace moe {
@@ -23,6 +25,8 @@ namespace {
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
@@ -37,28 +41,113 @@ struct DecodeArgs {
   uint16_t* out;
   float* part_o;   // [T * n_q][S][D]
   float2* part_ml; // [T * n_q][S]
+  int* part_n;     // [T * n_q]: splits (1: the output is there already)
   int64_t q_stride, out_stride, T;
   SeqView s;
-  int n_q, n_kv, G, S, ztiles;
+  int n_q, n_kv, G, S, room, likely;
   float scale_log2, v_ts;
 };
 
+// How a step's work is cut: into items of one tile of `size` query rows and
+// `chunk` 32-token units of a sequence, the same chunk for all, so that
+// workgroups are even however different the sequences' lengths are.  Every wave
+// works it out from the lengths.
+struct Item {
+  int b, r0, rows, len;  // sequence (-1: there are not so many items), its first row, rows, length
+  int inside;            // rows inside 0..T
+  int tile, kvh, sp, splits, chunk;
+};
+
+// This lane's sequence.
+struct LaneSeq {
+  int start, end, len;
+  int tiles, units;
+  __device__ __forceinline__ LaneSeq(const SeqView& s, int i0, int64_t T, int G, int size) {
+    const int i = min(i0 + lane_id(), s.n_seq - 1);
+    start = s.row_start[i];
+    end = s.row_start[i + 1];
+    len = s.kv_len[i];
+    const int64_t n = i0 + lane_id() < s.n_seq && start >= 0 ? min((int64_t)end, T) - start : 0;
+    tiles = n > 0 ? (int)((uint32_t)((int)n * G + size - 1) / (uint32_t)size) : 0;
+    units = n > 0 && len > 0 ? (len - 1) / 32 + 1 : 0;
+  }
+};
+
+// The item of workgroup id.  chunk: a multiple of the waves, as small as keeps
+// the items within `room` more than the tiles (what the grid holds), and kWhole
+// units or more unless the 256 CUs need shorter ones (8 slots of 1000 to 60000
+// tokens: 33 us; as many chunks of each sequence as of any other, 37).
+constexpr int kWhole = 4 * kWaves;
+__device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, int size, int n_kv,
+                                          int room, int S, int id) {
+  Item r;
+  r.b = -1;
+  r.chunk = INT32_MAX;
+  const LaneSeq first(s, 0, T, G, size);
+  const int span = min(s.n_seq, 64);  // lanes that hold something
+  if (S > 1) {
+    float work = 0.0f;
+    int most = 0;
+    for (int i0 = 0; i0 < s.n_seq; i0 += 64) {
+      const LaneSeq q = i0 ? LaneSeq(s, i0, T, G, size) : first;
+      work += (float)q.tiles * (float)q.units;
+      most = max(most, q.units);
+    }
+    for (int d = 1; d < span; d <<= 1) {
+      work += __shfl_xor(work, d);
+      most = max(most, __shfl_xor(most, d));
+    }
+    int chunk = (int)ceilf(work / (float)room);
+    if (chunk < kWhole) chunk = max(chunk, min((int)ceilf(work * n_kv / 256.0f), kWhole));
+    chunk = (max(chunk, (most + S - 1) / S) + kWaves - 1) / kWaves * kWaves;
+    r.chunk = max(__builtin_amdgcn_readfirstlane(chunk), kWaves);
+  }
+  int before = 0;
+  for (int i0 = 0; i0 < s.n_seq; i0 += 64) {
+    const LaneSeq q = i0 ? LaneSeq(s, i0, T, G, size) : first;
+    // (a row without tokens is answered too)
+    const int splits = S > 1 && q.units ? (int)((uint32_t)(q.units - 1) / (uint32_t)r.chunk) + 1 : 1;
+    int sum = q.tiles * splits * n_kv;
+    for (int d = 1; d < span; d <<= 1) {
+      const int v = __shfl_up(sum, d);
+      if (lane_id() >= d) sum += v;
+    }
+    const uint64_t past = __ballot(i0 + lane_id() < s.n_seq && before + sum > id);
+    if (!past) {
+      before += __builtin_amdgcn_readlane(sum, min(63, s.n_seq - 1 - i0));
+      continue;
+    }
+    const int l = __ffsll((unsigned long long)past) - 1;
+    if (l > 0) before += __builtin_amdgcn_readlane(sum, l - 1);
+    r.b = i0 + l;
+    r.r0 = __builtin_amdgcn_readlane(q.start, l);
+    const int64_t rows = (int64_t)__builtin_amdgcn_readlane(q.end, l) - r.r0;
+    r.rows = (int)min(rows, (int64_t)INT32_MAX);
+    r.len = __builtin_amdgcn_readlane(q.len, l);
+    r.inside = (int)min(rows, T - r.r0);
+    r.splits = __builtin_amdgcn_readlane(splits, l);
+    const int at = (int)((uint32_t)(id - before) / (uint32_t)r.splits);
+    r.sp = id - before - at * r.splits;
+    r.tile = (int)((uint32_t)at / (uint32_t)n_kv);
+    r.kvh = at - r.tile * n_kv;
+    break;
+  }
+  return r;
+}
+
 // What one tile of `size` query rows (row r = i * G + g: packed row i, head g of
-// the group) of a sequence sees, and how its 32-token units are split.
+// the group) of a sequence sees.
 struct TilePlan {
   int64_t hi;  // last token that any row of the tile sees (-1: none)
   int64_t lo;  // last token that all of them see
-  int units, per_split;
+  int units;   // 32-token units up to hi
 };
-__device__ __forceinline__ TilePlan tile_plan(int len, int rows, int inside, int G, int tile,
-                                              int size, int S) {
+__device__ __forceinline__ TilePlan tile_plan(const Item& it, int G, int size) {
   TilePlan p;
-  const int last = min((int)((uint32_t)(tile * size + size - 1) / (uint32_t)G), inside - 1);
-  p.hi = max((int64_t)len - rows + last, (int64_t)-1);
-  p.lo = (int64_t)len - rows + (int)((uint32_t)(tile * size) / (uint32_t)G);
+  const int last = min((int)((uint32_t)(it.tile * size + size - 1) / (uint32_t)G), it.inside - 1);
+  p.hi = max((int64_t)it.len - it.rows + last, (int64_t)-1);
+  p.lo = (int64_t)it.len - it.rows + (int)((uint32_t)(it.tile * size) / (uint32_t)G);
   p.units = (int)((p.hi + 32) >> 5);
-  const int even = (int)((uint32_t)(p.units + S - 1) / (uint32_t)S);
-  p.per_split = max((even + kWaves - 1) / kWaves * kWaves, kWaves);
   return p;
 }
 
@@ -116,7 +205,7 @@ struct Unit {
   static constexpr int JC = FMT == MOE_FMT_NVFP4 ? D / 16 : D / 16 / NC;
   static constexpr int NS = FMT == MOE_FMT_BF16 ? 1 : FMT == MOE_FMT_Q8_0 ? NC : 1;
   uint32_t k[2][W], v[2][W];
-  uint32_t ks[2][NC];      // scales of a key chunk: one or two E4M3 bytes, or an fp16
+  uint16_t ks[2][NC];      // scales of a key chunk: one or two E4M3 bytes, or an fp16
   uint32_t vs[2][NS][2];   // of the 4 tokens: E4M3 bytes in [0], or 4 fp16 for each chunk
 
   // First key element of step s (8 elements) of group g.
@@ -199,17 +288,28 @@ struct Unit {
 #endif
   }
 
+  // A key scale as a word.  Widened where it is used: beside its load, where the
+  // compiler would put that, it would wait for a prefetch in the midst of a unit
+  // (8 slots at 8 K tokens 17.2 us, with that 17.9).
+  __device__ __forceinline__ uint32_t key_scale(int t, int i) const {
+    uint16_t b = ks[t][i];
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm("" : "+v"(b));
+#endif
+    return b;
+  }
+
   // Key fragment s (8 elements of the lane's) of tile t, as 4 words.
   __device__ __forceinline__ v4u key(int t, int s) const {
     v4u r;
     const int i = s * 8 / EK;
     if constexpr (FMT == MOE_FMT_NVFP4) {
-      const v2h sp = fp8_pair(ks[t][i], 0);
+      const v2h sp = fp8_pair(key_scale(t, i), 0);
       const v2h sc = (s * 8 % EK) / 16 ? v2h{sp.y, sp.y} : v2h{sp.x, sp.x};
 #pragma unroll
       for (int q = 0; q < 4; ++q) r[q] = bits(fp4_pair(k[t][s], q) * sc);
     } else if constexpr (FMT == MOE_FMT_Q8_0) {
-      const v2h sp = halves(ks[t][i]);
+      const v2h sp = halves(key_scale(t, i));
       const v2h sc = {sp.x, sp.x};
 #pragma unroll
       for (int q = 0; q < 4; ++q) r[q] = bits(i8_pair(k[t][2 * s + (q >> 1)] ^ 0x80808080u, q & 1) * sc);
@@ -220,8 +320,8 @@ struct Unit {
     return r;
   }
 
-  // Value fragment j: tokens 4g.. of tile 0, then of tile 1 (the order of the
-  // score accumulators).
+  // Value fragment j of the block formats: tokens 4g.. of tile 0, then of tile 1
+  // (the order of the score accumulators).
   __device__ __forceinline__ v4u value(int j) const {
     v4u r;
 #pragma unroll
@@ -242,8 +342,6 @@ struct Unit {
           r[2 * t + h] = bits(fp4_pair(w, (j & 7) >> 1) * fp8_pair(vs[t][0][0], h));
         } else if constexpr (FMT == MOE_FMT_Q8_0) {
           r[2 * t + h] = bits(i8_pair(v[t][j] ^ 0x80808080u, h) * halves(vs[t][j / JC][h]));
-        } else {
-          r[2 * t + h] = v[t][2 * j + h];
         }
       }
     }
@@ -316,6 +414,24 @@ __device__ __forceinline__ v4f mma(v4u a, v4u b, v4f c) {
                                                   __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
+// o + value fragment j times the weights p.  16-bit values come as the operands of
+// two products of one tile of 16 tokens each, as they were loaded: put together
+// for one product of both, they were copied where they arrive, which waits for
+// every prefetch (8 slots of 16 K tokens 50 us, with that 74).
+template <int FMT, int D>
+__device__ __forceinline__ v4f weighted(const Unit<FMT, D>& c, int j, v4u p, v4f o) {
+  if constexpr (FMT == MOE_FMT_BF16) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      o = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+          __builtin_bit_cast(v4s, v2u{c.v[t][2 * j], c.v[t][2 * j + 1]}),
+          __builtin_bit_cast(v4s, v2u{p[2 * t], p[2 * t + 1]}), o, 0, 0, 0);
+    return o;
+  } else {
+    return mma<FMT>(c.value(j), p, o);
+  }
+}
+
 // Two softmax weights as a pair of the product's operand type, rounded to
 // nearest even (half a step of weights between 0 and 2^kGrow), and their sum
 // added to l: of the rounded weights, so that rounding does not shift the mean.
@@ -385,9 +501,8 @@ struct Carry {
   __device__ __forceinline__ void gather(const Unit<FMT, D>& c, const v4u (&p)[NT]) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const v4u v = c.value(j);
 #pragma unroll
-      for (int r = 0; r < NT; ++r) o[r][j] = mma<FMT>(v, p[r], o[r][j]);
+      for (int r = 0; r < NT; ++r) o[r][j] = weighted(c, j, p[r], o[r][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -460,7 +575,7 @@ struct Carry {
       seen.cut(k + 1, g);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const v4f add = mma<FMT>(seen.value(j), p, v4f{0.f, 0.f, 0.f, 0.f});
+        const v4f add = weighted(seen, j, p, v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (mine) out[Unit<FMT, D>::value_dim(4 * g + i, j)] += add[i];
@@ -504,30 +619,24 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
   __shared__ float m_s[kWaves][16], l_s[kWaves][16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
-  uint32_t id = blockIdx.x;
-  const int sp = (int)(id % a.S); id /= a.S;
-  const int kvh = (int)(id % a.n_kv); id /= a.n_kv;
-  const int zt = (int)(id % a.ztiles);
-  const int b = (int)(id / a.ztiles);  // (scalar arithmetic all along)
-
-  const int r0 = a.s.row_start[b], len = a.s.kv_len[b];
-  const int rows = (int)min((int64_t)a.s.row_start[b + 1] - r0, (int64_t)INT32_MAX);
-  if (r0 < 0 || r0 >= a.T || rows <= 0) return;
-  const int inside = (int)min((int64_t)rows, a.T - r0);  // (inside * G is below 2^31)
+  const Item it = find_item(a.s, a.T, a.G, 16 * NT, a.n_kv, a.room, a.S, (int)blockIdx.x);
+  if (it.b < 0) return;
+  const int b = it.b, r0 = it.r0, rows = it.rows, len = it.len, inside = it.inside, tile = it.tile;
+  const int kvh = it.kvh, sp = it.sp;
   const int P = 1 << a.s.log2P;
   const KvLayout lay = kv_layout(FMT, D, P);
   const size_t page_bytes = (size_t)a.n_kv * lay.head;
   const uint8_t* heads = a.pool + (size_t)kvh * lay.head;
   const typename Unit<FMT, D>::Lane at(n, g, P);
-
-  for (int tile = zt; tile * (16 * NT) < inside * a.G; tile += a.ztiles) {
-    const TilePlan plan = tile_plan(len, rows, inside, a.G, tile, 16 * NT, a.S);
-    const int u_begin = sp * plan.per_split, u_end = min(plan.units, u_begin + plan.per_split);
+  {
+    const TilePlan plan = tile_plan(it, a.G, 16 * NT);
+    const int u_begin = sp > 0 ? sp * it.chunk : 0;
+    const int u_end = min((int64_t)plan.units, (int64_t)u_begin + it.chunk);
     if (sp > 0 && u_begin >= u_end) {  // (split 0 also answers rows that see nothing)
       const int rr = tile * (16 * NT) + threadIdx.x, i = (int)((uint32_t)rr / (uint32_t)a.G);
       if (threadIdx.x < 16 * NT && rr < inside * a.G)
         a.part_ml[((int64_t)(r0 + i) * a.n_q + kvh * a.G + rr - i * a.G) * a.S + sp] = make_float2(kNone, 0.0f);
-      continue;
+      return;
     }
 
     Unit<FMT, D> c;
@@ -542,14 +651,6 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
     const auto block = [&](int page) {  // page 0 stands in for one that is not there
       return heads + (size_t)((unsigned)page < (unsigned)a.s.n_pages ? page : 0) * page_bytes;
     };
-    int u = u_begin + wave, page = 0, next = 0;
-    if (u < u_end) {
-      page = page_at(u);
-      next = page_at(min(u + kWaves, u_end - 1));
-      c.load_keys(block(page), lay, lay.head, (u * 32) & (P - 1), at);
-      c.load_values(block(page), lay, lay.head, P, (u * 32) & (P - 1), at);
-    }
-
     // this lane's query rows, their last visible tokens and their fragments
     Carry<FMT, D, NT> w;
 #pragma unroll
@@ -562,6 +663,19 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
       w.qs[t] = a.scale_log2;
 #pragma unroll
       for (int s = 0; s < KS; ++s) w.qf[t][s] = *reinterpret_cast<const v4u*>(qp + Unit<FMT, D>::key_dim(s, g));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    int u = u_begin + wave, page = 0, next = 0;
+    if (u < u_end) {
+      page = page_at(u);
+      next = page_at(min(u + kWaves, u_end - 1));
+      c.load_keys(block(page), lay, lay.head, (u * 32) & (P - 1), at);
+      c.load_values(block(page), lay, lay.head, P, (u * 32) & (P - 1), at);
+    }
+
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
       if constexpr (FMT != MOE_FMT_BF16) {
         // bf16 -> fp16, scaled by the power of two that puts the row's largest
         // magnitude into [2^14, 2^15): exact for values above 2^-29 of it
@@ -584,6 +698,12 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
                            (_Float16)(__uint_as_float(w.qf[t][s][i] & 0xffff0000u) * up)};
             w.qf[t][s][i] = bits(p);
           }
+      } else {
+#if defined(__HIP_DEVICE_COMPILE__)
+        // (waited for here, not in every unit)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) asm("" : "+v"(w.qf[t][s]));
+#endif
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) w.o[t][j] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -661,7 +781,8 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
       const int rr = (tile * NT + t) * 16 + qr, i = (int)((uint32_t)rr / (uint32_t)a.G);
       const int64_t orow = r0 + i, h = kvh * a.G + rr - i * a.G;
       if (rr >= inside * a.G) continue;
-      if (a.S == 1) {
+      if (d0 == 0 && sp == 0 && a.S > 1) a.part_n[orow * a.n_q + h] = it.splits;
+      if (it.splits == 1) {
         const float inv = (int64_t)len - rows + i < 0 ? 0.0f : a.v_ts / L;
 #pragma unroll
         for (int j = 0; j < E; ++j) acc[j] *= inv;
@@ -680,9 +801,8 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
 
 // Joins the splits of EL elements of one (row, head): weights exp2(m_s - M),
 // added in a fixed order, so the result does not depend on scheduling.  EL / 4
-// lanes hold the elements and 1024 / EL groups of them the splits, at most PER
-// each, and a split without units says so itself: all loads are on their way at
-// once, beside the search for the row's sequence.
+// lanes hold the elements and 1024 / EL groups of them the splits, PER at a time
+// each; the loads of as many as are likely start before their number is known.
 constexpr int kMaxSplit = 256;
 
 template <int D, int EL, int PER>
@@ -695,36 +815,52 @@ __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
   const int t = (int)(id / (uint32_t)a.n_q), h = (int)(id % (uint32_t)a.n_q);
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int64_t at = ((int64_t)t * a.n_q + h) * a.S;
+  // (a row outside the sequences has no number there: whatever it reads is not used)
+  const int ns = min(a.part_n[(int64_t)t * a.n_q + h], a.S);
   float2 ml[PER];
   float4 v[PER];
-  float M = kNone, L = 0.0f;
+  const auto load = [&](int i, int s) {
+    ml[i] = a.part_ml[at + s];
+    v[i] = *reinterpret_cast<const float4*>(a.part_o + (at + s) * D + 4 * x);
+  };
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int s = grp + NG * i;
-    ml[i] = make_float2(kNone, 0.0f);
-    if (s < a.S) {
-      ml[i] = a.part_ml[at + s];
-      v[i] = *reinterpret_cast<const float4*>(a.part_o + (at + s) * D + 4 * x);
+  for (int i = 0; i < PER; ++i)
+    if (grp + NG * i < a.likely) load(i, grp + NG * i);
+  const RowSeq q = find_row(a.s, t);
+  if (q.b < 0 || ns == 1) return;
+  float M = kNone, L = 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = grp; s0 < ns; s0 += NG * PER) {
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int s = s0 + NG * i;
+      if (s >= ns) ml[i] = make_float2(kNone, 0.0f);
+      else if (s >= a.likely || s0 != grp) load(i, s);
+      top = fmaxf(top, ml[i].x);
+    }
+    const float down = __builtin_amdgcn_exp2f(M - top);
+    o.x *= down; o.y *= down; o.z *= down; o.w *= down;
+    L *= down;
+    M = top;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (ml[i].x == kNone && ml[i].y == 0.0f) continue;  // nothing there
+      const float f = __builtin_amdgcn_exp2f(ml[i].x - M);
+      o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
+      L += f * ml[i].y;
     }
   }
-  const RowSeq q = find_row(a.s, t);
-  if (q.b < 0) return;
+  float all = M;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) M = fmaxf(M, ml[i].x);
-#pragma unroll
-  for (int d = LW; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
-  if (lane == 0) l_s[wave] = M;
+  for (int d = LW; d < 64; d <<= 1) all = fmaxf(all, __shfl_xor(all, d));
+  if (lane == 0) l_s[wave] = all;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) M = fmaxf(M, l_s[i]);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (ml[i].x == kNone && ml[i].y == 0.0f) continue;  // nothing there
-    const float f = __builtin_amdgcn_exp2f(ml[i].x - M);
-    o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
-    L += f * ml[i].y;
-  }
+  for (int i = 0; i < 4; ++i) all = fmaxf(all, l_s[i]);
+  const float down = __builtin_amdgcn_exp2f(M - all);
+  o.x *= down; o.y *= down; o.z *= down; o.w *= down;
+  L *= down;
 #pragma unroll
   for (int d = LW; d < 64; d <<= 1) {
     o.x += __shfl_xor(o.x, d); o.y += __shfl_xor(o.y, d);
@@ -752,48 +888,53 @@ __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
   }
 }
 
-// Up to 32 splits a whole head in one workgroup; more, 32 elements in each.
+// Up to 32 likely splits a whole head in one workgroup (32 rows with 16 splits:
+// 4.0 us, with 32 elements in each 9.4); more, 32 elements in each.
 template <int D>
 void launch_join(const DecodeArgs& a, hipStream_t stream) {
   const unsigned heads = (unsigned)(a.T * a.n_q);
-  if (a.S <= 32) k_attn_join<D, D, 32 * D / 1024><<<heads, 256, 0, stream>>>(a);
-  else if (a.S <= 64) k_attn_join<D, 32, 2><<<heads * (D / 32), 256, 0, stream>>>(a);
+  if (a.likely <= 32) k_attn_join<D, D, 32 * D / 1024><<<heads, 256, 0, stream>>>(a);
+  else if (a.likely <= 64) k_attn_join<D, 32, 2><<<heads * (D / 32), 256, 0, stream>>>(a);
   else k_attn_join<D, 32, kMaxSplit / 32><<<heads * (D / 32), 256, 0, stream>>>(a);
 }
 
-// Launch shape: query rows of a tile, tiles side by side for a sequence (more
-// are taken in turn), splits of a sequence's cache.
+// Launch shape: query rows of a tile, splits there is room for in the workspace
+// (1: no split), and for each key/value head chunks and items (the grid).
 struct Shape {
-  int tile, ztiles, S;
+  int tile, S, room, likely;
+  int64_t items;
 };
-// Split rule, measured on one MI355X with 32 query and 4 key/value heads of 128
-// (us, graph replay, NVFP4 unless said otherwise):
+// Measured on one MI355X with 32 query and 4 key/value heads of 128 (us, graph
+// replay, NVFP4 unless said otherwise):
 //   - 16 query rows to a tile, 32 when a sequence has more (the cache is read
-//     once for them: 4 rows of 8 slots at 16 K tokens 30 against 38);
+//     once for them: 4 rows of 8 slots at 16 K tokens 29 against 34);
 //   - up to 12 units (384 tokens) no split, so no joining launch: 300 tokens 7.2
-//     against 8.3, but 700 tokens 9.4 against 8.3;
-//   - splits of at least 4 units for each wave (8 slots at 8 K tokens 17.7, at
-//     one unit 20), unless workgroups for 192 CUs need shorter ones (one slot at
-//     700 tokens);
-//   - at most 4 workgroups a CU where the registers allow them (8 slots at 28 K
-//     tokens 32, with 2 a CU 35, with 1 46), 2 for the wider formats, which have
-//     enough bytes on their way with those (Q8_0, 8 x 16 K: 32, with 3 35; bf16
-//     75, with 4 92).
+//     against 8.8, but 700 tokens 9.2 against 8.8; nor with 97 workgroups or more
+//     that have up to 31 units each (32 slots of 700 tokens 10.5 against 12.5);
+//   - chunks of at least 4 units for each wave (64 slots of 500 tokens 9.6, at
+//     one unit 16.5; 8 slots at 8 K tokens 16.4 and 17.5), unless the CUs need
+//     shorter ones (8 slots of 2000 tokens 10.8, for 192 workgroups 11.5);
+//   - at most 4 workgroups a CU where the registers allow them (1000 to 60000
+//     tokens 33, with 3 a CU 36, with 2 38; equal lengths do not tell them apart),
+//     2 for the wider formats, which have enough bytes on their way with those
+//     (Q8_0, 8 x 16 K: 32, with 3 35; bf16 49 and 53), and for 32 rows (29 and 31).
 Shape shape_of(int fmt, int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) {
   const int G = n_q / n_kv;
-  const int64_t per_seq = (T + n_seq - 1) / n_seq;
+  const int64_t per_seq = (T + n_seq - 1) / n_seq, units = (max_len + 31) / 32;
   Shape r;
   r.tile = per_seq * G > 16 && D <= 128 ? 32 : 16;
-  r.ztiles = (int)((per_seq * G + r.tile - 1) / r.tile);
-  const int64_t base = (int64_t)n_seq * n_kv * r.ztiles, units = (max_len + 31) / 32;
-  const int per_cu = fmt == MOE_FMT_NVFP4 && r.tile == 16 && D <= 128 ? 4 : 2;
-  int64_t S = units / (4 * kWaves);
-  if (S < 192 / base) S = 192 / base;
-  if (S > 256 * per_cu / base) S = 256 * per_cu / base;
-  const int64_t most = (units + kWaves - 1) / kWaves;
-  if (S > most) S = most;
-  if (S > kMaxSplit) S = kMaxSplit;
-  r.S = S < 1 || units <= 3 * kWaves ? 1 : (int)S;
+  const int64_t tiles = T * G / r.tile + n_seq;  // at most: one part tile a sequence
+  const int64_t base = (int64_t)n_seq * n_kv * ((per_seq * G + r.tile - 1) / r.tile);
+  const int target = 256 * (fmt == MOE_FMT_NVFP4 && r.tile == 16 && D <= 128 ? 4 : 2);
+  r.likely = (int)std::min(std::max(units / kWhole, 192 / base), target / base);
+  // a single sequence may take all chunks; 64 MB of partial sums, but 8 chunks
+  int64_t S = std::max((int64_t)8, (64 << 20) / (T * n_q * D * 4));
+  S = std::min({S, (int64_t)kMaxSplit, (units + kWaves - 1) / kWaves});
+  r.S = r.likely <= 1 || units <= 3 * kWaves ? 1 : (int)S;
+  const int64_t fine = std::max((int64_t)256 / n_kv, tiles * ((units + kWhole - 1) / kWhole));
+  r.likely = std::min(r.likely, r.S);
+  r.room = (int)std::max((int64_t)1, std::min({(int64_t)target / n_kv, fine, tiles * r.S}));
+  r.items = tiles + (r.S > 1 ? r.room + 1 : 0);
   return r;
 }
 
@@ -814,7 +955,8 @@ size_t attn_decode_ws_bytes(int fmt, int n_kv, int D, int n_q, int n_seq, int64_
   const Shape sp = shape_of(fmt, D, n_kv, n_q, n_seq, T, max_len);
   if (sp.S == 1) return 0;
   const size_t n = (size_t)T * n_q * sp.S;
-  return align_up(n * D * sizeof(float)) + align_up(n * sizeof(float2));
+  return align_up(n * D * sizeof(float)) + align_up(n * sizeof(float2)) +
+         align_up((size_t)T * n_q * sizeof(int));
 }
 
 hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int n_q,
@@ -826,12 +968,13 @@ hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int
   while ((1 << l2) < c->page_tokens) ++l2;
   const bool fp4 = c->fmt == MOE_FMT_NVFP4;
   const size_t n = (size_t)T * n_q * sp.S;
-  DecodeArgs a{(const uint8_t*)c->pool, q, out, (float*)ws,
-               (float2*)((char*)ws + align_up(n * c->D * sizeof(float))), q_stride, out_stride, T,
+  char* const ml = (char*)ws + align_up(n * c->D * sizeof(float));
+  DecodeArgs a{(const uint8_t*)c->pool, q, out, (float*)ws, (float2*)ml,
+               (int*)(ml + align_up(n * sizeof(float2))), q_stride, out_stride, T,
                SeqView{s->row_start, s->kv_len, s->page_table, s->n_seq, s->max_pages, c->n_pages, l2},
-               n_q, c->n_kv, n_q / c->n_kv, sp.S, sp.ztiles,
+               n_q, c->n_kv, n_q / c->n_kv, sp.S, sp.room, sp.likely,
                scale * 1.4426950408889634f * (fp4 ? c->k_scale : 1.0f), fp4 ? c->v_scale : 1.0f};
-  const unsigned grid = (unsigned)((int64_t)sp.S * c->n_kv * sp.ztiles * s->n_seq);
+  const unsigned grid = (unsigned)(sp.items * c->n_kv);
   switch (c->fmt) {
     case MOE_FMT_NVFP4: launch_decode<MOE_FMT_NVFP4>(a, c->D, sp.tile, grid, stream); break;
     case MOE_FMT_Q8_0: launch_decode<MOE_FMT_Q8_0>(a, c->D, sp.tile, grid, stream); break;

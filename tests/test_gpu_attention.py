@@ -148,6 +148,25 @@ def test_decode_matches_reference(case):
         check_decode(s, n_kv * G, qv, run_decode(s, n_kv * G, qv, max_len=m))
 
 
+@pytest.mark.parametrize("fmt,n_kv,G,D,P,lens,rows", [
+    (NVFP4, 1, 8, 128, 32, [2500, 3, 0, 700, 33, 1500], [1, 1, 1, 0, 1, 3]),
+    (Q8_0, 2, 4, 64, 64, [1, 2049, 500, 64, 0, 1100], [2, 9, 0, 1, 1, 1]),
+    (BF16, 1, 2, 256, 32, [1200, 31, 1000], [1, 12, 1]),
+    (Q8_0, 1, 2, 64, 32, [1 + (37 * b) % 90 for b in range(75)] + [1500, 2, 900], [b % 3 for b in range(78)]),
+], ids=["nvfp4", "q8_0", "bf16", "78 sequences"])
+def test_decode_split_over_sequences_of_different_lengths(fmt, n_kv, G, D, P, lens, rows):
+    """The same chunks for all sequences, whatever the longest cache is said to be
+    (too short, right, far too long): same answers."""
+    print("ragged", FMT[fmt], len(lens), flush=True)
+    s = Setup(fmt, n_kv, D, P, lens, rows, seed=len(lens), k_ts=0.75, v_ts=1.3)
+    qv = ref.bf16_bits(1.5 * s.rng.standard_normal((s.T, n_kv * G * D)))
+    for m in (None, 32, 500, 1 << 20):
+        print("  max_len", m, flush=True)
+        got = run_decode(s, n_kv * G, qv, max_len=m)
+        check_decode(s, n_kv * G, qv, got)
+        assert (got[int(s.start[-1]):] == ref.bf16_bits([7.0])[0]).all(), "rows behind the last sequence"
+
+
 @pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
 def test_decode_many_rows_empty_rows_and_strides(fmt):
     """Rows before a sequence's first token (fewer tokens than rows) give zero,
