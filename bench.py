@@ -98,15 +98,16 @@ def progress(msg):
 
 
 def sources_digest():
-    """sha256 over the library's kernel sources with comments and blank space
-    removed: counter readings are only used while the code they were taken on
-    is unchanged (a comment edit keeps them)."""
+    """sha256 over the sources of the expert-FFN kernels (the ones the counter
+    summaries are of) with comments and blank space removed: counter readings
+    are only used while the code they were taken on is unchanged (a comment
+    edit keeps them)."""
     import hashlib
     import re
     d = os.path.join(ROOT, "quantized_expert_ffn_router_amd", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(d)):
-        if f.endswith((".hip", ".h")):
+        if f.endswith((".hip", ".h")) and f.startswith(("common", "ffn_", "gate_", "gemv_", "iq")):
             with open(os.path.join(d, f), encoding="utf-8") as fh:
                 code = fh.read()
             code = re.sub(r"/\*.*?\*/", " ", code, flags=re.S)
