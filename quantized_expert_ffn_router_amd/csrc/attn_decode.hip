@@ -12,6 +12,11 @@
 // fragment of the second when V's fragment lists its tokens in the same order:
 // the softmax weights go from one product to the next without leaving their
 // lanes, and a row's maximum needs two lane swaps.
+//
+// Measured on one MI355X, both launches, 32 query and 4 key/value heads of 128:
+// 8 slots of 16 K tokens in bf16 49 us (5.4 TB/s of cache, a large copy's rate), in
+// Q8_0 32 us (4.4 TB/s), in NVFP4 one slot of 262144 tokens 33.5 us (4.5 TB/s); there
+// decoding keeps the vector units busy beside the loads.
 #include <type_traits>
 
 #include <algorithm>
@@ -920,7 +925,8 @@ struct Shape {
 //     (Q8_0, 8 x 16 K: 32, with 3 35; bf16 49 and 53), and for 32 rows (29 and 31).
 Shape shape_of(int fmt, int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) {
   const int G = n_q / n_kv;
-  const int64_t per_seq = (T + n_seq - 1) / n_seq, units = (max_len + 31) / 32;
+  const int64_t per_seq = (T + n_seq - 1) / n_seq;
+  const int64_t units = (std::min(max_len, (int64_t)INT32_MAX) + 31) / 32;  // (lengths are 32-bit)
   Shape r;
   r.tile = per_seq * G > 16 && D <= 128 ? 32 : 16;
   const int64_t tiles = T * G / r.tile + n_seq;  // at most: one part tile a sequence

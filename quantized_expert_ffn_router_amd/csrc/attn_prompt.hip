@@ -11,6 +11,13 @@
 // per tile), and the score accumulators, rounded to bf16, are the operand of
 // the second product as they lie; V's fragments come out of LDS transposed
 // (ds_read_b64_tr_b16) with their tokens in the same order.
+//
+// Bound by the matrix units at the clock they hold under load: 8192 rows behind
+// 8192 keys (32 heads of 128) 1364 us, 1.21 PFLOP/s of visible pairs, where a large
+// bf16 library product reaches 1.17.  16384 rows of nine prompts of 630 to 3150
+// rows: 345 us, 0.89; there every tile's start, the part of its last keys that is
+// masked, and the output weigh more.  333 rows take 14 us: six tiles of keys one
+// after the other, 1.1 us each, on a card that is mostly empty.
 #include "attn_common.h"
 
 namespace moe {
