@@ -13,6 +13,13 @@
 
 namespace moe {
 
+// Two values as bf16, rounded to nearest even.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  const v2b r = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
 // Byte offsets inside one (page, head) block; head = bytes of the block.
 struct KvLayout {
   uint32_t ks, vq, vs, head;

@@ -592,15 +592,10 @@ struct Carry {
 
 template <int N>
 __device__ __forceinline__ void store_row(uint16_t* d, const float (&v)[N]) {
-  uint32_t w[N < 2 ? 1 : N / 2];
-  if constexpr (N == 1) {
-    *d = f32_to_bf16_rne(v[0]);
-    return;
-  }
+  uint32_t w[N / 2];
 #pragma unroll
   for (int j = 0; j < N / 2; ++j)
-    w[j] = (uint32_t)f32_to_bf16_rne(v[2 * j]) | ((uint32_t)f32_to_bf16_rne(v[2 * j + 1]) << 16);
-  if constexpr (N == 2) *reinterpret_cast<uint32_t*>(d) = w[0];
+    w[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
   if constexpr (N == 4) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
   if constexpr (N >= 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
   if constexpr (N == 16) *reinterpret_cast<uint4*>(d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -888,8 +883,7 @@ __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
     const float inv = (int64_t)q.len - q.rows + (t - q.r0) < 0 ? 0.0f : a.v_ts / L;
     uint16_t* d = a.out + t * a.out_stride + (int64_t)h * D + 4 * x;
     *reinterpret_cast<uint2*>(d) =
-        make_uint2((uint32_t)f32_to_bf16_rne(o.x * inv) | ((uint32_t)f32_to_bf16_rne(o.y * inv) << 16),
-                   (uint32_t)f32_to_bf16_rne(o.z * inv) | ((uint32_t)f32_to_bf16_rne(o.w * inv) << 16));
+        make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
   }
 }
 

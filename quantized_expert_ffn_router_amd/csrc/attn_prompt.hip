@@ -214,6 +214,8 @@ struct Rows {
   // the softmax in its shadow, and fragments read kAhead steps early.  A weight
   // is ready when its step of the second product begins: 20 of a lane's 32 go
   // with the first product, the rest with the first three quarters of the second.
+  // NEXT false: there is no next tile, only the weighted values.
+  template <bool NEXT>
   __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, float c,
                                        v16f (&x)[2], v16f (&y)[2]) {
     constexpr int N1 = 2 * KS, N2 = 4 * NJ, kAhead = 3, kRing = 4;
@@ -224,10 +226,15 @@ struct Rows {
     const auto weights_by = [](int i) {
       return i < 0 ? 0 : i < N1 ? 20 * (i + 1) / N1 : min(32, 20 + 12 * (i - N1 + 1) / (3 * NJ));
     };
+    constexpr int I0 = NEXT ? 0 : N1;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) f[i] = fragment(i);
+    for (int i = I0; i < I0 + kAhead; ++i) f[i % kRing] = fragment(i);
+    if constexpr (!NEXT) {
 #pragma unroll
-    for (int i = 0; i < N1 + N2; ++i) {
+      for (int v = 0; v < weights_by(N1 - 1); ++v) weight(x, c, p, v);
+    }
+#pragma unroll
+    for (int i = I0; i < N1 + N2; ++i) {
       if (i + kAhead < N1 + N2) f[(i + kAhead) % kRing] = fragment(i + kAhead);
       if (i < N1) {
         v16f zero;
@@ -358,22 +365,21 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
     s0 = a.kv_start[i]; s1 = a.kv_start[i + 1];
     const int64_t n = (int64_t)q1 - q0;
     sum = i0 + lane < a.n_seq && n > 0 ? (int)((n + BM - 1) / BM) : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
+    for (int d = 1; d < 64 && d < a.n_seq; d <<= 1) {
       const int v = __shfl_up(sum, d);
       if (lane >= d) sum += v;
     }
   };
   for (int i0 = 0; i0 < a.n_seq; i0 += 64) {
     round(i0);
-    total += __builtin_amdgcn_readlane(sum, 63);
+    total += __builtin_amdgcn_readlane(sum, min(63, a.n_seq - 1 - i0));
   }
   const int want = total - 1 - slot;
   if (want < 0) return;
   if (a.n_seq > 64) {
     for (;; first += 64) {
       round(first);
-      const int all = __builtin_amdgcn_readlane(sum, 63);
+      const int all = __builtin_amdgcn_readlane(sum, min(63, a.n_seq - 1 - first));
       if (before + all > want) break;
       before += all;
     }
@@ -434,20 +440,22 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
     const auto step = [&](int it, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1) {
       arrive(it, k0, v1);
       v16f y[2];
-      w.step(k1, v0, a.c, x, y);
+      w.template step<true>(k1, v0, a.c, x, y);
       x[0] = y[0];
       x[1] = y[1];
     };
     // Tiles that not every row sees: a wave leaves out those none of its rows
-    // does.  (After the last tile K's buffer holds no next one: those scores are
-    // masked whatever they are.)
+    // does, and the scores of the one after its last.
     const int last = __builtin_amdgcn_readfirstlane(hi_wave < 0 ? -1 : (int)(hi_wave / kBN));
     const auto edge_step = [&](int it, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1) {
       arrive(it, k0, v1);
       if (it > last) return;
       v16f y[2];
-      w.step(k1, v0, a.c, x, y);
-      w.mask(y, (int64_t)(it + 1) * kBN);
+      if (it < last) {
+        w.scores(k1, y);
+        w.mask(y, (int64_t)(it + 1) * kBN);
+      }
+      w.template step<false>(k1, v0, a.c, x, y);
       x[0] = y[0];
       x[1] = y[1];
     };
@@ -475,15 +483,19 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
   }
   if (!live) return;
   const float inv = !keys ? __uint_as_float(0x7fc00000u) : w.limit < 0 ? 0.0f : 1.0f / w.l;
-  uint16_t* d = a.out + (r0 + i_row) * a.out_stride + (int64_t)head * D + 4 * h;
+  // A lane holds 4 of every 8 elements, its partner in the other half of the wave
+  // the other 4: one swap of two pieces gives each 8 in a row, for one store.
+  uint16_t* d = a.out + (r0 + i_row) * a.out_stride + (int64_t)head * D + 8 * h;
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
+    for (int i = 0; i < 16; i += 8) {
       const v16f& o = w.o[j];
-      const uint32_t w0 = (uint32_t)f32_to_bf16_rne(o[i] * inv) | ((uint32_t)f32_to_bf16_rne(o[i + 1] * inv) << 16);
-      const uint32_t w1 = (uint32_t)f32_to_bf16_rne(o[i + 2] * inv) | ((uint32_t)f32_to_bf16_rne(o[i + 3] * inv) << 16);
-      *reinterpret_cast<uint2*>(d + 32 * j + 2 * i) = make_uint2(w0, w1);
+      const auto lo = __builtin_amdgcn_permlane32_swap(bf16_pair(o[i] * inv, o[i + 1] * inv),
+                                                       bf16_pair(o[i + 4] * inv, o[i + 5] * inv), false, false);
+      const auto hi = __builtin_amdgcn_permlane32_swap(bf16_pair(o[i + 2] * inv, o[i + 3] * inv),
+                                                       bf16_pair(o[i + 6] * inv, o[i + 7] * inv), false, false);
+      *reinterpret_cast<uint4*>(d + 32 * j + 2 * i) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
     }
 }
 

@@ -24,13 +24,6 @@ __device__ __forceinline__ void wave_lds_fence() {
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Two values as bf16, rounded to nearest even.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
-  const v2b r = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, r);
-}
-
 // Sum over groups of N lanes (8, 16 or 32): within a row of 16 by lane
 // permutations of the adder's operand.
 template <int CTRL>
