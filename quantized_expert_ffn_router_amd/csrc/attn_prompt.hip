@@ -13,10 +13,10 @@
 // (ds_read_b64_tr_b16) with their tokens in the same order.
 //
 // Bound by the matrix units at the clock they hold under load: 8192 rows behind
-// 8192 keys (32 heads of 128) 1364 us, 1.21 PFLOP/s of visible pairs, where a large
+// 8192 keys (32 heads of 128) 1350 us, 1.22 PFLOP/s of visible pairs, where a large
 // bf16 library product reaches 1.17.  16384 rows of nine prompts of 630 to 3150
-// rows: 345 us, 0.89; there every tile's start, the part of its last keys that is
-// masked, and the output weigh more.  333 rows take 14 us: six tiles of keys one
+// rows: 325 us, 0.94; there every tile's start, the part of its last keys that is
+// masked, and the output weigh more.  333 rows take 12 us: six tiles of keys one
 // after the other, 1.1 us each, on a card that is mostly empty.
 #include "attn_common.h"
 
@@ -334,7 +334,9 @@ __device__ __forceinline__ void careful_pass(Rows<D>& w, uint8_t* kt, uint8_t* v
 //
 // Scores of the next tile are computed while the present one's go through the
 // exponential: the two share nothing, so matrix and vector instructions fill
-// one another's gaps within a wave.
+// one another's gaps within a wave.  Not so for the tiles that a row sees in part:
+// there the code would be twice as long and need more registers than there are
+// (nine prompts 337 us, so 393).
 constexpr float kFar = 18446744073709551616.0f;  // 2^64
 
 template <int D, int WAVES>
@@ -516,14 +518,14 @@ hipError_t launch_attn_prompt(int n_q, int n_kv, int D, int n_seq, const int32_t
   const PromptArgs a{q_start, kv_start ? kv_start : q_start, q, k, v, out, q_stride, k_stride,
                      v_stride, out_stride, T, Tk, n_q, n_q / n_kv, n_seq,
                      scale * 1.4426950408889634f};
-  // 128 rows a workgroup, two workgroups a CU: the best or within 3 % of it from
-  // 100 rows on (one MI355X, 32 heads of 128: 2048 rows 51 us, with 256 rows a
-  // workgroup 58, with 64 rows 52; 8192 rows 489, 483 and 601).  For long
-  // sequences 256 rows, which read every key half as often: 8192 rows behind
-  // 8192 keys 1356 us against 1411.
+  // 128 rows a workgroup, two workgroups a CU: the best or within 4 % of it up to
+  // 2048 rows (one MI355X, 32 heads of 128: 333 rows 12.3 us, 64 rows a workgroup
+  // 11.7, 256 rows 15; 2048 rows 50, 54 and 59).  For long sequences 256 rows, which
+  // read every key half as often: 4096 rows 136 us against 150, 8192 rows behind
+  // 8192 keys 1360 against 1435.
   switch (D) {
     case 64: return launch<64, 4>(a, stream);
-    case 128: return T / n_seq >= 8192 ? launch<128, 8>(a, stream) : launch<128, 4>(a, stream);
+    case 128: return T / n_seq >= 4096 ? launch<128, 8>(a, stream) : launch<128, 4>(a, stream);
     default: return launch<256, 4>(a, stream);
   }
 }
