@@ -523,8 +523,9 @@ moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int3
  * q, out: bf16 [T] rows of n_q * D (out may be q).  max_len: the longest
  * kv_len expected; it decides how the work is split, never the result's
  * validity (0: max_pages * page_tokens).  ws: moe_attn_workspace_bytes of the
- * same arguments; nothing in it needs to start at zero.  Calls that may
- * overlap need workspaces of their own. */
+ * same cache, heads and n_seq, with this T and max_len or larger ones; nothing
+ * in it needs to start at zero.  Calls that may overlap need workspaces of
+ * their own. */
 size_t moe_attn_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_seq, int64_t T,
                                 int64_t max_len);
 moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_t n_q,

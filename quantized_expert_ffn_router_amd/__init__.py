@@ -538,6 +538,10 @@ def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: floa
     that every chunk of a prompt attends to what the cache holds."""
     c, D = cache.desc, cache.D
     qw, kw = cache.n_q * D, cache.n_kv * D
+    if T > buf.T_max:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: T={T} > T_max={buf.T_max}")
+    if prompt is not None and min(prompt[2].numel(), prompt[3].numel()) < prompt[1] * kw:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: k, v are smaller than Tk={prompt[1]} rows")
     moe_kv_append(c, cache.qkv_desc, buf.seqs, qkv, qw + 2 * kw, T, None, buf.q, qw, buf.k, kw, stream)
     if prompt is None:
         moe_attn_decode(c, buf.seqs, cache.n_q, buf.q, qw, T, max_len, scale, buf.out, qw, buf.ws,

@@ -5,6 +5,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "attn_common.h"
@@ -737,8 +738,13 @@ size_t moe_attn_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_se
     return 0;
   }
   // max_len 0 stands for the page table's capacity, which is not known here:
-  // the longest cache gives the largest split
-  return moe::attn_decode_ws_bytes(c->fmt, c->n_kv, c->D, n_q, n_seq, T, max_len ? max_len : INT32_MAX);
+  // the longest cache gives the largest split.  Fewer rows can need more (they
+  // are split finer); beyond 2^14 (row, head) pairs there are no splits.
+  size_t most = 0;
+  for (int64_t t = 1; t <= T && t * n_q <= 1 << 14; ++t)
+    most = std::max(most, moe::attn_decode_ws_bytes(c->fmt, c->n_kv, c->D, n_q, n_seq, t,
+                                                    max_len ? max_len : INT32_MAX));
+  return most;
 }
 
 moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_t n_q,

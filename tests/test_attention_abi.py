@@ -139,6 +139,32 @@ def test_workspace_grows_with_the_longest_cache_only_as_far_as_it_helps():
     assert q.moe_attn_workspace_bytes(c, 7, 1, 1, 64) == 0 and "n_q=7" in q.last_error()
 
 
+@pytest.mark.parametrize("fmt", [q.MOE_FMT_NVFP4, q.MOE_FMT_Q8_0, q.MOE_FMT_BF16])
+@pytest.mark.parametrize("n_q,n_kv,D", [(32, 4, 128), (5, 5, 64), (16, 2, 256), (1, 1, 64)])
+def test_workspace_serves_every_smaller_step(fmt, n_q, n_kv, D):
+    """Buffers made for the largest step are used for all: bytes never fall as
+    rows or the longest cache grow."""
+    c = cache(fmt=fmt, n_kv=n_kv, D=D)
+    for n_seq in (1, 8, 64, 300):
+        for longest in (300, 5000, 10 ** 5):
+            b = [q.moe_attn_workspace_bytes(c, n_q, n_seq, t, longest) for t in (*range(1, 600, 7), 5000, 60000)]
+            assert b == sorted(b), (n_seq, longest)
+        for t in (1, 9, 100, 600):
+            b = [q.moe_attn_workspace_bytes(c, n_q, n_seq, t, n) for n in (1, 384, 385, 1000, 9999, 10 ** 7, 0)]
+            assert b == sorted(b), (n_seq, t)
+
+
+def test_attention_forward_refuses_what_its_buffers_cannot_hold():
+    c = q.KvCache(NVFP4, 8, 2, 64, 32, 4, device="cpu")
+    buf = q.AttnBuffers(c, 1, 6, 2, device="cpu")
+    qkv = torch.zeros(7, 12 * 64, dtype=torch.bfloat16)
+    with pytest.raises(q.MoeError, match="T_max=6"):
+        q.attention_forward(c, buf, qkv, 7, 0.125)
+    k, v = torch.zeros(40, 128, dtype=torch.bfloat16), torch.zeros(39, 128, dtype=torch.bfloat16)
+    with pytest.raises(q.MoeError, match="Tk=40"):
+        q.attention_forward(c, buf, qkv, 6, 0.125, prompt=(buf.kv_len, 40, k, v))
+
+
 def test_rope_frequencies():
     f, s = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 64, 10000.0)
     i = np.arange(32)

@@ -644,3 +644,34 @@ def test_attention_forward_then_layer_forward():
     # a decode row's weights are fp16 and a prompt's bf16 (2^-8), the row itself
     # is rounded to bf16 a few times over in each of the two layers
     assert err < 8 * 2.0 ** -8, float(err)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+def test_buffers_for_long_prompts_serve_short_steps(fmt):
+    """A prompt of 600 rows, then steps of 2 and 24 rows over long caches, in buffers made for 600
+    rows: bit for bit what buffers of each step's own size give."""
+    n_q, n_kv, D, P, pages = 8, 2, 128, 64, 40
+    gen = torch.Generator(device=dev).manual_seed(5)
+    rope = q.moe_rope_freqs(q.MOE_ROPE_LINEAR, 64, 10000.0, 4.0)
+    table = i32(np.random.default_rng(2).permutation(2 * pages).reshape(2, pages))
+    qkv = torch.randn(600, (n_q + 2 * n_kv) * D, generator=gen, device=dev).bfloat16()
+    got = []
+    for own in (False, True):
+        cache = q.KvCache(fmt, n_q, n_kv, D, P, 2 * pages, rope=rope, interleaved=1)
+        lens, outs, big = [0, 0], [], q.AttnBuffers(cache, 2, 600, pages)
+        for rows in ([590, 10], [300, 300], [1, 1], [4, 20], [1, 1]):
+            n = sum(rows)
+            buf = q.AttnBuffers(cache, 2, n, pages) if own else big
+            lens = [a + b for a, b in zip(lens, rows)]
+            print("step", FMT[fmt], own, rows, flush=True)
+            buf.page_table.copy_(table)
+            buf.row_start.copy_(i32([0, rows[0], n]))
+            buf.kv_len.copy_(i32(lens))
+            prompt = None
+            if n > 100:
+                kv = [torch.empty(sum(lens), n_kv * D, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+                prompt = (i32([0, lens[0], sum(lens)]), sum(lens), *kv)
+            outs.append(q.attention_forward(cache, buf, qkv[:n], n, D ** -0.5, prompt)[:n].clone())
+        torch.cuda.synchronize()
+        got.append(torch.cat(outs))
+    assert torch.isfinite(got[0].float()).all() and torch.equal(got[0], got[1])
