@@ -458,6 +458,91 @@ def test_prompt_matches_reference(n_q, n_kv, D, qlen, klen):
     assert np.array_equal(run_prompt(n_q, n_kv, D, qs, ks, T, Tk, qv, kv, vv, in_place=True)[:qs[-1]], got[:qs[-1]])
 
 
+def test_prompt_many_sequences():
+    """More sequences than lanes: empty ones, and prompts on both sides of 64 and 128 of them."""
+    qlen = [(5 * b) % 7 for b in range(150)]
+    qlen[62:66], qlen[127:130] = [70, 1, 0, 131], [0, 40, 66]
+    klen = [n + (b % 3) * 40 for b, n in enumerate(qlen)]
+    rng = np.random.default_rng(3)
+    for D in (64, 128):
+        qs, ks = (np.concatenate([[0], np.cumsum(x)]).tolist() for x in (qlen, klen))
+        qv = ref.bf16_bits(1.5 * rng.standard_normal((qs[-1] + 2, 2 * D)))
+        kv, vv = (ref.bf16_bits(rng.standard_normal((ks[-1], D))) for _ in range(2))
+        print("prompt, 150 sequences", D, flush=True)
+        got = run_prompt(2, 1, D, qs, ks, qs[-1] + 2, ks[-1], qv, kv, vv)
+        check_prompt(2, 1, D, qs, ks, qv, kv, vv, got)
+        assert (got[qs[-1]:] == ref.bf16_bits([7.0])[0]).all()
+
+
+def test_prompt_long():
+    """4200 rows behind 100 cached keys, the larger tile of rows: rows at tile ends and between,
+    also with a value and a key that only later rows see being NaN."""
+    n, L, D = 4200, 4300, 128
+    rng = np.random.default_rng(4)
+    qv = ref.bf16_bits(1.5 * rng.standard_normal((n, 2 * D)))
+    kv, vv = (ref.bf16_bits(rng.standard_normal((L, D))) for _ in range(2))
+    k, v, scale = ref.bf16_val(kv), ref.bf16_val(vv), float(np.float32(D ** -0.5))
+    rows = sorted({0, 1, n - 1, n - 2} | set(range(255, n, 256)) | set(range(256, n, 256)) | set(range(31, n, 97)))
+    for bad in (None, 2999, 3000):
+        print("prompt, 4200 rows, NaN at", bad, flush=True)
+        kb, vb = kv.copy(), vv.copy()
+        if bad is not None:
+            (kb if bad % 2 else vb)[bad, 7] = 0x7fc0
+        got = run_prompt(2, 1, D, [0, n], [0, L], n, L, qv, kb, vb)
+        for i in rows + [2898, 2899, 2900, 2901]:
+            for h in range(2):
+                c, lim = slice(h * D, (h + 1) * D), L - n + i
+                have = ref.bf16_val(got[i, c])
+                if bad is not None and lim >= bad:
+                    assert np.isnan(have).all() if bad % 2 else np.isnan(have[7]), (bad, i, h)
+                    continue
+                want, pv, qk = ref.attend(ref.bf16_val(qv[i, c]), k, v, lim, scale)
+                bound = ref.attend_bound(want, pv, qk, lim + 1, 0.0, D, BF16)
+                assert (np.abs(have - want) <= bound).all(), (bad, i, h)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+def test_pages_beyond_32_bit_offsets(fmt):
+    """A pool of more than 4 GiB: tokens in its last pages as in the first pages of a small one."""
+    n_kv, D, P, n_q = 8, 256, 256, 8
+    pb = q.moe_kv_page_bytes(fmt, n_kv, D, P)
+    far = (1 << 32) // pb + 3
+    gen = torch.Generator(device=dev).manual_seed(6)
+    qkv = torch.randn(600, (n_q + 2 * n_kv) * D, generator=gen, device=dev).bfloat16()
+    got = []
+    for n_pages, pages in ((3, [2, 0, 1]), (far, [far - 1, far - 3, far - 2])):
+        print("pool", FMT[fmt], n_pages, flush=True)
+        cache = q.KvCache(fmt, n_q, n_kv, D, P, n_pages)
+        buf = q.AttnBuffers(cache, 1, 600, 3)
+        buf.page_table.copy_(i32([pages]))
+        buf.row_start.copy_(i32([0, 600]))
+        buf.kv_len.copy_(i32([600]))
+        kv = [torch.empty(600, n_kv * D, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+        one = q.attention_forward(cache, buf, qkv, 600, 1 / 16, (buf.row_start, 600, *kv)).clone()
+        buf.row_start.copy_(i32([0, 1]))
+        buf.kv_len.copy_(i32([601]))
+        two = q.attention_forward(cache, buf, qkv, 1, 1 / 16)[:1].clone()
+        torch.cuda.synchronize()
+        got.append((one, two, *kv))
+        del cache, buf
+    assert all(torch.isfinite(a.float()).all() and torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_read_many_sequences():
+    """Spans of more sequences than lanes."""
+    lens = [(3 * b) % 8 for b in range(140)]
+    lens[63], lens[64], lens[128] = 45, 0, 33
+    s = Setup(Q8_0, 1, 64, 32, lens, [0] * 140, seed=8)
+    start = np.concatenate([[0], np.cumsum(lens)])
+    ko, vo = (torch.full((int(start[-1]), 64), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    print("read, 140 sequences", flush=True)
+    q.moe_kv_read(s.cache, s.seqs, None, i32(start), int(start[-1]), ko, 64, vo, 64)
+    torch.cuda.synchronize()
+    for w, got in ((0, bits(ko)), (1, bits(vo))):
+        want = [s.ref.get(w, s.table[b, j // 32], j % 32, 0) for b, n in enumerate(lens) for j in range(n)]
+        assert np.array_equal(got, ref.bf16_bits(np.array(want, np.float64)))
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("val", [math.nan, math.inf])
 def test_prompt_unseen_tokens_have_no_influence(D, val):
