@@ -197,18 +197,24 @@ struct AppendArgs {
 // 8 elements of a head: z * w / rms(z), then the rotation of the lane's four
 // pairs: (z[i], z[i + 4]) where the lane holds both halves' elements, neighbours
 // otherwise.  T: float for queries (a few 2^-24, against the 2^-9 of the
-// rounding to bf16), double for keys.
+// rounding to bf16), double for keys.  The squares are summed in fp64 for both:
+// those of a bf16 value may lie outside fp32.
 template <int LPH, int D, typename T>
 __device__ __forceinline__ void norm_turn(T (&z)[8], const float (&w)[8], bool normed, float eps,
                                           bool halves, bool turn, const T (&cs)[8]) {
   if (normed) {
-    T ss = 0;
+    double ss = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fma(z[i], z[i], ss);
+    for (int i = 0; i < 8; ++i) ss = fma((double)z[i], (double)z[i], ss);
     ss = group_sum<LPH>(ss);
-    const T r = rsqrt(ss / (T)D + (T)eps);
+    double r = rsqrt(ss / (double)D + (double)eps);
+    if (sizeof(T) == 4 && r > 0x1p100) {  // (beyond fp32 for the smallest values)
+      r *= 0x1p-64;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = z[i] * r * (T)w[i];
+      for (int i = 0; i < 8; ++i) z[i] *= (T)0x1p64;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = z[i] * (T)r * (T)w[i];
   }
   if (turn) {
 #pragma unroll
@@ -219,6 +225,35 @@ __device__ __forceinline__ void norm_turn(T (&z)[8], const float (&w)[8], bool n
       z[halves ? i + 4 : 2 * i + 1] = nv;
     }
   }
+}
+
+// Buffer accesses of 8 bytes a lane at a byte offset: nothing happens (a load
+// gives 0) from `bytes` on.
+#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass does not know the builtins)
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+#else
+typedef const void* Rsrc;
+#endif
+__device__ __forceinline__ Rsrc buffer_of(const uint16_t* p, int bytes) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, bytes, 0x00020000);
+#else
+  return p;
+#endif
+}
+__device__ __forceinline__ uint2 load_8(Rsrc r, uint32_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+  return make_uint2(x[0], x[1]);
+#else
+  return make_uint2(0, 0);
+#endif
+}
+__device__ __forceinline__ void store_8(Rsrc r, uint32_t at, uint2 x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  __builtin_amdgcn_raw_buffer_store_b64(v2u{x.x, x.y}, r, at, 0, 0);
+#endif
 }
 
 // One wave per row, D/8 lanes per head, 64/(D/8) heads at a time: the row's
@@ -263,7 +298,8 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
     return;
   }
   const int n = lane % LPH, g = lane / LPH;
-  const int q_groups = (a.n_q + HPW - 1) / HPW, kv_groups = (a.n_kv + HPW - 1) / HPW;
+  const int n_q = __builtin_amdgcn_readfirstlane(a.n_q), n_kv = __builtin_amdgcn_readfirstlane(a.n_kv);
+  const int q_groups = (n_q + HPW - 1) / HPW, kv_groups = (n_kv + HPW - 1) / HPW;
   const int groups = q_groups + 2 * kv_groups, step = gridDim.y;
   const uint16_t* row = a.qkv + t * a.qkv_stride;
   // places of the lane's 8 elements in a query or key head: 4 pairs
@@ -275,19 +311,23 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
   const auto head_of = [&](int u) {
     const int k = u < q_groups ? u : u < q_groups + kv_groups ? u - q_groups : u - q_groups - kv_groups;
     const int h = k * HPW + g;
-    return h < (u < q_groups ? a.n_q : a.n_kv) ? h : -1;
+    return h < (u < q_groups ? n_q : n_kv) ? h : -1;
   };
+  // Buffer accesses, out of range where there is no head (or row): no access is
+  // behind a branch, which would make every wait for a load one for the stores
+  // after it, too.
+  constexpr uint32_t kNowhere = 0x80000000u;
+  const Rsrc from = buffer_of(row, mine ? (n_q + 2 * n_kv) * D * 2 : 0);
   const auto fetch = [&](int u, uint2& xa, uint2& xb) {
-    const int h = head_of(u);
-    if (h < 0) return;
+    const int h = u < groups ? head_of(u) : -1;
     const bool v = u >= q_groups + kv_groups;
-    const uint16_t* p = row + (size_t)(h + (u < q_groups ? 0 : v ? a.n_q + a.n_kv : a.n_q)) * D;
-    xa = *reinterpret_cast<const uint2*>(p + (v ? 8 * n : a0));
-    xb = *reinterpret_cast<const uint2*>(p + (v ? 8 * n + 4 : b0));
+    const uint32_t at = 2 * (h + (u < q_groups ? 0 : v ? n_q + n_kv : n_q)) * D;
+    xa = load_8(from, h < 0 ? kNowhere : at + 2 * (v ? 8 * n : a0));
+    xb = load_8(from, h < 0 ? kNowhere : at + 2 * (v ? 8 * n + 4 : b0));
   };
   int u = mine ? blockIdx.y : groups;
-  uint2 xa = make_uint2(0, 0), xb = make_uint2(0, 0);
-  if (u < groups) fetch(u, xa, xb);
+  uint2 xa, xb;
+  fetch(u, xa, xb);
 
   if constexpr (!QUADS) {
     q = find_row(a.s, t);
@@ -297,7 +337,7 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
   const int page = page_of(a.s, q.b, tok);
   const int P = 1 << a.s.log2P, o = (int)(tok & (P - 1));
   const KvLayout lay = kv_layout(FMT, D, P);
-  uint8_t* page_p = a.pool + (size_t)max(page, 0) * ((size_t)a.n_kv * lay.head);
+  uint8_t* page_p = a.pool + (size_t)max(page, 0) * ((size_t)n_kv * lay.head);
 
   const double p = (double)(a.pos && mine ? (int64_t)a.pos[t] : tok);
   for (int i = lane; i < a.rot / 2; i += 64) {
@@ -307,10 +347,18 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
   }
   wave_lds_fence();
   const auto weights = [&](const float* w, float (&out)[8]) {
-    if (!w) return;
-    const float4 wa = *reinterpret_cast<const float4*>(w + a0), wb = *reinterpret_cast<const float4*>(w + b0);
-    out[0] = wa.x; out[1] = wa.y; out[2] = wa.z; out[3] = wa.w;
-    out[4] = wb.x; out[5] = wb.y; out[6] = wb.z; out[7] = wb.w;
+    if (w) {
+      const float4 wa = *reinterpret_cast<const float4*>(w + a0), wb = *reinterpret_cast<const float4*>(w + b0);
+      out[0] = wa.x; out[1] = wa.y; out[2] = wa.z; out[3] = wa.w;
+      out[4] = wb.x; out[5] = wb.y; out[6] = wb.z; out[7] = wb.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i] = 1.0f;
+    }
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("" : "+v"(out[i]));  // (waited for here, not in every group)
+#endif
   };
   // the cache's part of a group: x, 8 consecutive elements of a lane
   const auto store = [&](int h, bool is_v, uint4 x) {
@@ -329,23 +377,23 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
         cs[2 * i + 1] = (float)c.y;
       }
     }
+    const Rsrc to = buffer_of(a.q_out + t * a.q_stride, n_q * D * 2);
     for (; u < q_groups; u += step) {
       const int h = head_of(u);
       float z[8] = {lo16(xa.x), hi16(xa.x), lo16(xa.y), hi16(xa.y),
                     lo16(xb.x), hi16(xb.x), lo16(xb.y), hi16(xb.y)};
-      if (u + step < groups) fetch(u + step, xa, xb);
+      fetch(u + step, xa, xb);
       norm_turn<LPH, D>(z, w, a.q_norm != nullptr, a.eps, split, turn, cs);
-      if (h < 0) continue;
-      uint16_t* d = a.q_out + t * a.q_stride + (size_t)h * D;
-      *reinterpret_cast<uint2*>(d + a0) = make_uint2(bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]));
-      *reinterpret_cast<uint2*>(d + b0) = make_uint2(bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7]));
+      const uint32_t at = 2 * h * D;
+      store_8(to, h < 0 ? kNowhere : at + 2 * a0, make_uint2(bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3])));
+      store_8(to, h < 0 ? kNowhere : at + 2 * b0, make_uint2(bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7])));
     }
   }
   for (; u < q_groups + kv_groups; u += step) {
     const int h = head_of(u);
     double z[8] = {lo16(xa.x), hi16(xa.x), lo16(xa.y), hi16(xa.y),
                    lo16(xb.x), hi16(xb.x), lo16(xb.y), hi16(xb.y)};
-    if (u + step < groups) fetch(u + step, xa, xb);
+    fetch(u + step, xa, xb);
     float w[8];
     double cs[8];
     weights(a.k_norm, w);
@@ -380,7 +428,7 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
     for (; u < groups; u += step) {
       const int h = head_of(u);
       const uint4 x = make_uint4(xa.x, xa.y, xb.x, xb.y);
-      if (u + step < groups) fetch(u + step, xa, xb);
+      fetch(u + step, xa, xb);
       store(h, true, x);
     }
     return;
@@ -394,7 +442,7 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
     for (; u < groups; u += step) {
       const int h = head_of(u);
       const uint4 x = make_uint4(xa.x, xa.y, xb.x, xb.y);
-      if (u + step < groups) fetch(u + step, xa, xb);
+      fetch(u + step, xa, xb);
       uint8_t* const mine_s = v_s + ((wave * HPW + g) * D + 8 * n) * VB;
       if constexpr (FMT == MOE_FMT_BF16) {
         *reinterpret_cast<uint4*>(mine_s) = x;
@@ -406,7 +454,7 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
       }
       __syncthreads();
       const int th = (u - q_groups - kv_groups) * HPW + tg;
-      if (th < a.n_kv && page >= 0) {
+      if (th < n_kv && page >= 0) {
         uint8_t* dst = page_p + (size_t)th * lay.head + lay.vq + ((o >> 2) * D + td) * 4 * VB;
         uint32_t w[4];
 #pragma unroll

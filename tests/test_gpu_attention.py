@@ -234,13 +234,14 @@ def append_inputs(s, n_q, seed):
     return ref.bf16_bits(rng.standard_normal((s.T, w)) * 2.0)
 
 
-def run_append(s, n_q, qkv, norm, rot, inter, freq, scale, pos=None, in_place=False, k_out=True):
+def run_append(s, n_q, qkv, norm, rot, inter, freq, scale, pos=None, in_place=False, k_out=True,
+               eps=1e-6):
     D = s.D
     w, kw = (n_q + 2 * s.n_kv) * D, s.n_kv * D
     x = to_dev(qkv)
     nq, nk = (torch.from_numpy(n).to(dev) if n is not None else None for n in norm)
     f = torch.from_numpy(freq).to(dev)
-    d = q.QkvDesc(n_q, 1e-6, nq.data_ptr() if nq is not None else None,
+    d = q.QkvDesc(n_q, eps, nq.data_ptr() if nq is not None else None,
                   nk.data_ptr() if nk is not None else None, rot, inter, f.data_ptr(), scale)
     p = i32(pos) if pos is not None else None
     if in_place:
@@ -257,7 +258,7 @@ def run_append(s, n_q, qkv, norm, rot, inter, freq, scale, pos=None, in_place=Fa
     return bits(qo), (bits(ko) if k_out else None), bits(x)
 
 
-def check_append(s, n_q, qkv, norm, rot, inter, freq, scale, got_q, got_k, pos=None):
+def check_append(s, n_q, qkv, norm, rot, inter, freq, scale, got_q, got_k, pos=None, eps=1e-6):
     """Updates the reference pool and compares everything."""
     D, n_kv = s.D, s.n_kv
     for b, (n, L) in enumerate(zip(s.rows, s.lens)):
@@ -267,7 +268,7 @@ def check_append(s, n_q, qkv, norm, rot, inter, freq, scale, got_q, got_k, pos=N
             for h in range(n_q + 2 * n_kv):
                 x = qkv[t, h * D:(h + 1) * D]
                 if h < n_q + n_kv:
-                    y = ref.norm_rotate(ref.bf16_val(x), norm[0 if h < n_q else 1], 1e-6, p, rot, inter, freq, scale)
+                    y = ref.norm_rotate(ref.bf16_val(x), norm[0 if h < n_q else 1], eps, p, rot, inter, freq, scale)
                     have = got_q[t, h * D:(h + 1) * D] if h < n_q else got_k[t, (h - n_q) * D:(h - n_q + 1) * D]
                     err = np.abs(ref.bf16_val(have) - y)
                     assert (err <= 2.0 ** -8 * np.abs(y) + 1e-38).all(), (b, i, h)
@@ -318,6 +319,26 @@ def test_append_whole_and_part_quads(fmt, D, n_kv):
     got_q, got_k, _ = run_append(s, n_q, qkv, norm, 32, 0, freq, 1.0)
     check_append(s, n_q, qkv, norm, 32, 0, freq, 1.0, got_q, got_k)
     assert (got_q[int(s.start[-1]):] == ref.bf16_bits([7.0])[0]).all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_append_norms_of_tiny_and_huge_heads(eps):
+    """Heads whose squares lie outside fp32: the largest and the smallest bf16
+    values, and some between."""
+    n_q, D = 9, 64
+    s = Setup(BF16, 1, D, 32, [9], [9], seed=12, pad_rows=0)
+    qkv = append_inputs(s, n_q, 7)
+    x = ref.bf16_val(qkv).reshape(s.T, n_q + 2, D)
+    x = np.clip(x / 8, -0.99, 0.99)
+    for t, m in enumerate([1e-37, 2.0 ** -120, 1e-25, 1e-19, 1.0, 1e18, 1e20, 1e30, 3e38]):
+        x[t] *= m
+    x[0, 3], x[0, 9] = 2.0 ** -133, -(2.0 ** -133)  # the smallest there is
+    qkv = ref.bf16_bits(x.reshape(s.T, -1))
+    norm = [np.full(D, 1.5, np.float32)] * 2
+    freq, _ = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 64, 10000.0)
+    print("append, tiny and huge", eps, flush=True)
+    got_q, got_k, _ = run_append(s, n_q, qkv, norm, 64, 0, freq, 1.0, eps=eps)
+    check_append(s, n_q, qkv, norm, 64, 0, freq, 1.0, got_q, got_k, eps=eps)
 
 
 def test_append_far_positions_scaled_and_given():
