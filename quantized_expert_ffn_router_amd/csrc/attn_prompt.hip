@@ -13,7 +13,7 @@
 // (ds_read_b64_tr_b16) with their tokens in the same order.
 //
 // Bound by the matrix units at the clock they hold under load: 8192 rows behind
-// 8192 keys (32 heads of 128) 1350 us, 1.22 PFLOP/s of visible pairs, where a large
+// 8192 keys (32 heads of 128) 1350 to 1430 us, 1.2 PFLOP/s of visible pairs, where a large
 // bf16 library product reaches 1.17.  16384 rows of nine prompts of 630 to 3150
 // rows: 325 us, 0.94; there every tile's start, the part of its last keys that is
 // masked, and the output weigh more.  333 rows take 12 us: six tiles of keys one

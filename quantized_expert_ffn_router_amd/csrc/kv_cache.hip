@@ -269,11 +269,11 @@ __device__ __forceinline__ void store_8(Rsrc r, uint32_t at, uint2 x) {
 // QUADS (the formats that keep four tokens' values side by side): the four waves
 // take the tokens of one aligned quad of a sequence, so that the quad's values
 // are written as whole pieces, put together in LDS; a quad that is not whole in
-// this call is written value by value.  16384 rows (bf16 cache) 97 us without, 86
+// this call is written value by value.  16384 rows (bf16 cache) 95 us without, 70
 // with it.
 //
 // Bound by memory, one read and one write of everything: 16384 rows of 40 heads of
-// 128 into a bf16 cache 84 us, 4.2 TB/s (a large copy reaches 5.15); 4096 rows
+// 128 into a bf16 cache 70 us, 5.0 TB/s (a large copy reaches 5.15); 4096 rows
 // into NVFP4 19 us, 4.3 TB/s.  A decode step's 8 rows take 4.4 us, the launch and
 // one chain of loads.
 template <int FMT, int D, bool HALVES>
@@ -315,7 +315,7 @@ __global__ __launch_bounds__(64 * kRows) void k_kv_append(AppendArgs a) {
   };
   // Buffer accesses, out of range where there is no head (or row): no access is
   // behind a branch, which would make every wait for a load one for the stores
-  // after it, too.
+  // after it, too (16384 rows 70 us, with branches 85).
   constexpr uint32_t kNowhere = 0x80000000u;
   const Rsrc from = buffer_of(row, mine ? (n_q + 2 * n_kv) * D * 2 : 0);
   const auto fetch = [&](int u, uint2& xa, uint2& xb) {
@@ -691,7 +691,7 @@ hipError_t launch_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const 
   // (quads: n rows of a sequence lie in at most n/4 + 2 of them)
   const int64_t wgs = c->fmt == MOE_FMT_NVFP4 ? (T + kRows - 1) / kRows : T / 4 + 2 * (int64_t)s->n_seq;
   // few rows: the heads of a row spread over workgroups (each takes the row's
-  // angles again: 4096 rows 19.2 us over 1024 workgroups, 22 over 4096)
+  // angles again: 6001 rows 17.8 us over 1526 workgroups, 19.7 over 3052)
   int hs = (int)((1024 + wgs - 1) / wgs);
   hs = hs < 1 ? 1 : hs > groups ? groups : hs;
   return by_format(c->fmt, c->D, [&](auto F, auto DD) {
