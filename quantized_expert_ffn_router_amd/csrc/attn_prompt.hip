@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
     const int i = min(i0 + lane, a.n_seq - 1);
     q0 = a.q_start[i]; q1 = a.q_start[i + 1];
     s0 = a.kv_start[i]; s1 = a.kv_start[i + 1];
-    const int64_t n = (int64_t)q1 - q0;
+    const int64_t n = min((int64_t)q1, a.T) - q0;  // (rows from T on are left out)
     sum = i0 + lane < a.n_seq && n > 0 ? (int)((n + BM - 1) / BM) : 0;
     for (int d = 1; d < 64 && d < a.n_seq; d <<= 1) {
       const int v = __shfl_up(sum, d);
@@ -379,12 +379,13 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
   const int want = total - 1 - slot;
   if (want < 0) return;
   if (a.n_seq > 64) {
-    for (;; first += 64) {
+    for (; first < a.n_seq; first += 64) {
       round(first);
       const int all = __builtin_amdgcn_readlane(sum, min(63, a.n_seq - 1 - first));
       if (before + all > want) break;
       before += all;
     }
+    if (first >= a.n_seq) return;  // (no sequence has it: starts that do not ascend)
   }
   const int at = __ffsll((unsigned long long)__ballot(before + sum > want)) - 1;
   const int64_t r0 = __builtin_amdgcn_readlane(q0, at), rows = __builtin_amdgcn_readlane(q1, at) - r0;

@@ -610,6 +610,17 @@ def test_prompt_bad_ranges_give_nan():
     assert np.isnan(ref.bf16_val(got[10:])).all()
 
 
+def test_prompt_rows_beyond_t_are_left_out():
+    """The last sequence claims more rows than there are: those inside are answered, at the
+    positions that its claim gives them."""
+    rng = np.random.default_rng(4)
+    T, L = 40, 1000
+    qv = ref.bf16_bits(rng.standard_normal((T, 128)))
+    kv, vv = (ref.bf16_bits(rng.standard_normal((20 + L, 128))) for _ in range(2))
+    got = run_prompt(1, 1, 128, [0, 20, 920], [0, 20, 20 + L], T, 20 + L, qv, kv, vv)
+    check_prompt(1, 1, 128, [0, 20, 920], [0, 20, 20 + L], qv, kv, vv, got, rows=range(20))
+
+
 @pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
 def test_prompt_chunk_then_decode_steps(fmt):
     """The operators together, as a server uses them: a prompt appended in two
