@@ -48,11 +48,21 @@ struct RowSeq {
   int b, r0, len;
   int64_t rows;
 };
-__device__ __forceinline__ RowSeq find_row(const SeqView& s, int64_t t) {
+// Values whose loads are to be on their way together: the compiler would put one
+// whose use is behind a branch there, a round trip later.
+__device__ __forceinline__ void loaded(int& a, int& b, int& c, int& d) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+#endif
+}
+// also: another such value of the caller's.
+__device__ __forceinline__ RowSeq find_row(const SeqView& s, int64_t t, int* also = nullptr) {
   RowSeq r{-1, 0, 0, 0};
   for (int i0 = 0; i0 < s.n_seq; i0 += 64) {
     const int i = min(i0 + lane_id(), s.n_seq - 1);
-    const int start = s.row_start[i], end = s.row_start[i + 1], len = s.kv_len[i];
+    int start = s.row_start[i], end = s.row_start[i + 1], len = s.kv_len[i];
+    int none = 0;
+    loaded(end, start, len, also ? *also : none);
     const uint64_t behind = __ballot(i0 + lane_id() < s.n_seq && (int64_t)end > t);
     if (!behind) continue;
     const int l = __ffsll((unsigned long long)behind) - 1;
@@ -79,14 +89,13 @@ __device__ __forceinline__ RowSeq find_quad(const SeqView& s, int64_t T, int uni
     const int64_t lo = max(start, 0), hi = min((int64_t)end, T);
     const int64_t tok = (int64_t)len - ((int64_t)end - start) + (lo - start);
     int sum = i0 + lane_id() < s.n_seq && hi > lo ? (int)(((tok + hi - lo - 1) >> 2) - (tok >> 2)) + 1 : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
+    for (int d = 1; d < 64 && d < s.n_seq; d <<= 1) {
       const int v = __shfl_up(sum, d);
       if (lane_id() >= d) sum += v;
     }
     const uint64_t past = __ballot(before + sum > unit);
     if (!past) {
-      before += __builtin_amdgcn_readlane(sum, 63);
+      before += __builtin_amdgcn_readlane(sum, min(63, s.n_seq - 1 - i0));
       continue;
     }
     const int l = __ffsll((unsigned long long)past) - 1;

@@ -816,7 +816,7 @@ __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int64_t at = ((int64_t)t * a.n_q + h) * a.S;
   // (a row outside the sequences has no number there: whatever it reads is not used)
-  const int ns = min(a.part_n[(int64_t)t * a.n_q + h], a.S);
+  int ns = a.part_n[(int64_t)t * a.n_q + h];
   float2 ml[PER];
   float4 v[PER];
   const auto load = [&](int i, int s) {
@@ -826,7 +826,8 @@ __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     if (grp + NG * i < a.likely) load(i, grp + NG * i);
-  const RowSeq q = find_row(a.s, t);
+  const RowSeq q = find_row(a.s, t, &ns);
+  ns = __builtin_amdgcn_readfirstlane(min(ns, a.S));
   if (q.b < 0 || ns == 1) return;
   float M = kNone, L = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
