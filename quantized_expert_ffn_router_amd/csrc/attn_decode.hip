@@ -594,8 +594,7 @@ template <int N>
 __device__ __forceinline__ void store_row(uint16_t* d, const float (&v)[N]) {
   uint32_t w[N / 2];
 #pragma unroll
-  for (int j = 0; j < N / 2; ++j)
-    w[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+  for (int j = 0; j < N / 2; ++j) w[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
   if constexpr (N == 4) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
   if constexpr (N >= 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
   if constexpr (N == 16) *reinterpret_cast<uint4*>(d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -628,173 +627,171 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
   const size_t page_bytes = (size_t)a.n_kv * lay.head;
   const uint8_t* heads = a.pool + (size_t)kvh * lay.head;
   const typename Unit<FMT, D>::Lane at(n, g, P);
-  {
-    const TilePlan plan = tile_plan(it, a.G, 16 * NT);
-    const int u_begin = sp > 0 ? sp * it.chunk : 0;
-    const int u_end = min((int64_t)plan.units, (int64_t)u_begin + it.chunk);
-    if (sp > 0 && u_begin >= u_end) {  // (split 0 also answers rows that see nothing)
-      const int rr = tile * (16 * NT) + threadIdx.x, i = (int)((uint32_t)rr / (uint32_t)a.G);
-      if (threadIdx.x < 16 * NT && rr < inside * a.G)
-        a.part_ml[((int64_t)(r0 + i) * a.n_q + kvh * a.G + rr - i * a.G) * a.S + sp] = make_float2(kNone, 0.0f);
-      return;
-    }
+  const TilePlan plan = tile_plan(it, a.G, 16 * NT);
+  const int u_begin = sp > 0 ? sp * it.chunk : 0;
+  const int u_end = min((int64_t)plan.units, (int64_t)u_begin + it.chunk);
+  if (sp > 0 && u_begin >= u_end) {  // (split 0 also answers rows that see nothing)
+    const int rr = tile * (16 * NT) + threadIdx.x, i = (int)((uint32_t)rr / (uint32_t)a.G);
+    if (threadIdx.x < 16 * NT && rr < inside * a.G)
+      a.part_ml[((int64_t)(r0 + i) * a.n_q + kvh * a.G + rr - i * a.G) * a.S + sp] = make_float2(kNone, 0.0f);
+    return;
+  }
 
-    Unit<FMT, D> c;
-    // Entries of the page table, by scalar loads (a wave's units are its own); a
-    // unit past the table's end has none.
-    const int* const row = a.s.page_table + (int64_t)b * a.s.max_pages;
-    const auto page_at = [&](int u) {
-      const int i = (int)(((int64_t)u * 32) >> a.s.log2P);
-      const int p = *(const int __attribute__((address_space(4)))*)(uintptr_t)(row + min(i, a.s.max_pages - 1));
-      return i < a.s.max_pages ? p : -1;
-    };
-    const auto block = [&](int page) {  // page 0 stands in for one that is not there
-      return heads + (size_t)((unsigned)page < (unsigned)a.s.n_pages ? page : 0) * page_bytes;
-    };
-    // this lane's query rows, their last visible tokens and their fragments
-    Carry<FMT, D, NT> w;
+  Unit<FMT, D> c;
+  // Entries of the page table, by scalar loads (a wave's units are its own); a
+  // unit past the table's end has none.
+  const int* const row = a.s.page_table + (int64_t)b * a.s.max_pages;
+  const auto page_at = [&](int u) {
+    const int i = (int)(((int64_t)u * 32) >> a.s.log2P);
+    const int p = *(const int __attribute__((address_space(4)))*)(uintptr_t)(row + min(i, a.s.max_pages - 1));
+    return i < a.s.max_pages ? p : -1;
+  };
+  const auto block = [&](int page) {  // page 0 stands in for one that is not there
+    return heads + (size_t)((unsigned)page < (unsigned)a.s.n_pages ? page : 0) * page_bytes;
+  };
+  // this lane's query rows, their last visible tokens and their fragments
+  Carry<FMT, D, NT> w;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int r = (tile * NT + t) * 16 + n, i = (int)((uint32_t)r / (uint32_t)a.G);
-      const int row = r0 + i, head = kvh * a.G + r - i * a.G;
-      const bool live = r < inside * a.G;
-      w.limit[t] = live ? (int64_t)len - rows + i : -1;
-      const uint16_t* qp = a.q + (live ? row : r0) * a.q_stride + (size_t)(live ? head : kvh * a.G) * D;
-      w.qs[t] = a.scale_log2;
+  for (int t = 0; t < NT; ++t) {
+    const int r = (tile * NT + t) * 16 + n, i = (int)((uint32_t)r / (uint32_t)a.G);
+    const int row = r0 + i, head = kvh * a.G + r - i * a.G;
+    const bool live = r < inside * a.G;
+    w.limit[t] = live ? (int64_t)len - rows + i : -1;
+    const uint16_t* qp = a.q + (live ? row : r0) * a.q_stride + (size_t)(live ? head : kvh * a.G) * D;
+    w.qs[t] = a.scale_log2;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) w.qf[t][s] = *reinterpret_cast<const v4u*>(qp + Unit<FMT, D>::key_dim(s, g));
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    for (int s = 0; s < KS; ++s) w.qf[t][s] = *reinterpret_cast<const v4u*>(qp + Unit<FMT, D>::key_dim(s, g));
+  }
+  __builtin_amdgcn_sched_barrier(0);
 
-    int u = u_begin + wave, page = 0, next = 0;
-    if (u < u_end) {
-      page = page_at(u);
-      next = page_at(min(u + kWaves, u_end - 1));
-      c.load_keys(block(page), lay, lay.head, (u * 32) & (P - 1), at);
-      c.load_values(block(page), lay, lay.head, P, (u * 32) & (P - 1), at);
-    }
+  int u = u_begin + wave, page = 0, next = 0;
+  if (u < u_end) {
+    page = page_at(u);
+    next = page_at(min(u + kWaves, u_end - 1));
+    c.load_keys(block(page), lay, lay.head, (u * 32) & (P - 1), at);
+    c.load_values(block(page), lay, lay.head, P, (u * 32) & (P - 1), at);
+  }
 
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if constexpr (FMT != MOE_FMT_BF16) {
-        // bf16 -> fp16, scaled by the power of two that puts the row's largest
-        // magnitude into [2^14, 2^15): exact for values above 2^-29 of it
-        uint32_t top = 0;
+  for (int t = 0; t < NT; ++t) {
+    if constexpr (FMT != MOE_FMT_BF16) {
+      // bf16 -> fp16, scaled by the power of two that puts the row's largest
+      // magnitude into [2^14, 2^15): exact for values above 2^-29 of it
+      uint32_t top = 0;
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            top = max(top, max(w.qf[t][s][i] & 0x7fffu, (w.qf[t][s][i] >> 16) & 0x7fffu));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        const int e = min(max(141 - (int)(top >> 7), -113), 126);
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        w.qs[t] *= __uint_as_float((uint32_t)(127 - e) << 23);
+        for (int i = 0; i < 4; ++i)
+          top = max(top, max(w.qf[t][s][i] & 0x7fffu, (w.qf[t][s][i] >> 16) & 0x7fffu));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+      const int e = min(max(141 - (int)(top >> 7), -113), 126);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      w.qs[t] *= __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const v2h p = {(_Float16)(__uint_as_float(w.qf[t][s][i] << 16) * up),
-                           (_Float16)(__uint_as_float(w.qf[t][s][i] & 0xffff0000u) * up)};
-            w.qf[t][s][i] = bits(p);
-          }
-      } else {
+        for (int i = 0; i < 4; ++i) {
+          const v2h p = {(_Float16)(__uint_as_float(w.qf[t][s][i] << 16) * up),
+                         (_Float16)(__uint_as_float(w.qf[t][s][i] & 0xffff0000u) * up)};
+          w.qf[t][s][i] = bits(p);
+        }
+    } else {
 #if defined(__HIP_DEVICE_COMPILE__)
-        // (waited for here, not in every unit)
+      // (waited for here, not in every unit)
 #pragma unroll
-        for (int s = 0; s < KS; ++s) asm("" : "+v"(w.qf[t][s]));
+      for (int s = 0; s < KS; ++s) asm("" : "+v"(w.qf[t][s]));
 #endif
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) w.o[t][j] = v4f{0.f, 0.f, 0.f, 0.f};
-      w.m[t] = kNone;
-      w.l[t] = 0.0f;
     }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) w.o[t][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    w.m[t] = kNone;
+    w.l[t] = 0.0f;
+  }
 
-    // The loads of the next unit are not conditional (after a wave's last one they
-    // read nothing): a load that may or may not be there would have to be waited
-    // for with the others.
-    bool wild = false;
+  // The loads of the next unit are not conditional (after a wave's last one they
+  // read nothing): a load that may or may not be there would have to be waited
+  // for with the others.
+  bool wild = false;
 #pragma unroll 1
-    for (; u < u_end; u += kWaves) {
-      const int64_t t0 = (int64_t)u * 32;
-      const bool more = u + kWaves < u_end;
-      const int o = ((u + kWaves) * 32) & (P - 1), bytes = more ? (int)lay.head : 0;
-      const uint8_t* blk = block(next);
-      if ((unsigned)page >= (unsigned)a.s.n_pages) {
-        // nothing to read: rows that see a token of it have no answer
+  for (; u < u_end; u += kWaves) {
+    const int64_t t0 = (int64_t)u * 32;
+    const bool more = u + kWaves < u_end;
+    const int o = ((u + kWaves) * 32) & (P - 1), bytes = more ? (int)lay.head : 0;
+    const uint8_t* blk = block(next);
+    if ((unsigned)page >= (unsigned)a.s.n_pages) {
+      // nothing to read: rows that see a token of it have no answer
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (w.limit[t] >= t0) w.l[t] = __uint_as_float(0x7fc00000u);
-      }
-      page = next;
-      next = page_at(min(u + 2 * kWaves, u_end - 1));
-      wild |= w.unit(c, t0 + 31 > plan.lo, t0, (int)min(plan.hi + 1 - t0, (int64_t)32), g,
-             [&] { c.load_keys(blk, lay, bytes, o, at); },
-                     [&] { c.load_values(blk, lay, bytes, P, o, at); });
+      for (int t = 0; t < NT; ++t)
+        if (w.limit[t] >= t0) w.l[t] = __uint_as_float(0x7fc00000u);
     }
+    page = next;
+    next = page_at(min(u + 2 * kWaves, u_end - 1));
+    wild |= w.unit(c, t0 + 31 > plan.lo, t0, (int)min(plan.hi + 1 - t0, (int64_t)32), g,
+           [&] { c.load_keys(blk, lay, bytes, o, at); },
+                   [&] { c.load_values(blk, lay, bytes, P, o, at); });
+  }
 
-    // join the waves' parts
+  // join the waves' parts
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float l = groups_sum(w.l[t]);
-      __syncthreads();  // former parts have been read
-      if (g == 0) { m_s[wave][n] = w.m[t]; l_s[wave][n] = l; }
-      float* const part = o_s[wave][n];
+  for (int t = 0; t < NT; ++t) {
+    const float l = groups_sum(w.l[t]);
+    __syncthreads();  // former parts have been read
+    if (g == 0) { m_s[wave][n] = w.m[t]; l_s[wave][n] = l; }
+    float* const part = o_s[wave][n];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        constexpr int JC = Unit<FMT, D>::JC;
+    for (int i = 0; i < 4; ++i) {
+      constexpr int JC = Unit<FMT, D>::JC;
 #pragma unroll
-        for (int j = 0; j < NJ; j += JC < 4 ? 2 : 4) {
-          float* e = part + Unit<FMT, D>::value_dim(4 * g + i, j);
-          if constexpr (JC < 4)
-            *reinterpret_cast<float2*>(e) = make_float2(w.o[t][j][i], w.o[t][j + 1][i]);
-          else
-            *reinterpret_cast<float4*>(e) =
-                make_float4(w.o[t][j][i], w.o[t][j + 1][i], w.o[t][j + 2][i], w.o[t][j + 3][i]);
-        }
+      for (int j = 0; j < NJ; j += JC < 4 ? 2 : 4) {
+        float* e = part + Unit<FMT, D>::value_dim(4 * g + i, j);
+        if constexpr (JC < 4)
+          *reinterpret_cast<float2*>(e) = make_float2(w.o[t][j][i], w.o[t][j + 1][i]);
+        else
+          *reinterpret_cast<float4*>(e) =
+              make_float4(w.o[t][j][i], w.o[t][j + 1][i], w.o[t][j + 2][i], w.o[t][j + 3][i]);
       }
-      if (wild) {
-        for (int v = u_begin + wave; v < u_end; v += kWaves) {
-          const int64_t t0 = (int64_t)v * 32;
-          const int pg = page_at(v);
-          if (t0 + 31 <= plan.lo || (unsigned)pg >= (unsigned)a.s.n_pages) continue;
-          c.load_keys(block(pg), lay, lay.head, (v * 32) & (P - 1), at);
-          c.load_values(block(pg), lay, lay.head, P, (v * 32) & (P - 1), at);
-          w.wild_values(c, t, t0, (int)min(plan.hi + 1 - t0, (int64_t)32), g, part);
-        }
+    }
+    if (wild) {
+      for (int v = u_begin + wave; v < u_end; v += kWaves) {
+        const int64_t t0 = (int64_t)v * 32;
+        const int pg = page_at(v);
+        if (t0 + 31 <= plan.lo || (unsigned)pg >= (unsigned)a.s.n_pages) continue;
+        c.load_keys(block(pg), lay, lay.head, (v * 32) & (P - 1), at);
+        c.load_values(block(pg), lay, lay.head, P, (v * 32) & (P - 1), at);
+        w.wild_values(c, t, t0, (int)min(plan.hi + 1 - t0, (int64_t)32), g, part);
       }
-      __syncthreads();
-      const int qr = threadIdx.x / (D / E), d0 = (threadIdx.x % (D / E)) * E;
-      float M = kNone, L = 0.0f, acc[E];
+    }
+    __syncthreads();
+    const int qr = threadIdx.x / (D / E), d0 = (threadIdx.x % (D / E)) * E;
+    float M = kNone, L = 0.0f, acc[E];
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) M = fmaxf(M, m_s[i][qr]);
+    for (int i = 0; i < kWaves; ++i) M = fmaxf(M, m_s[i][qr]);
 #pragma unroll
-      for (int j = 0; j < E; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < E; ++j) acc[j] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        const float f = __builtin_amdgcn_exp2f(m_s[i][qr] - M);
-        L += f * l_s[i][qr];
+    for (int i = 0; i < kWaves; ++i) {
+      const float f = __builtin_amdgcn_exp2f(m_s[i][qr] - M);
+      L += f * l_s[i][qr];
 #pragma unroll
-        for (int j = 0; j < E; ++j) acc[j] += f * o_s[i][qr][d0 + j];
-      }
-      const int rr = (tile * NT + t) * 16 + qr, i = (int)((uint32_t)rr / (uint32_t)a.G);
-      const int64_t orow = r0 + i, h = kvh * a.G + rr - i * a.G;
-      if (rr >= inside * a.G) continue;
-      if (d0 == 0 && sp == 0 && a.S > 1) a.part_n[orow * a.n_q + h] = it.splits;
-      if (it.splits == 1) {
-        const float inv = (int64_t)len - rows + i < 0 ? 0.0f : a.v_ts / L;
+      for (int j = 0; j < E; ++j) acc[j] += f * o_s[i][qr][d0 + j];
+    }
+    const int rr = (tile * NT + t) * 16 + qr, i = (int)((uint32_t)rr / (uint32_t)a.G);
+    const int64_t orow = r0 + i, h = kvh * a.G + rr - i * a.G;
+    if (rr >= inside * a.G) continue;
+    if (d0 == 0 && sp == 0 && a.S > 1) a.part_n[orow * a.n_q + h] = it.splits;
+    if (it.splits == 1) {
+      const float inv = (int64_t)len - rows + i < 0 ? 0.0f : a.v_ts / L;
 #pragma unroll
-        for (int j = 0; j < E; ++j) acc[j] *= inv;
-        store_row<E>(a.out + orow * a.out_stride + h * D + d0, acc);
-      } else {
-        const int64_t at = (orow * a.n_q + h) * a.S + sp;
-        if (d0 == 0) a.part_ml[at] = make_float2(M, L);
-        float* d = a.part_o + at * D + d0;
+      for (int j = 0; j < E; ++j) acc[j] *= inv;
+      store_row<E>(a.out + orow * a.out_stride + h * D + d0, acc);
+    } else {
+      const int64_t at = (orow * a.n_q + h) * a.S + sp;
+      if (d0 == 0) a.part_ml[at] = make_float2(M, L);
+      float* d = a.part_o + at * D + d0;
 #pragma unroll
-        for (int j = 0; j < E; j += 4)
-          *reinterpret_cast<float4*>(d + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-      }
+      for (int j = 0; j < E; j += 4)
+        *reinterpret_cast<float4*>(d + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
     }
   }
 }
