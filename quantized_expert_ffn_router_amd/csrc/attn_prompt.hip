@@ -365,6 +365,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
     const int i = min(i0 + lane, a.n_seq - 1);
     q0 = a.q_start[i]; q1 = a.q_start[i + 1];
     s0 = a.kv_start[i]; s1 = a.kv_start[i + 1];
+    loaded(q0, q1, s0, s1);
     const int64_t n = min((int64_t)q1, a.T) - q0;  // (rows from T on are left out)
     sum = i0 + lane < a.n_seq && n > 0 ? (int)((n + BM - 1) / BM) : 0;
     for (int d = 1; d < 64 && d < a.n_seq; d <<= 1) {
