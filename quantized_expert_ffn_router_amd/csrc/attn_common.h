@@ -9,7 +9,9 @@
 // of four tokens), so every fragment of a 16-token step is one vector load.
 #pragma once
 
-#include "common.h"
+#include <type_traits>
+
+#include "gate_common.h"
 
 namespace moe {
 
@@ -48,6 +50,21 @@ struct RowSeq {
   int b, r0, len;
   int64_t rows;
 };
+// Wave-wide sum, in the order of wave_incl_scan.
+__device__ __forceinline__ float wave_sum(float v) {
+  const auto add = [&](auto CTRL, auto ROWS) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL(), ROWS(), 0xf, ROWS() == 0xf));
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x112>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x114>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x118>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x142>(), integral_constant<int, 0xa>());
+  add(integral_constant<int, 0x143>(), integral_constant<int, 0xc>());
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
 // Values whose loads are to be on their way together: the compiler would put one
 // whose use is behind a branch there, a round trip later.
 __device__ __forceinline__ void loaded(int& a, int& b, int& c, int& d) {
@@ -88,14 +105,11 @@ __device__ __forceinline__ RowSeq find_quad(const SeqView& s, int64_t T, int uni
     const int start = s.row_start[i], end = s.row_start[i + 1], len = s.kv_len[i];
     const int64_t lo = max(start, 0), hi = min((int64_t)end, T);
     const int64_t tok = (int64_t)len - ((int64_t)end - start) + (lo - start);
-    int sum = i0 + lane_id() < s.n_seq && hi > lo ? (int)(((tok + hi - lo - 1) >> 2) - (tok >> 2)) + 1 : 0;
-    for (int d = 1; d < 64 && d < s.n_seq; d <<= 1) {
-      const int v = __shfl_up(sum, d);
-      if (lane_id() >= d) sum += v;
-    }
+    const int sum = wave_incl_scan(
+        i0 + lane_id() < s.n_seq && hi > lo ? (int)(((tok + hi - lo - 1) >> 2) - (tok >> 2)) + 1 : 0);
     const uint64_t past = __ballot(before + sum > unit);
     if (!past) {
-      before += __builtin_amdgcn_readlane(sum, min(63, s.n_seq - 1 - i0));
+      before += __builtin_amdgcn_readlane(sum, 63);
       continue;
     }
     const int l = __ffsll((unsigned long long)past) - 1;

@@ -89,7 +89,6 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
   r.b = -1;
   r.chunk = INT32_MAX;
   const LaneSeq first(s, 0, T, G, size);
-  const int span = min(s.n_seq, 64);  // lanes that hold something
   if (S > 1) {
     float work = 0.0f;
     int most = 0;
@@ -98,10 +97,8 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
       work += (float)q.tiles * (float)q.units;
       most = max(most, q.units);
     }
-    for (int d = 1; d < span; d <<= 1) {
-      work += __shfl_xor(work, d);
-      most = max(most, __shfl_xor(most, d));
-    }
+    work = wave_sum(work);
+    most = wave_max(most);
     int chunk = (int)ceilf(work / (float)room);
     if (chunk < kWhole) chunk = max(chunk, min((int)ceilf(work * n_kv / 256.0f), kWhole));
     chunk = (max(chunk, (most + S - 1) / S) + kWaves - 1) / kWaves * kWaves;
@@ -112,14 +109,10 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
     const LaneSeq q = i0 ? LaneSeq(s, i0, T, G, size) : first;
     // (a row without tokens is answered too)
     const int splits = S > 1 && q.units ? (int)((uint32_t)(q.units - 1) / (uint32_t)r.chunk) + 1 : 1;
-    int sum = q.tiles * splits * n_kv;
-    for (int d = 1; d < span; d <<= 1) {
-      const int v = __shfl_up(sum, d);
-      if (lane_id() >= d) sum += v;
-    }
+    const int sum = wave_incl_scan(q.tiles * splits * n_kv);
     const uint64_t past = __ballot(i0 + lane_id() < s.n_seq && before + sum > id);
     if (!past) {
-      before += __builtin_amdgcn_readlane(sum, min(63, s.n_seq - 1 - i0));
+      before += __builtin_amdgcn_readlane(sum, 63);
       continue;
     }
     const int l = __ffsll((unsigned long long)past) - 1;

@@ -367,22 +367,18 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
     s0 = a.kv_start[i]; s1 = a.kv_start[i + 1];
     loaded(q0, q1, s0, s1);
     const int64_t n = min((int64_t)q1, a.T) - q0;  // (rows from T on are left out)
-    sum = i0 + lane < a.n_seq && n > 0 ? (int)((n + BM - 1) / BM) : 0;
-    for (int d = 1; d < 64 && d < a.n_seq; d <<= 1) {
-      const int v = __shfl_up(sum, d);
-      if (lane >= d) sum += v;
-    }
+    sum = wave_incl_scan(i0 + lane < a.n_seq && n > 0 ? (int)((n + BM - 1) / BM) : 0);
   };
   for (int i0 = 0; i0 < a.n_seq; i0 += 64) {
     round(i0);
-    total += __builtin_amdgcn_readlane(sum, min(63, a.n_seq - 1 - i0));
+    total += __builtin_amdgcn_readlane(sum, 63);
   }
   const int want = total - 1 - slot;
   if (want < 0) return;
   if (a.n_seq > 64) {
     for (; first < a.n_seq; first += 64) {
       round(first);
-      const int all = __builtin_amdgcn_readlane(sum, min(63, a.n_seq - 1 - first));
+      const int all = __builtin_amdgcn_readlane(sum, 63);
       if (before + all > want) break;
       before += all;
     }

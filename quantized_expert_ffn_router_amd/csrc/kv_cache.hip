@@ -529,14 +529,11 @@ __global__ __launch_bounds__(256) void k_kv_read(ReadArgs a) {
     loaded(from, len, o0, o1);
     from = a.first ? max(from, 0) : 0;
     const int64_t stop = min((int64_t)len, from + max((int64_t)o1 - o0, (int64_t)0));
-    int sum = i0 + lane < a.s.n_seq && stop > from ? (int)((stop - 1) >> 4) - (from >> 4) + 1 : 0;
-    for (int d = 1; d < 64 && d < a.s.n_seq; d <<= 1) {
-      const int v = __shfl_up(sum, d);
-      if (lane >= d) sum += v;
-    }
+    const int sum = wave_incl_scan(
+        i0 + lane < a.s.n_seq && stop > from ? (int)((stop - 1) >> 4) - (from >> 4) + 1 : 0);
     const uint64_t past = __ballot(before + sum > unit);
     if (!past) {
-      before += __builtin_amdgcn_readlane(sum, min(63, a.s.n_seq - 1 - i0));
+      before += __builtin_amdgcn_readlane(sum, 63);
       continue;
     }
     const int l = __ffsll((unsigned long long)past) - 1;
