@@ -642,15 +642,17 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
   const auto block = [&](int page) {  // page 0 stands in for one that is not there
     return heads + (size_t)((unsigned)page < (unsigned)a.s.n_pages ? page : 0) * page_bytes;
   };
-  // this lane's query rows, their last visible tokens and their fragments
+  // this lane's query rows, their last visible tokens and their fragments; a lane
+  // without a row takes the tile's last one (its answer goes nowhere, but it has a
+  // say in when the maxima move: another tile's row may be overwritten meanwhile,
+  // where the output takes the queries' place)
   Carry<FMT, D, NT> w;
+  const int last = inside * a.G - 1;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int r = (tile * NT + t) * 16 + n, i = (int)((uint32_t)r / (uint32_t)a.G);
-    const int row = r0 + i, head = kvh * a.G + r - i * a.G;
-    const bool live = r < inside * a.G;
-    w.limit[t] = live ? (int64_t)len - rows + i : -1;
-    const uint16_t* qp = a.q + (live ? row : r0) * a.q_stride + (size_t)(live ? head : kvh * a.G) * D;
+    const int r = (tile * NT + t) * 16 + n, mine = min(r, last), i = (int)((uint32_t)mine / (uint32_t)a.G);
+    w.limit[t] = r <= last ? (int64_t)len - rows + i : -1;
+    const uint16_t* qp = a.q + (int64_t)(r0 + i) * a.q_stride + (size_t)(kvh * a.G + mine - i * a.G) * D;
     w.qs[t] = a.scale_log2;
 #pragma unroll
     for (int s = 0; s < KS; ++s) w.qf[t][s] = *reinterpret_cast<const v4u*>(qp + Unit<FMT, D>::key_dim(s, g));

@@ -1,0 +1,48 @@
+"""Corners of the key/value cache and attention operators that the cases of
+test_gpu_attention.py do not reach, against the same 64-bit reference and bounds."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attn_ref as ref
+import quantized_expert_ffn_router_amd as q
+from attn_ref import BF16, NVFP4, Q8_0
+from test_gpu_attention import FMT, Setup, check_decode, run_decode
+
+pytestmark = pytest.mark.gpu
+
+dev = "cuda"
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode_tiles_do_not_depend_on_other_tiles_rows(fmt, D):
+    """5 rows of 8 heads a group: the last tile holds the last row alone, and its
+    bits are the same whatever the first row's queries are."""
+    print("other tiles", FMT[fmt], D, flush=True)
+    s = Setup(fmt, 1, D, 32, [384], [5], seed=3, pad_rows=0)
+    qv = ref.bf16_bits(3 * s.rng.standard_normal((s.T, 8 * D)))
+    got = []
+    for mag in (1.0, 0.0, 3.0, 10.0):
+        x = qv.copy()
+        x[0] = ref.bf16_bits(mag * ref.bf16_val(qv[0]))
+        got.append(run_decode(s, 8, x))
+    check_decode(s, 8, qv, got[0])
+    for g in got[1:]:
+        assert np.array_equal(g[4], got[0][4])
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("D,rows", [(128, [5, 3, 9]), (64, [7, 1, 13]), (256, [3, 5, 1])])
+def test_decode_in_place_is_bit_for_bit_the_same(fmt, D, rows):
+    """Several tiles a sequence, the last ones partly filled, without a split (so
+    each tile stores its own output): the output in the queries' place."""
+    print("in place", FMT[fmt], D, rows, flush=True)
+    s = Setup(fmt, 2, D, 32, [300, 64, 340], rows, seed=6, pad_rows=1)
+    qv = ref.bf16_bits(3 * s.rng.standard_normal((s.T, 16 * D)))
+    want = run_decode(s, 16, qv)
+    n = int(s.start[-1])
+    for _ in range(5):
+        assert np.array_equal(run_decode(s, 16, qv, out="q")[:n], want[:n])
