@@ -431,7 +431,8 @@ size_t moe_kv_page_bytes(int32_t fmt, int32_t n_kv, int32_t D, int32_t page_toke
  * kv_len[b] tokens: row row_start[b] + i of n rows is token
  * kv_len[b] - n + i.  Token j lies in page page_table[b][j / page_tokens].
  * The arrays live on the device, so their contents are checked there: rows
- * outside 0..T are not touched, a row before its sequence's first token
+ * outside 0..T are not touched (those of the same sequence inside are answered
+ * as ever), a row before its sequence's first token
  * (kv_len[b] < n) stores nothing and sees nothing, and a page outside
  * 0..n_pages-1 (or a token past max_pages pages) is neither read nor written:
  * whatever should have been read from it is NaN in the results. */

@@ -63,16 +63,17 @@ struct Item {
   int tile, kvh, sp, splits, chunk;
 };
 
-// This lane's sequence.
+// This lane's sequence: its rows from row 0 on (row t is token len - end + t
+// wherever its first row lies).
 struct LaneSeq {
   int start, end, len;
   int tiles, units;
   __device__ __forceinline__ LaneSeq(const SeqView& s, int i0, int64_t T, int G, int size) {
     const int i = min(i0 + lane_id(), s.n_seq - 1);
-    start = s.row_start[i];
+    start = max(s.row_start[i], 0);
     end = s.row_start[i + 1];
     len = s.kv_len[i];
-    const int64_t n = i0 + lane_id() < s.n_seq && start >= 0 ? min((int64_t)end, T) - start : 0;
+    const int64_t n = i0 + lane_id() < s.n_seq ? min((int64_t)end, T) - start : 0;
     tiles = n > 0 ? (int)((uint32_t)((int)n * G + size - 1) / (uint32_t)size) : 0;
     units = n > 0 && len > 0 ? (len - 1) / 32 + 1 : 0;
   }

@@ -9,7 +9,8 @@ import torch
 import attn_ref as ref
 import quantized_expert_ffn_router_amd as q
 from attn_ref import BF16, NVFP4, Q8_0
-from test_gpu_attention import FMT, Setup, check_decode, run_decode
+from test_gpu_attention import (FMT, Setup, append_inputs, check_append, check_decode, run_append,
+                                run_decode)
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,38 @@ def test_decode_in_place_is_bit_for_bit_the_same(fmt, D, rows):
     n = int(s.start[-1])
     for _ in range(5):
         assert np.array_equal(run_decode(s, 16, qv, out="q")[:n], want[:n])
+
+
+def starts_before_row_0(s, skipped):
+    """The first sequence's first `skipped` rows lie before row 0."""
+    s.start = s.start - skipped
+    s.T -= skipped
+    s.to_device()
+    s.start, s.rows = np.maximum(s.start, 0), [s.rows[0] - skipped, *s.rows[1:]]
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("L", [3, 60, 700, 2100])
+def test_decode_rows_before_row_0_are_left_out(fmt, L):
+    """A sequence's rows inside 0..T are answered at their own positions, with and
+    without a split, wherever its first row lies (3 tokens: rows that see nothing)."""
+    for skipped, rows in ((4, [6, 2]), (39, [40, 1]), (5, [5, 3])):
+        print("rows before row 0", FMT[fmt], L, skipped, rows, flush=True)
+        s = Setup(fmt, 2, 64, 32, [L, 40], rows, seed=4, pad_rows=1)
+        starts_before_row_0(s, skipped)
+        qv = ref.bf16_bits(s.rng.standard_normal((s.T, 4 * 64)))
+        got = run_decode(s, 4, qv)
+        check_decode(s, 4, qv, got)
+        assert (got[int(s.start[-1]):] == ref.bf16_bits([7.0])[0]).all()
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+def test_append_rows_before_row_0_are_left_out(fmt):
+    print("append, rows before row 0", FMT[fmt], flush=True)
+    s = Setup(fmt, 2, 64, 32, [50, 9], [21, 5], seed=7, pad_rows=1)
+    starts_before_row_0(s, 9)
+    qkv = append_inputs(s, 4, 9)
+    freq, _ = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 32, 10000.0)
+    norm = [np.ones(64, np.float32)] * 2
+    got_q, got_k, _ = run_append(s, 4, qkv, norm, 32, 0, freq, 1.0)
+    check_append(s, 4, qkv, norm, 32, 0, freq, 1.0, got_q, got_k)
