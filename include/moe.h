@@ -543,7 +543,9 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
  * queries' own.  q: bf16 [T] rows of n_q * D; k, v: bf16 [Tk] rows of n_kv * D;
  * out: bf16 [T] rows of n_q * D (may be q, with the same stride).  k_stride and
  * v_stride: at most 2^24.  Rows outside
- * the sequences are left as they are; indices are held inside T and Tk. */
+ * the sequences are left as they are; indices are held inside T and Tk: of a
+ * sequence with rows outside 0..T those inside are answered, one with keys
+ * outside 0..Tk has NaN rows. */
 moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
                            const int32_t* q_start, const int32_t* kv_start, int64_t T, int64_t Tk,
                            const uint16_t* q, int64_t q_stride, const uint16_t* k,

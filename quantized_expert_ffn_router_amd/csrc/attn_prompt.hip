@@ -366,7 +366,10 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
     q0 = a.q_start[i]; q1 = a.q_start[i + 1];
     s0 = a.kv_start[i]; s1 = a.kv_start[i + 1];
     loaded(q0, q1, s0, s1);
-    const int64_t n = min((int64_t)q1, a.T) - q0;  // (rows from T on are left out)
+    // (rows before 0 and from T on are left out; a row's position counts from the
+    // sequence's end)
+    q0 = max(q0, 0);
+    const int64_t n = min((int64_t)q1, a.T) - q0;
     sum = wave_incl_scan(i0 + lane < a.n_seq && n > 0 ? (int)((n + BM - 1) / BM) : 0);
   };
   for (int i0 = 0; i0 < a.n_seq; i0 += 64) {
@@ -401,7 +404,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
 
   Rows<D> w;
   const int64_t i_row = i_wg + wave * 32 + n;
-  const bool live = i_row < rows && r0 + i_row >= 0 && r0 + i_row < a.T;
+  const bool live = i_row < rows && r0 + i_row < a.T;
   w.limit = live && keys ? len - rows + i_row : -1;
   const uint16_t* qp = a.q + (live ? r0 + i_row : 0) * a.q_stride + (int64_t)head * D + 8 * h;
 #pragma unroll

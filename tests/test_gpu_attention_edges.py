@@ -9,8 +9,8 @@ import torch
 import attn_ref as ref
 import quantized_expert_ffn_router_amd as q
 from attn_ref import BF16, NVFP4, Q8_0
-from test_gpu_attention import (FMT, Setup, append_inputs, check_append, check_decode, run_append,
-                                run_decode)
+from test_gpu_attention import (FMT, Setup, append_inputs, check_append, check_decode, check_prompt, run_append,
+                                run_decode, run_prompt)
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,19 @@ def test_append_rows_before_row_0_are_left_out(fmt):
     norm = [np.ones(64, np.float32)] * 2
     got_q, got_k, _ = run_append(s, 4, qkv, norm, 32, 0, freq, 1.0)
     check_append(s, 4, qkv, norm, 32, 0, freq, 1.0, got_q, got_k)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prompt_rows_before_row_0_are_left_out(D):
+    """Sequences whose first row lies before row 0, behind longer keys or not: the
+    rows inside are answered at their own positions, a row alone in the first
+    tile's place among them."""
+    rng = np.random.default_rng(D)
+    for first, ends, keys in ((-127, [2], [129]), (-1000, [130, 180], [1130, 60]), (-3, [40, 41, 300], [20, 1, 259])):
+        print("prompt, rows before row 0", D, first, ends, flush=True)
+        T, ks = ends[-1] + 1, np.concatenate([[0], np.cumsum(keys)]).tolist()
+        qv = ref.bf16_bits(rng.standard_normal((T, 2 * D)))
+        kv, vv = (ref.bf16_bits(rng.standard_normal((ks[-1], D))) for _ in range(2))
+        got = run_prompt(2, 1, D, [first, *ends], ks, T, ks[-1], qv, kv, vv)
+        check_prompt(2, 1, D, [0, *ends], ks, qv, kv, vv, got)
+        assert (got[ends[-1]:] == ref.bf16_bits([7.0])[0]).all()
