@@ -504,8 +504,8 @@ moe_status moe_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const moe
 /* The cache read back as bf16 rows (rounded once where the format's values
  * need it), for prompt chunks that attend to a cached prefix.  Token j of
  * sequence b, first[b] <= j < kv_len[b], goes to row out_start[b] + j -
- * first[b] of k_out and v_out (n_kv * D wide), as long as that row is below
- * out_start[b+1] and R.  first: device int32 [n_seq], or NULL: 0.  out_start:
+ * first[b] of k_out and v_out (n_kv * D wide), as long as there is such a token
+ * (0 <= j) and row (0 <= row < R) and the row is below out_start[b+1].  first: device int32 [n_seq], or NULL: 0.  out_start:
  * device int32 [n_seq + 1], ascending.  k_out or v_out may be NULL.  row_start
  * of the batch is not read. */
 moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int32_t* first,

@@ -521,16 +521,19 @@ __global__ __launch_bounds__(256) void k_kv_read(ReadArgs a) {
   const int unit = (int)blockIdx.x * 4 + wave, h = blockIdx.y;
   // the sequence that holds this unit: tokens f.. and units of its span, summed
   int before = 0, u = -1, b = -1;
-  int64_t f = 0, end = 0, out = 0;
+  int64_t f = 0, end = 0, out = 0;  // first token, the one after the last, row of token 0
   for (int i0 = 0; i0 < a.s.n_seq; i0 += 64) {
     const int i = min(i0 + lane, a.s.n_seq - 1);
-    int from = (a.first ? a.first : a.s.kv_len)[i], len = a.s.kv_len[i];
+    int begin = (a.first ? a.first : a.s.kv_len)[i], len = a.s.kv_len[i];
     int o0 = a.out_start[i], o1 = a.out_start[i + 1];
-    loaded(from, len, o0, o1);
-    from = a.first ? max(from, 0) : 0;
-    const int64_t stop = min((int64_t)len, from + max((int64_t)o1 - o0, (int64_t)0));
+    loaded(begin, len, o0, o1);
+    if (!a.first) begin = 0;
+    // (tokens before the sequence's first, or whose row lies before row 0, are left out)
+    const int64_t at_0 = (int64_t)begin - o0;  // the token of row 0
+    const int64_t from = max(max((int64_t)begin, at_0), (int64_t)0);
+    const int64_t stop = min((int64_t)len, at_0 + o1);
     const int sum = wave_incl_scan(
-        i0 + lane < a.s.n_seq && stop > from ? (int)((stop - 1) >> 4) - (from >> 4) + 1 : 0);
+        i0 + lane < a.s.n_seq && stop > from ? (int)(((stop - 1) >> 4) - (from >> 4)) + 1 : 0);
     const uint64_t past = __ballot(before + sum > unit);
     if (!past) {
       before += __builtin_amdgcn_readlane(sum, 63);
@@ -539,9 +542,9 @@ __global__ __launch_bounds__(256) void k_kv_read(ReadArgs a) {
     const int l = __ffsll((unsigned long long)past) - 1;
     if (l > 0) before += __builtin_amdgcn_readlane(sum, l - 1);
     b = i0 + l;
-    f = __builtin_amdgcn_readlane(from, l);
-    out = __builtin_amdgcn_readlane(o0, l);
-    end = min((int64_t)__builtin_amdgcn_readlane(len, l), f + __builtin_amdgcn_readlane(o1, l) - out);
+    f = __builtin_amdgcn_readlane((int)from, l);  // (both fit: from < stop <= len)
+    end = __builtin_amdgcn_readlane((int)stop, l);
+    out = (int64_t)__builtin_amdgcn_readlane(o0, l) - __builtin_amdgcn_readlane(begin, l);
     u = unit - before;
     break;
   }
@@ -551,7 +554,7 @@ __global__ __launch_bounds__(256) void k_kv_read(ReadArgs a) {
   const int P = 1 << a.s.log2P, o = (int)(t0 & (P - 1));
   const KvLayout lay = kv_layout(FMT, D, P);
   const uint8_t* blk = a.pool + (size_t)max(page, 0) * ((size_t)a.n_kv * lay.head) + (size_t)h * lay.head;
-  const int64_t row0 = out + t0 - f;
+  const int64_t row0 = out + t0;
   const auto wanted = [&](int j) {  // token j of the unit
     return t0 + j >= f && t0 + j < end && row0 + j >= 0 && row0 + j < a.R;
   };

@@ -9,8 +9,8 @@ import torch
 import attn_ref as ref
 import quantized_expert_ffn_router_amd as q
 from attn_ref import BF16, NVFP4, Q8_0
-from test_gpu_attention import (FMT, Setup, append_inputs, check_append, check_decode, check_prompt, run_append,
-                                run_decode, run_prompt)
+from test_gpu_attention import (FMT, Setup, append_inputs, bits, check_append, check_decode, check_prompt, i32,
+                                run_append, run_decode, run_prompt)
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,28 @@ def test_prompt_rows_before_row_0_are_left_out(D):
         got = run_prompt(2, 1, D, [first, *ends], ks, T, ks[-1], qv, kv, vv)
         check_prompt(2, 1, D, [0, *ends], ks, qv, kv, vv, got)
         assert (got[ends[-1]:] == ref.bf16_bits([7.0])[0]).all()
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("first,start", [
+    ([0, 60], [-370, 30, 40]),   # the first rows before row 0
+    ([17, 0], [-30, -3, 40]),    # a whole sequence, and a few rows of the next
+    ([-5, 65], [0, 20, 40]),     # tokens before the sequence's first: their rows stay as they are
+    ([-40, -3], [-20, 10, 60]),  # both; rows from R on
+    ([-(2 ** 31), 2 ** 31 - 1], [-(2 ** 31), 0, 40]),
+])
+def test_read_outside_the_rows_and_tokens(fmt, first, start):
+    print("read outside", FMT[fmt], first, start, flush=True)
+    D, R = 64, 40
+    s = Setup(fmt, 2, D, 32, [400, 70], [0, 0], seed=8)
+    ko, vo = (torch.full((R, 2 * D), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    q.moe_kv_read(s.cache, s.seqs, i32(first), i32(start), R, ko, 2 * D, vo, 2 * D)
+    torch.cuda.synchronize()
+    for w, got in ((0, bits(ko)), (1, bits(vo))):
+        want = np.full((R, 2 * D), ref.bf16_bits([7.0])[0], np.uint16)
+        for b in range(2):
+            for r in range(max(start[b], 0), min(start[b + 1], R)):
+                j = first[b] + r - start[b]
+                if 0 <= j < s.lens[b]:
+                    want[r] = np.concatenate([ref.bf16_bits(s.ref.get(w, s.table[b, j // 32], j % 32, h)) for h in range(2)])
+        assert np.array_equal(ref.bf16_val(got), ref.bf16_val(want)), w
