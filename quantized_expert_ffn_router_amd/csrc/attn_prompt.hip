@@ -403,10 +403,12 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
   const int n_full = lo < kBN - 1 ? 0 : (int)min((lo + 1) / kBN, (int64_t)n_tiles);
 
   Rows<D> w;
-  const int64_t i_row = i_wg + wave * 32 + n;
-  const bool live = i_row < rows && r0 + i_row < a.T;
+  const int64_t i_row = i_wg + wave * 32 + n, last_row = min(rows, a.T - r0) - 1;
+  const bool live = i_row <= last_row;
   w.limit = live && keys ? len - rows + i_row : -1;
-  const uint16_t* qp = a.q + (live ? r0 + i_row : 0) * a.q_stride + (int64_t)head * D + 8 * h;
+  // (a lane without a row takes the tile's last one: another tile's may be
+  // overwritten meanwhile, where the output takes the queries' place)
+  const uint16_t* qp = a.q + (r0 + min(i_row, last_row)) * a.q_stride + (int64_t)head * D + 8 * h;
 #pragma unroll
   for (int s = 0; s < KS; ++s) w.qf[s] = *reinterpret_cast<const v4u*>(qp + 16 * s);
   w.places(lane);
@@ -480,7 +482,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_prompt(Pr
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int i = 0; i < 16; ++i) bad = fmaf(w.o[j][i], 0.0f, bad);  // NaN if one is not finite
-  if (__syncthreads_or(bad != 0.0f)) {
+  if (__syncthreads_or(live && bad != 0.0f)) {
     careful_pass<D, WAVES>(w, k_even, v_even, K, V, a.c, n_tiles, lo + wave * 32, wave, lane);
     w.finish();
   }

@@ -123,3 +123,27 @@ def test_read_outside_the_rows_and_tokens(fmt, first, start):
                 if 0 <= j < s.lens[b]:
                     want[r] = np.concatenate([ref.bf16_bits(s.ref.get(w, s.table[b, j // 32], j % 32, h)) for h in range(2)])
         assert np.array_equal(ref.bf16_val(got), ref.bf16_val(want)), w
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prompt_tiles_do_not_depend_on_other_tiles_rows(D):
+    """Partly filled tiles of three prompts, the first row of all being NaN, or far
+    larger than the others: the rows of the other tiles keep their bits, also with
+    the output in the queries' place.  (The keys of a prompt's first tile are
+    small, so a pass with a running maximum would round the weights differently.)"""
+    rng = np.random.default_rng(D)
+    qs = [0, 130, 330, 375]
+    T = qs[-1]
+    small = np.concatenate([np.arange(n) < 64 for n in np.diff(qs)])[:, None]
+    qv = ref.bf16_bits(2 * rng.standard_normal((T, 2 * D)))
+    kv = ref.bf16_bits(rng.standard_normal((T, D)) * np.where(small, 0.05, 1.0))
+    vv = ref.bf16_bits(rng.standard_normal((T, D)))
+    want = run_prompt(2, 1, D, qs, None, T, T, qv, kv, vv)
+    check_prompt(2, 1, D, qs, None, qv, kv, vv, want, [0, 64, 127, 128, 129, 199, 44])
+    for row0 in (np.full(2 * D, math.nan), 1e5 * ref.bf16_val(qv[0])):
+        x = qv.copy()
+        x[0] = ref.bf16_bits(row0)
+        for in_place in (False, True, True, True):
+            print("prompt, other tiles", D, row0[0], in_place, flush=True)
+            got = run_prompt(2, 1, D, qs, None, T, T, x, kv, vv, in_place=in_place)
+            assert np.array_equal(got[128:], want[128:])
