@@ -40,6 +40,14 @@ constexpr int kStreamed = 2;         // cache policy of loads that are read once
 constexpr float kNone = -3.0e38f;   // running maximum before any token
 constexpr float kGrow = 8.0f;       // log2 headroom before the accumulators are rescaled
 
+// Weights are relative to the running maximum less this (log2).  With fp16 weights
+// (to 65504) the largest is 2^7 to 2^15, so that one vanishes only below 2^-32 of
+// the largest, not 2^-25: 380 tokens of weight 2^-26 behind one of weight 1 and
+// value 0 lose a quarter of their sum without, those that share its wave.  bf16
+// weights have fp32's exponents.
+template <int FMT>
+constexpr float kRaise = FMT == MOE_FMT_BF16 ? 0.0f : 7.0f;
+
 struct DecodeArgs {
   const uint8_t* pool;
   const uint16_t* q;
@@ -432,8 +440,9 @@ __device__ __forceinline__ v4f weighted(const Unit<FMT, D>& c, int j, v4u p, v4f
 }
 
 // Two softmax weights as a pair of the product's operand type, rounded to
-// nearest even (half a step of weights between 0 and 2^kGrow), and their sum
-// added to l: of the rounded weights, so that rounding does not shift the mean.
+// nearest even (half a step, 2^-11 or 2^-8: the types that meet the matrix units),
+// and their sum added to l: of the rounded weights, so that rounding does not shift
+// the mean.
 template <int FMT>
 __device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
   if constexpr (FMT == MOE_FMT_BF16) {
@@ -449,7 +458,7 @@ __device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
 }
 
 // What a wave carries for one tile of NT * 16 query rows (a lane column is one
-// row of each 16): running maximum, sum, and the weighted values.
+// row of each 16): running maximum (less kRaise), sum, and the weighted values.
 template <int FMT, int D, int NT>
 struct Carry {
   static constexpr int KS = D / 32, NJ = D / 16;
@@ -477,8 +486,8 @@ struct Carry {
       float mx = fmaxf(fmaxf(x[r][0][0], x[r][0][1]), fmaxf(x[r][0][2], x[r][0][3]));
       mx = fmaxf(mx, fmaxf(fmaxf(x[r][1][0], x[r][1][1]), fmaxf(x[r][1][2], x[r][1][3])));
       mx = groups_max(mx) * qs[r];
-      if (__any(mx > m[r] + kGrow)) {
-        const float mn = fmaxf(m[r], mx), al = __builtin_amdgcn_exp2f(m[r] - mn);
+      if (__any(mx > m[r] + (kRaise<FMT> + kGrow))) {
+        const float mn = fmaxf(m[r], mx - kRaise<FMT>), al = __builtin_amdgcn_exp2f(m[r] - mn);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -777,9 +786,9 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
     if (rr >= inside * a.G) continue;
     if (d0 == 0 && sp == 0 && a.S > 1) a.part_n[orow * a.n_q + h] = it.splits;
     if (it.splits == 1) {
-      const float inv = (int64_t)len - rows + i < 0 ? 0.0f : a.v_ts / L;
+      const float inv = (int64_t)len - rows + i < 0 ? 0.0f : 1.0f / L;
 #pragma unroll
-      for (int j = 0; j < E; ++j) acc[j] *= inv;
+      for (int j = 0; j < E; ++j) acc[j] = acc[j] * inv * a.v_ts;
       store_row<E>(a.out + orow * a.out_stride + h * D + d0, acc);
     } else {
       const int64_t at = (orow * a.n_q + h) * a.S + sp;
@@ -874,10 +883,10 @@ __global__ __launch_bounds__(256) void k_attn_join(DecodeArgs a) {
       o.x += w.x; o.y += w.y; o.z += w.z; o.w += w.w;
       L += l_s[i];
     }
-    const float inv = (int64_t)q.len - q.rows + (t - q.r0) < 0 ? 0.0f : a.v_ts / L;
+    const float inv = (int64_t)q.len - q.rows + (t - q.r0) < 0 ? 0.0f : 1.0f / L, ts = a.v_ts;
     uint16_t* d = a.out + t * a.out_stride + (int64_t)h * D + 4 * x;
-    *reinterpret_cast<uint2*>(d) =
-        make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+    *reinterpret_cast<uint2*>(d) = make_uint2(bf16_pair(o.x * inv * ts, o.y * inv * ts),
+                                              bf16_pair(o.z * inv * ts, o.w * inv * ts));
   }
 }
 

@@ -147,3 +147,51 @@ def test_prompt_tiles_do_not_depend_on_other_tiles_rows(D):
             print("prompt, other tiles", D, row0[0], in_place, flush=True)
             got = run_prompt(2, 1, D, qs, None, T, T, x, kv, vv, in_place=in_place)
             assert np.array_equal(got[128:], want[128:])
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("L", [380, 2001])
+@pytest.mark.parametrize("gap", [12, 20, 24, 26])
+def test_decode_small_weights_beside_a_large_one(fmt, L, gap):
+    """The first token outweighs every other 2^gap to 2^(5 gap / 6) times and has the
+    value 0, so that the output is what the others add up to.  A weight is off by
+    2^-11 of it (2^-8 for the 16-bit cache) or, below fp16's normal numbers, by
+    2^-25 where the largest is 2^7 or more: 2^-32 of the largest."""
+    print("small weights", FMT[fmt], L, gap, flush=True)
+    D = 64
+    s = Setup(fmt, 1, D, 32, [L], [1], seed=5, pad_rows=0)
+    rng = np.random.default_rng(6)
+    for j in range(L):
+        k, v = np.zeros(D), 0.5 + rng.random(D)
+        k[0], k[1] = 0.5 * rng.integers(0, 3), 6.0  # (the same scale for every token)
+        if j == 0:
+            k[0], v[:] = 6.0, 0.0
+        for w, x in ((0, k), (1, v)):
+            s.ref.put(w, s.table[0, j // 32], j % 32, 0, ref.bf16_bits(x))
+    s.to_device()
+    x = np.zeros((1, D))
+    x[0, 0] = gap * math.log(2) / 6 * math.sqrt(D)
+    qv = ref.bf16_bits(x)
+    have = ref.bf16_val(run_decode(s, 1, qv)[0])
+    k, v = s.ref.tokens(s.table[0], L, 0)
+    want, pv, qk = ref.attend(ref.bf16_val(qv[0]), k, v, L - 1, float(np.float32(D ** -0.5)))
+    bound = ref.attend_bound(want, pv, qk, L, 0.0, D, fmt)  # (without its own term for small weights)
+    if fmt != BF16:
+        bound += (np.abs(v).sum(0) + L * np.abs(want)) * 2.0 ** -32
+    assert (np.abs(have - want) <= bound).all(), float((np.abs(have - want) / bound).max())
+
+
+@pytest.mark.parametrize("ts", [2.0 ** -118, 2.0 ** 100])
+def test_decode_value_scales_of_any_size(ts):
+    """The values' scale of the whole cache is applied to the weighted mean: with
+    values and scale times a power of two, so are the outputs, up to a step of
+    bf16's subnormal numbers."""
+    got = []
+    for t in (1.0, ts):
+        print("value scale", t, flush=True)
+        s = Setup(NVFP4, 1, 64, 32, [40, 700], [1, 1], seed=5, pad_rows=0, v_ts=t, vary=(1.0, t))
+        qv = ref.bf16_bits(s.rng.standard_normal((s.T, 2 * 64)))
+        got.append(ref.bf16_val(run_decode(s, 2, qv)))
+        if t == 1.0:
+            check_decode(s, 2, qv, ref.bf16_bits(got[0]))
+    assert (np.abs(got[1] - ts * got[0]) <= 2.0 ** -133).all()
