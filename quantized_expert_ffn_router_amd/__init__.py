@@ -498,6 +498,9 @@ class KvCache:
         self.pool = torch.empty(n_pages * self.page_bytes, dtype=torch.uint8, device=dev)
         t = lambda a, dt: None if a is None else torch.as_tensor(a, dtype=dt, device=dev).contiguous()  # noqa: E731
         self.q_norm, self.k_norm = t(q_norm, torch.float32), t(k_norm, torch.float32)
+        for name, w in (("q_norm", self.q_norm), ("k_norm", self.k_norm)):
+            if w is not None and w.numel() != D:
+                raise MoeError(MOE_ERR_INVALID_ARG, f"KvCache: {name} has {w.numel()} weights, not D={D}")
         freqs, scale = (None, 1.0) if rope is None else rope
         self.inv_freq = t(freqs, torch.float64)
         rot = 0 if freqs is None else 2 * len(freqs)
@@ -516,6 +519,7 @@ class AttnBuffers:
         import torch
         dev = torch.device(device)
         self.T_max = T_max
+        self.heads = (cache.n_q, cache.n_kv, cache.D)
         i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)  # noqa: E731
         bf16 = lambda heads: torch.empty((T_max, heads * cache.D), dtype=torch.bfloat16, device=dev)  # noqa: E731
         self.row_start, self.kv_len, self.page_table = i32(n_seq + 1), i32(n_seq), i32(n_seq, max_pages)
@@ -525,6 +529,20 @@ class AttnBuffers:
         self.q, self.k, self.out = bf16(cache.n_q), bf16(cache.n_kv), bf16(cache.n_q)
         self.ws_bytes = moe_attn_workspace_bytes(cache.desc, cache.n_q, n_seq, T_max, self.max_len)
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=dev)
+
+
+def _check_rows(t, numel, device, name):
+    """t: contiguous bf16 values (or their bits) on the cache's device, numel of
+    them or more.  (An address cannot be checked.)"""
+    import torch
+    if isinstance(t, int):
+        return
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or not t.is_contiguous():
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: {name} must be bf16 and contiguous")
+    if t.numel() < numel:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: {name} has {t.numel()} elements of {numel}")
+    if t.device != device:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: {name} is on {t.device}, the cache on {device}")
 
 
 def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: float, prompt=None,
@@ -542,6 +560,18 @@ def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: floa
         raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: T={T} > T_max={buf.T_max}")
     if prompt is not None and min(prompt[2].numel(), prompt[3].numel()) < prompt[1] * kw:
         raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: k, v are smaller than Tk={prompt[1]} rows")
+    if buf.heads != (cache.n_q, cache.n_kv, D):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: buffers for heads {buf.heads}, "
+                       f"the cache has {(cache.n_q, cache.n_kv, D)}")
+    dev = cache.pool.device
+    _check_rows(qkv, T * (qw + 2 * kw), dev, "qkv")
+    if prompt is not None:
+        import torch
+        start = prompt[0]
+        if start.dtype != torch.int32 or start.numel() <= buf.seqs.n_seq or not start.is_contiguous() or start.device != dev:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: kv_start must be int32 [{buf.seqs.n_seq + 1}] on {dev}")
+        _check_rows(prompt[2], prompt[1] * kw, dev, "k")
+        _check_rows(prompt[3], prompt[1] * kw, dev, "v")
     moe_kv_append(c, cache.qkv_desc, buf.seqs, qkv, qw + 2 * kw, T, None, buf.q, qw, buf.k, kw, stream)
     if prompt is None:
         moe_attn_decode(c, buf.seqs, cache.n_q, buf.q, qw, T, max_len, scale, buf.out, qw, buf.ws,
