@@ -489,7 +489,7 @@ moe_status moe_rope_freqs(int32_t kind, int32_t rot_dim, double base, double fac
  *   q_out: bf16 [T] rows of n_q * D, q_stride apart; k_out: the same with
  *   n_kv * D, or NULL (for moe_attn_prompt, whose values may stay in qkv).
  *   q_out and k_out may be the query and key parts of qkv itself (the same
- *   addresses and stride); other overlaps are not allowed.
+ *   addresses and stride); other overlaps are refused.
  *   Keys and values go into the cache at the rows' tokens.  Rows at or behind
  *   row_start[n_seq] are left as they are.  pos: device int32 [T], the rows'
  *   rotary positions, or NULL: the token's index in its sequence.  The page
@@ -521,7 +521,8 @@ moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int3
  * keys, values and softmax weights meet the matrix units as fp16 (block
  * formats; the query rows scaled by a power of two each) or bf16 (16-bit
  * cache).  What a row does not see has no influence on it, also if it is NaN or infinite.
- * q, out: bf16 [T] rows of n_q * D (out may be q).  max_len: the longest
+ * q, out: bf16 [T] rows of n_q * D (out may be q, with the same stride; other
+ * overlaps are refused).  max_len: the longest
  * kv_len expected; it decides how the work is split, never the result's
  * validity (0: max_pages * page_tokens).  ws: moe_attn_workspace_bytes of the
  * same cache, heads and n_seq, with this T and max_len or larger ones; nothing
@@ -541,7 +542,8 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
  * rounding and empty rows as moe_attn_decode, with bf16 operands.
  * q_start, kv_start: device int32 [n_seq + 1], ascending; kv_start NULL: the
  * queries' own.  q: bf16 [T] rows of n_q * D; k, v: bf16 [Tk] rows of n_kv * D;
- * out: bf16 [T] rows of n_q * D (may be q, with the same stride).  k_stride and
+ * out: bf16 [T] rows of n_q * D (may be q, with the same stride; other overlaps
+ * are refused).  k_stride and
  * v_stride: at most 2^24.  Rows outside
  * the sequences are left as they are; indices are held inside T and Tk: of a
  * sequence with rows outside 0..T those inside are answered, one with keys

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <utility>
 
 #include "attn_common.h"
 #include "gemv_common.h"
@@ -576,6 +577,31 @@ moe_status check_rows(const void* p, int64_t stride, int64_t width, const char* 
   return check_aligned(p, name, where);
 }
 
+struct RowBlock {  // n rows of `width` 16-bit elements, stride apart
+  const void* p;
+  int64_t stride, width, n;
+};
+
+bool share_elements(RowBlock a, RowBlock b) {
+  if (a.n < 1 || b.n < 1) return false;
+  if ((uintptr_t)a.p > (uintptr_t)b.p) std::swap(a, b);
+  const int64_t at = (int64_t)(((uintptr_t)b.p - (uintptr_t)a.p) / 2);  // of b's first row, from a's
+  if (at >= (a.n - 1) * a.stride + a.width) return false;
+  // rows inside one another's range: side by side at the same stride, or not known to be apart
+  if (a.stride != b.stride) return true;
+  const int64_t d = at % a.stride;
+  return d < a.width || d + b.width > a.stride;
+}
+
+// An output's rows are not those of an input, except in the input's own place.
+moe_status check_apart(RowBlock out, RowBlock in, bool in_place, const char* out_name,
+                       const char* in_name, const char* where) {
+  if (in_place && out.p == in.p && (out.stride == in.stride || out.n == 1)) return MOE_OK;
+  if (!share_elements(out, in)) return MOE_OK;
+  return fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s%s", where, out_name, in_name,
+              in_place ? " other than at its address and stride" : "");
+}
+
 moe_status check_cache(const moe_kv_cache* c, const char* where) {
   CHECK_PTR(c, where);
   moe_status st = check_cache_shape(c->fmt, c->n_kv, c->D, c->page_tokens, where);
@@ -701,6 +727,13 @@ moe_status moe_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const moe
   if (k_out && (st = check_rows(k_out, k_stride, kw, "k_out", W)) != MOE_OK) return st;
   if ((st = check_aligned(p->q_norm, "q_norm", W)) != MOE_OK) return st;
   if ((st = check_aligned(p->k_norm, "k_norm", W)) != MOE_OK) return st;
+  const RowBlock in{qkv, qkv_stride, qw + 2 * kw, T}, qo{q_out, q_stride, qw, T}, ko{k_out, k_stride, kw, T};
+  if ((st = check_apart(qo, in, true, "q_out", "qkv", W)) != MOE_OK) return st;
+  if (k_out) {
+    if (k_out != qkv + qw || (k_stride != qkv_stride && T > 1))  // (the keys' own place)
+      if ((st = check_apart(ko, in, false, "k_out", "qkv", W)) != MOE_OK) return st;
+    if ((st = check_apart(ko, qo, false, "k_out", "q_out", W)) != MOE_OK) return st;
+  }
   return hip_status(W, moe::launch_kv_append(c, p, s, qkv, qkv_stride, T, pos, q_out, q_stride,
                                              k_out, k_stride, stream));
 }
@@ -720,6 +753,9 @@ moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int3
   const int64_t kw = (int64_t)c->n_kv * c->D;
   if (k_out && (st = check_rows(k_out, k_stride, kw, "k_out", W)) != MOE_OK) return st;
   if (v_out && (st = check_rows(v_out, v_stride, kw, "v_out", W)) != MOE_OK) return st;
+  if (k_out && v_out &&
+      (st = check_apart({k_out, k_stride, kw, R}, {v_out, v_stride, kw, R}, false, "k_out", "v_out", W)) != MOE_OK)
+    return st;
   return hip_status(W, moe::launch_kv_read(c, s, first, out_start, R, k_out, k_stride, v_out,
                                            v_stride, stream));
 }
@@ -769,6 +805,7 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu", W, ws_bytes, need);
     if ((st = check_aligned(ws, "ws", W)) != MOE_OK) return st;
   }
+  if ((st = check_apart({out, out_stride, qw, T}, {q, q_stride, qw, T}, true, "out", "q", W)) != MOE_OK) return st;
   return hip_status(W, moe::launch_attn_decode(c, s, n_q, q, q_stride, T, max_len, scale, out,
                                                out_stride, ws, stream));
 }
@@ -801,6 +838,12 @@ moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
     // a tile of 64 rows is read with 32-bit byte offsets
     if (k_stride > (1 << 24) || v_stride > (1 << 24))
       return fail(MOE_ERR_UNSUPPORTED, "%s: k and v strides are at most 2^24 elements", W);
+  }
+  const RowBlock o{out, out_stride, qw, T};
+  if ((st = check_apart(o, {q, q_stride, qw, T}, true, "out", "q", W)) != MOE_OK) return st;
+  if (Tk > 0) {
+    if ((st = check_apart(o, {k, k_stride, kw, Tk}, false, "out", "k", W)) != MOE_OK) return st;
+    if ((st = check_apart(o, {v, v_stride, kw, Tk}, false, "out", "v", W)) != MOE_OK) return st;
   }
   return hip_status(W, moe::launch_attn_prompt(n_q, n_kv, D, n_seq, q_start, kv_start, T, Tk, q,
                                                q_stride, k, k_stride, v, v_stride, scale, out,

@@ -254,3 +254,26 @@ def test_reference_attention_and_rotation_against_torch():
         assert np.array_equal(a[0][32:], x[32:])
     n = ref.norm_rotate(np.full(64, 3.0), np.ones(64), 0.0, 0, 0, 0, f, 1.0)
     assert np.allclose(n, 1.0)
+
+
+# ------------------------------------------------- outputs in their inputs' place
+
+def refused(call, **kw):
+    return call(**kw) == BAD and "overlaps" in q.last_error()
+
+
+def test_outputs_overlap_inputs_only_in_their_own_place():
+    w = 12 * 128  # elements of a row: 8 query, 2 key and 2 value heads of 128
+    behind = A + 2 * 4 * w  # the first address behind the 4 rows
+    for kw in (dict(qs=w + 8), dict(qo=A + 16, qs=w), dict(qo=A - 16, qs=w), dict(qo=A + 2 * 1016, T=1),
+               dict(qo=A + 2 * 3 * w + 16), dict(qs=w, ko=A, ks=w), dict(qs=w, ko=A + 2 * 1024, ks=w + 8),
+               dict(qs=w, ko=A + 2 * 1024 + 16, ks=w), dict(qo=behind, ko=behind + 2 * 1016, ks=1024)):
+        assert refused(append, **kw), (kw, q.last_error())
+    for out, x, os, xs in ((A, A, 1032, 1024), (A, A + 16, 1024, 1024), (A + 16, A, 1024, 1024), (A + 16, A, 1200, 1200),
+                           (A + 2 * 1104, A, 1200, 1200), (A + 2 * 1104, A, 1600, 1200)):
+        assert refused(decode, out=out, x=x, os=os, xs=xs), (out, x, os, xs, q.last_error())
+        assert refused(prompt, out=out, x=x, os=os, xst=xs, k=A << 9, v=A << 9), (out, x, os, xs, q.last_error())
+    for kw in (dict(v=A + 2 * 1016), dict(v=A, vst=1024), dict(v=A + 2 * 3 * 1024, vst=1024), dict(k=A + 16), dict(k=A, kst=1024)):
+        assert refused(prompt, **{"k": A << 9, "v": A << 9, **kw}), (kw, q.last_error())
+    for kw in (dict(), dict(vo=A + 16), dict(vo=A + 2 * 3 * 256, vs=512), dict(ks=512, vs=512, vo=A + 2 * 248)):
+        assert refused(read, **kw), (kw, q.last_error())

@@ -195,3 +195,40 @@ def test_decode_value_scales_of_any_size(ts):
         if t == 1.0:
             check_decode(s, 2, qv, ref.bf16_bits(got[0]))
     assert (np.abs(got[1] - ts * got[0]) <= 2.0 ** -133).all()
+
+
+def test_outputs_beside_their_inputs_in_one_buffer():
+    """Rows of one wide buffer may hold inputs and outputs side by side: the same
+    bits as with buffers of their own."""
+    D, n_q, n_kv, P, L = 64, 4, 2, 32, 50
+    qw, kw = n_q * D, n_kv * D
+    gen = torch.Generator(device=dev).manual_seed(3)
+    qkv = torch.randn(L, qw + 2 * kw, generator=gen, device=dev).bfloat16()
+    f = torch.from_numpy(q.moe_rope_freqs(q.MOE_ROPE_PLAIN, D, 10000.0)[0]).to(dev)
+    d = q.QkvDesc(n_q, 1e-6, None, None, D, 0, f.data_ptr(), 1.0)
+    got = []
+    for wide in (False, True):
+        print("one buffer", wide, flush=True)
+        cache = q.KvCache(Q8_0, n_q, n_kv, D, P, 2)
+        buf = q.AttnBuffers(cache, 1, L, 2)
+        buf.page_table.copy_(i32([[1, 0]]))
+        buf.row_start.copy_(i32([0, L]))
+        buf.kv_len.copy_(i32([L]))
+        widths = [qw + 2 * kw, qw, kw, kw, kw, qw, qw]
+        if wide:  # projections, queries, keys, keys and values read back, two outputs
+            st, whole = sum(widths), torch.full((L, sum(widths)), 7.0, dtype=torch.bfloat16, device=dev)
+            parts = list(torch.split(whole, widths, 1))
+        else:
+            parts = [torch.full((L, n), 7.0, dtype=torch.bfloat16, device=dev) for n in widths]
+        strides = [st if wide else n for n in widths]
+        parts[0].copy_(qkv)
+        x, qo, ko, kr, vr, o1, o2 = parts
+        xs, qs, ks, krs, vrs, s1, s2 = strides
+        q.moe_kv_append(cache.desc, d, buf.seqs, x, xs, L, None, qo, qs, ko, ks)
+        q.moe_kv_read(cache.desc, buf.seqs, None, buf.row_start, L, kr, krs, vr, vrs)
+        q.moe_attn_prompt(n_q, n_kv, D, 1, buf.row_start, None, L, L, qo, qs, kr, krs, vr, vrs, 0.125, o1, s1)
+        q.moe_attn_decode(cache.desc, buf.seqs, n_q, qo, qs, L, 0, 0.125, o2, s2, buf.ws, buf.ws_bytes)
+        torch.cuda.synchronize()
+        got.append([p.clone() for p in parts])
+    for a, b in zip(*got):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)
