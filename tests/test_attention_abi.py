@@ -277,3 +277,38 @@ def test_outputs_overlap_inputs_only_in_their_own_place():
         assert refused(prompt, **{"k": A << 9, "v": A << 9, **kw}), (kw, q.last_error())
     for kw in (dict(), dict(vo=A + 16), dict(vo=A + 2 * 3 * 256, vs=512), dict(ks=512, vs=512, vo=A + 2 * 248)):
         assert refused(read, **kw), (kw, q.last_error())
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16])
+def test_pages_made_at_once_read_back_byte_by_byte(fmt):
+    import attn_pages
+    for n_kv, D, P in ((2, 64, 32), (1, 128, 64), (3, 256, 32)):
+        gen = torch.Generator().manual_seed(D)
+        lens = [70, 1, 33]
+        pool, table, kv = attn_pages.make(fmt, n_kv, D, P, lens, gen, "cpu", 0.75, 1.5)
+        c = ref.Cache(fmt, n_kv, D, P, pool.numel() // q.moe_kv_page_bytes(fmt, n_kv, D, P), 0.75, 1.5)
+        c.pool = pool.numpy()
+        for b, L in enumerate(lens):
+            for h in range(n_kv):
+                got = c.tokens(table[b].numpy(), L, h)
+                for w in (0, 1):
+                    assert np.array_equal(got[w], kv[b][w][:, h].numpy()), (D, b, h, w)
+    x, k, v = (torch.randn(4, 64, dtype=torch.float64, generator=gen), *(torch.randn(20, 64, dtype=torch.float64, generator=gen) for _ in range(2)))
+    want, _ = attn_pages.attend(x, k, v, torch.tensor([0, 5, 19, 11]), 0.2, fmt, 64)
+    for i, lim in enumerate((0, 5, 19, 11)):
+        assert np.allclose(want[i].numpy(), ref.attend(x[i].numpy(), k.numpy(), v.numpy(), lim, 0.2)[0], atol=1e-13)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16])
+def test_a_part_of_a_long_sequence_left_out_is_outside_the_bounds(fmt):
+    import attn_pages
+    gen = torch.Generator().manual_seed(1)
+    for D in (64, 128, 256):
+        L = 1 << 14
+        k, v = attn_pages.make(fmt, 1, D, 64, [L], gen, "cpu")[2][0]
+        x = 1.5 * torch.randn(2, D, dtype=torch.float64, generator=gen)
+        want, bound = attn_pages.attend(x, k[:, 0], v[:, 0], torch.tensor([L - 1, L - 1]), D ** -0.5, fmt, 4096)
+        for part in (0, 100, 255):
+            keep = torch.arange(L) * 256 // L != part
+            less, _ = attn_pages.attend(x, k[keep, 0], v[keep, 0], torch.tensor([L, L]), D ** -0.5, fmt, 4096)
+            assert (((less - want).abs() / bound).max(1).values > 8).all(), (D, part)

@@ -232,3 +232,51 @@ def test_outputs_beside_their_inputs_in_one_buffer():
         got.append([p.clone() for p in parts])
     for a, b in zip(*got):
         assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("D,n_q,n_kv", [(64, 9, 3), (128, 10, 5), (256, 3, 3)])
+def test_append_in_place_with_whole_quads(fmt, D, n_q, n_kv):
+    """Queries and keys in their own place of the projections, prompts of whole and
+    part quads: cache bytes and rows as stated, the values' part untouched."""
+    print("append in place", FMT[fmt], D, flush=True)
+    s = Setup(fmt, n_kv, D, 32, [13, 43, 3, 8, 70], [13, 38, 5, 8, 2], seed=D, v_ts=1.5, pad_rows=2)
+    qkv = append_inputs(s, n_q, 6)
+    norm = [np.full(D, 1.25, np.float32), np.ones(D, np.float32)]
+    freq, _ = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 32, 10000.0)
+    got_q, got_k, whole = run_append(s, n_q, qkv, norm, 32, 0, freq, 1.0, in_place=True)
+    check_append(s, n_q, qkv, norm, 32, 0, freq, 1.0, got_q, got_k)
+    n = int(s.start[-1])
+    assert np.array_equal(whole[:n, (n_q + n_kv) * D:], qkv[:n, (n_q + n_kv) * D:])
+    assert np.array_equal(whole[n:], qkv[n:])
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+def test_append_of_a_long_prompt_in_place_and_apart(fmt):
+    """4101 rows of two sequences, a workgroup to each four (with few rows the heads of
+    a row are spread over several): the same bits in place and apart."""
+    D, n_q, n_kv, P, rows = 64, 8, 4, 64, [4000, 101]
+    T, w, kw = sum(rows), (n_q + 2 * n_kv) * D, n_kv * D
+    gen = torch.Generator(device=dev).manual_seed(3)
+    x0 = (2 * torch.randn(T, w, generator=gen, device=dev)).bfloat16()
+    rope = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 64, 10000.0)
+    got = []
+    for in_place in (True, False):
+        print("long append", FMT[fmt], in_place, flush=True)
+        cache = q.KvCache(fmt, n_q, n_kv, D, P, 67, np.ones(D), np.ones(D), rope)
+        cache.pool.fill_(0xff)
+        buf = q.AttnBuffers(cache, 2, T, 64)
+        buf.page_table[0, :63] = torch.arange(63, device=dev)
+        buf.page_table[1, :2] = i32([66, 64])
+        buf.row_start.copy_(i32([0, rows[0], T]))
+        buf.kv_len.copy_(i32(rows))
+        x = x0.clone()
+        qo, ko = (x, x.data_ptr() + 2 * n_q * D) if in_place else (torch.empty(T, n_q * D, dtype=torch.bfloat16, device=dev),
+                                                                  torch.empty(T, kw, dtype=torch.bfloat16, device=dev))
+        qs, ks = (w, w) if in_place else (n_q * D, kw)
+        q.moe_kv_append(cache.desc, cache.qkv_desc, buf.seqs, x, w, T, None, qo, qs, ko, ks)
+        torch.cuda.synchronize()
+        assert torch.equal(x[:, n_q * D + kw:], x0[:, n_q * D + kw:])
+        got.append((x[:, :n_q * D], x[:, n_q * D:n_q * D + kw], cache.pool) if in_place else (qo, ko, cache.pool))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
