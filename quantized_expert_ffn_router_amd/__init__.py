@@ -545,6 +545,15 @@ def _check_rows(t, numel, device, name):
         raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: {name} is on {t.device}, the cache on {device}")
 
 
+def _launches_on(device, stream):
+    """Whether a call's kernels run on this device: on the current one, if no
+    stream is given."""
+    import torch
+    if device.type != "cuda":
+        return False
+    return stream is not None or device.index == torch.cuda.current_device()
+
+
 def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: float, prompt=None,
                       max_len=0, stream=None):
     """One layer's attention over the step's rows qkv (bf16 [T][n_q + 2 n_kv][D],
@@ -572,6 +581,10 @@ def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: floa
             raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: kv_start must be int32 [{buf.seqs.n_seq + 1}] on {dev}")
         _check_rows(prompt[2], prompt[1] * kw, dev, "k")
         _check_rows(prompt[3], prompt[1] * kw, dev, "v")
+    if buf.q.device != dev:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: buffers on {buf.q.device}, the cache on {dev}")
+    if T > 0 and not _launches_on(dev, stream):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: the cache is on {dev}, not the current GPU")
     moe_kv_append(c, cache.qkv_desc, buf.seqs, qkv, qw + 2 * kw, T, None, buf.q, qw, buf.k, kw, stream)
     if prompt is None:
         moe_attn_decode(c, buf.seqs, cache.n_q, buf.q, qw, T, max_len, scale, buf.out, qw, buf.ws,

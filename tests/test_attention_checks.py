@@ -68,3 +68,15 @@ def test_a_step_without_rows_passes_the_checks():
     c.desc.pool = (c.desc.pool + 255) & ~255
     for qkv in (rows(0, 12), rows(ROWS, 12), rows(ROWS, 12).view(torch.int16)):
         assert q.attention_forward(c, buf, qkv, 0, 0.125, stream=0) is buf.out
+
+
+def test_a_cache_that_is_not_on_the_current_gpu_is_refused(monkeypatch):
+    """Host memory, buffers elsewhere, and another GPU than the current one."""
+    c, buf = setup()
+    with pytest.raises(q.MoeError, match="the cache is on cpu"):
+        q.attention_forward(c, buf, rows(ROWS, 12), ROWS, 0.125)
+    with pytest.raises(q.MoeError, match="buffers on meta"):
+        q.attention_forward(c, q.AttnBuffers(c, 2, ROWS, 2, device="meta"), rows(ROWS, 12), ROWS, 0.125)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert q._launches_on(torch.device("cuda", 0), None) and not q._launches_on(torch.device("cuda", 1), None)
+    assert q._launches_on(torch.device("cuda", 1), 0x1000) and not q._launches_on(torch.device("cpu"), 0x1000)
