@@ -775,9 +775,9 @@ size_t moe_attn_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_se
   }
   // max_len 0 stands for the page table's capacity, which is not known here:
   // the longest cache gives the largest split.  Fewer rows can need more (they
-  // are split finer); beyond 2^14 (row, head) pairs there are no splits.
+  // are split finer); beyond kSplitPairs there are no splits.
   size_t most = 0;
-  for (int64_t t = 1; t <= T && t * n_q <= 1 << 14; ++t)
+  for (int64_t t = 1; t <= T && t * n_q <= moe::kSplitPairs; ++t)
     most = std::max(most, moe::attn_decode_ws_bytes(c->fmt, c->n_kv, c->D, n_q, n_seq, t,
                                                     max_len ? max_len : INT32_MAX));
   return most;

@@ -147,6 +147,8 @@ hipError_t launch_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const 
 hipError_t launch_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int32_t* first,
                           const int32_t* out_start, int64_t R, uint16_t* k_out, int64_t k_stride,
                           uint16_t* v_out, int64_t v_stride, hipStream_t stream);
+// Most (row, query head) pairs of a step whose sequences are split in moe_attn_decode.
+constexpr int64_t kSplitPairs = 1 << 14;
 size_t attn_decode_ws_bytes(int fmt, int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len);
 hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int n_q,
                               const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,

@@ -87,7 +87,7 @@ struct LaneSeq {
   }
 };
 
-// The item of workgroup id.  chunk: a multiple of the waves, as small as keeps
+// The item of workgroup id.  S 1: sequences are not split.  chunk: a multiple of the waves, as small as keeps
 // the items within `room` more than the tiles (what the grid holds), and kWhole
 // units or more unless the 256 CUs need shorter ones (8 slots of 1000 to 60000
 // tokens: 33 us; as many chunks of each sequence as of any other, 37).
@@ -911,8 +911,12 @@ struct Shape {
 //   - 16 query rows to a tile, 32 when a sequence has more (the cache is read
 //     once for them: 4 rows of 8 slots at 16 K tokens 29 against 34);
 //   - up to 12 units (384 tokens) no split, so no joining launch: 300 tokens 7.2
-//     against 8.8, but 700 tokens 9.2 against 8.8; nor with 97 workgroups or more
-//     that have up to 31 units each (32 slots of 700 tokens 10.5 against 12.5);
+//     against 8.8, but 700 tokens 9.2 against 8.8; up to 31 units where the
+//     sequences alone are more than half of the workgroups aimed at (32 slots of
+//     700 tokens 10.5 against 12.5; in bf16 65 slots of 2000 tokens 68 against 63
+//     with a split), up to 255 where they are more than all (257 slots of 4000 and
+//     of 8000 tokens 108 and 212 against 120 and 224, but 256 of 500 and one of 8000
+//     66 against 36 with a split, one of 131072 807 against 85);
 //   - chunks of at least 4 units for each wave (64 slots of 500 tokens 9.6, at
 //     one unit 16.5; 8 slots at 8 K tokens 16.4 and 17.5), unless the CUs need
 //     shorter ones (8 slots of 2000 tokens 10.8, for 192 workgroups 11.5);
@@ -930,10 +934,12 @@ Shape shape_of(int fmt, int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t 
   const int64_t base = (int64_t)n_seq * n_kv * ((per_seq * G + r.tile - 1) / r.tile);
   const int target = 256 * (fmt == MOE_FMT_NVFP4 && r.tile == 16 && D <= 128 ? 4 : 2);
   r.likely = (int)std::min(std::max(units / kWhole, 192 / base), target / base);
-  // a single sequence may take all chunks; 64 MB of partial sums, but 8 chunks
-  int64_t S = std::max((int64_t)8, (64 << 20) / (T * n_q * D * 4));
+  // a single sequence may take all chunks; 64 MB of partial sums, 8 chunks or none
+  int64_t S = (64 << 20) / (T * n_q * D * 4);
+  const bool fits = S >= 8 && T * n_q <= kSplitPairs;
   S = std::min({S, (int64_t)kMaxSplit, (units + kWaves - 1) / kWaves});
-  r.S = r.likely <= 1 || units <= 3 * kWaves ? 1 : (int)S;
+  const int whole = r.likely > 1 ? 3 * kWaves : base > target ? 255 : 31;
+  r.S = !fits || units <= whole ? 1 : (int)S;
   const int64_t fine = std::max((int64_t)256 / n_kv, tiles * ((units + kWhole - 1) / kWhole));
   r.likely = std::min(r.likely, r.S);
   r.room = (int)std::max((int64_t)1, std::min({(int64_t)target / n_kv, fine, tiles * r.S}));

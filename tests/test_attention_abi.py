@@ -312,3 +312,21 @@ def test_a_part_of_a_long_sequence_left_out_is_outside_the_bounds(fmt):
             keep = torch.arange(L) * 256 // L != part
             less, _ = attn_pages.attend(x, k[keep, 0], v[keep, 0], torch.tensor([L, L]), D ** -0.5, fmt, 4096)
             assert (((less - want).abs() / bound).max(1).values > 8).all(), (D, part)
+
+
+@pytest.mark.parametrize("fmt,n_seq,n_kv,G,D,rows,longest", [
+    (BF16, 65, 4, 8, 128, 1, 131072), (Q8_0, 65, 4, 8, 128, 1, 131072), (BF16, 33, 8, 4, 128, 1, 262144),
+    (NVFP4, 65, 8, 4, 128, 1, 131072), (Q8_0, 16, 8, 2, 256, 5, 150000), (NVFP4, 300, 4, 8, 128, 1, 40000)])
+def test_long_sequences_are_split_however_many_others_there_are(fmt, n_seq, n_kv, G, D, rows, longest):
+    """A workspace is asked for, so a long sequence among many does not stay with one
+    workgroup a head; never more than 64 MB of partial sums, and none for steps of
+    too many rows."""
+    c = cache(fmt=fmt, n_kv=n_kv, D=D)
+    T = n_seq * rows
+    b = q.moe_attn_workspace_bytes(c, n_kv * G, n_seq, T, longest)
+    # (8 of D + 2 values each, and the numbers of chunks; parts are aligned to 256 bytes)
+    assert T * n_kv * G * 8 * (D + 2) * 4 <= b <= (64 << 20) * (1 + 2 / D) + T * n_kv * G * 4 + 768
+    most = q.moe_attn_workspace_bytes(c, n_kv * G, n_seq, 1 << 16, 0)
+    assert most <= (64 << 20) * (1 + 2 / D) + (1 << 14) * 4 + 768
+    assert decode(c=c, s=seqs(n=n_seq, width=1 << 13), n_q=n_kv * G, T=T, max_len=longest, xs=n_kv * G * D, os=n_kv * G * D, ws=None) == BAD
+    assert "ws is NULL" in q.last_error()

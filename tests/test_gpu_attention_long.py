@@ -65,3 +65,13 @@ def test_decode_one_long_sequence_among_short_ones(fmt, n_kv, G, D, P):
     second round of the join), whatever the longest cache is said to be."""
     for lens, rows in (([33000, 300], [1, 1]), ([100, 60000, 7, 33, 1, 500, 64, 20], [1] * 8), ([90, 41000, 600], [3, 2, 1])):
         check(fmt, n_kv, G, D, P, lens, rows, (None, 2000, 1 << 20))
+
+
+@pytest.mark.parametrize("fmt,n_kv,G,D,n,short,L,rows", [
+    (BF16, 4, 2, 64, 66, 50, 40000, 1), (Q8_0, 4, 2, 128, 66, 50, 40000, 1), (NVFP4, 8, 1, 64, 140, 40, 30000, 1),
+    (Q8_0, 8, 2, 256, 16, 60, 20000, 5), (BF16, 8, 1, 64, 70, 33, 9000, 1)])
+def test_decode_one_long_sequence_among_many(fmt, n_kv, G, D, n, short, L, rows):
+    """Steps whose short sequences alone take more than half, or all, of the GPU."""
+    lens = [1 + (short * b) % (2 * short) for b in range(n)]
+    lens[n // 2], lens[-1] = L, rows
+    check(fmt, n_kv, G, D, 64, lens, [min(rows, x) for x in lens], (None, 1 << 20))
