@@ -101,7 +101,8 @@ def sources_digest():
     """sha256 over the sources of the expert-FFN kernels (the ones the counter
     summaries are of) with comments and blank space removed: counter readings
     are only used while the code they were taken on is unchanged (a comment
-    edit keeps them)."""
+    edit keeps them).  api.hip, which chooses among these kernels and holds all
+    other calls too, is not part of it."""
     import hashlib
     import re
     d = os.path.join(ROOT, "quantized_expert_ffn_router_amd", "csrc")

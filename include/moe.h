@@ -519,8 +519,8 @@ moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int3
  *   out = sum_j softmax(s)_j v_j,
  * sums and softmax in fp32; out bf16, zero for a row that sees no token.  The
  * keys, values and softmax weights meet the matrix units as fp16 (block
- * formats; the query rows scaled by a power of two each) or bf16 (16-bit
- * cache).  What a row does not see has no influence on it, also if it is NaN or infinite.
+ * formats; the query rows scaled by a power of two each; a weight below 2^-32
+ * of the largest counts as none) or bf16 (16-bit cache).  What a row does not see has no influence on it, also if it is NaN or infinite.
  * q, out: bf16 [T] rows of n_q * D (out may be q, with the same stride; other
  * overlaps are refused).  max_len: the longest
  * kv_len expected; it decides how the work is split, never the result's

@@ -13,10 +13,11 @@
 // the softmax weights go from one product to the next without leaving their
 // lanes, and a row's maximum needs two lane swaps.
 //
-// Measured on one MI355X, both launches, 32 query and 4 key/value heads of 128:
-// 8 slots of 16 K tokens in bf16 49 us (5.4 TB/s of cache, a large copy's rate), in
-// Q8_0 32 us (4.4 TB/s), in NVFP4 one slot of 262144 tokens 33.5 us (4.5 TB/s); there
-// decoding keeps the vector units busy beside the loads.
+// Measured on one MI355X, both launches, 32 query and 4 key/value heads of 128, inputs
+// that no cache holds: 8 slots of 16 K tokens in bf16 49 us (5.5 TB/s, above a large
+// copy's 5.15), in Q8_0 31 us (4.6 TB/s), in NVFP4 24 (3.2) and one slot of 262144
+// tokens 33 us (4.6 TB/s); there decoding keeps the vector units busy beside the
+// loads.  Heads of 64 and of 256, those 8 slots: 28, 19, 17 and 94, 59, 40 us.
 #include <type_traits>
 
 #include <algorithm>

@@ -13,11 +13,13 @@
 // (ds_read_b64_tr_b16) with their tokens in the same order.
 //
 // Bound by the matrix units at the clock they hold under load: 8192 rows behind
-// 8192 keys (32 heads of 128) 1350 to 1430 us, 1.2 PFLOP/s of visible pairs, where a large
-// bf16 library product reaches 1.17.  16384 rows of nine prompts of 630 to 3150
-// rows: 325 us, 0.94; there every tile's start, the part of its last keys that is
+// 8192 keys (32 heads of 128) 1350 to 1450 us over runs and cards, 1.14 to 1.22 PFLOP/s
+// of visible pairs, where a large bf16 library product reaches 1.17.  16384 rows of
+// nine prompts of 630 to 3150 rows: 323 to 342 us (359 as single launches under a
+// profiler), 0.9 to 0.95; there every tile's start, the part of its last keys that is
 // masked, and the output weigh more.  333 rows take 12 us: six tiles of keys one
-// after the other, 1.1 us each, on a card that is mostly empty.
+// after the other, 1.1 us each, on a card that is mostly empty.  8192 rows at heads
+// of 64, 128 and 256: 280, 478 and 1030 us (0.98, 1.15 and 1.07 PFLOP/s).
 #include "attn_common.h"
 
 namespace moe {
@@ -105,7 +107,7 @@ struct Tiles {
   }
 };
 
-// Two softmax weights as bf16, rounded to nearest even (half a step, 2^-9: the
+// Two softmax weights as bf16, rounded to nearest even (half a step, 2^-8: the
 // operand type of the second product), and their sum added to l -- of the
 // rounded weights, so that rounding does not shift a row's mean.
 __device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {

@@ -196,7 +196,7 @@ struct AppendArgs {
 
 // 8 elements of a head: z * w / rms(z), then the rotation of the lane's four
 // pairs: (z[i], z[i + 4]) where the lane holds both halves' elements, neighbours
-// otherwise.  T: float for queries (a few 2^-24, against the 2^-9 of the
+// otherwise.  T: float for queries (a few 2^-24, against the 2^-8 of the
 // rounding to bf16), double for keys.  The squares are summed in fp64 for both:
 // those of a bf16 value may lie outside fp32.
 template <int LPH, int D, typename T>
