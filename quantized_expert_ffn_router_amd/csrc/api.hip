@@ -586,11 +586,11 @@ bool share_elements(RowBlock a, RowBlock b) {
   if (a.n < 1 || b.n < 1) return false;
   if ((uintptr_t)a.p > (uintptr_t)b.p) std::swap(a, b);
   const int64_t at = (int64_t)(((uintptr_t)b.p - (uintptr_t)a.p) / 2);  // of b's first row, from a's
-  if (at >= (a.n - 1) * a.stride + a.width) return false;
+  if ((__int128)at >= (__int128)(a.n - 1) * a.stride + a.width) return false;
   // rows inside one another's range: side by side at the same stride, or not known to be apart
   if (a.stride != b.stride) return true;
   const int64_t d = at % a.stride;
-  return d < a.width || d + b.width > a.stride;
+  return d < a.width || b.width > a.stride - d;
 }
 
 // An output's rows are not those of an input, except in the input's own place.

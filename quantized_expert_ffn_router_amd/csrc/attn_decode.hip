@@ -109,7 +109,8 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
     }
     work = wave_sum(work);
     most = wave_max(most);
-    int chunk = (int)ceilf(work / (float)room);
+    // (a sequence has less than 2^27 units: held to 2^30, it stays an int)
+    int chunk = (int)fminf(ceilf(work / (float)room), 0x1p30f);
     if (chunk < kWhole) chunk = max(chunk, min((int)ceilf(work * n_kv / 256.0f), kWhole));
     chunk = (max(chunk, (most + S - 1) / S) + kWaves - 1) / kWaves * kWaves;
     r.chunk = max(__builtin_amdgcn_readfirstlane(chunk), kWaves);

@@ -75,3 +75,10 @@ def test_decode_one_long_sequence_among_many(fmt, n_kv, G, D, n, short, L, rows)
     lens = [1 + (short * b) % (2 * short) for b in range(n)]
     lens[n // 2], lens[-1] = L, rows
     check(fmt, n_kv, G, D, 64, lens, [min(rows, x) for x in lens], (None, 1 << 20))
+
+
+def test_decode_many_rows_of_long_sequences():
+    """The work of a step over its workgroups exceeds any one sequence: as many rows
+    as are still split, heads enough that few chunks fit beside them."""
+    check(BF16, 64, 1, 64, 32, [1500, 8300, 90, 8300], [60, 60, 60, 60], (None, 1 << 20))
+    check(NVFP4, 2, 8, 128, 64, [9000, 300, 12000], [300, 200, 350], (None,))
