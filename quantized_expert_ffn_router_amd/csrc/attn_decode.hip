@@ -72,6 +72,12 @@ struct Item {
   int tile, kvh, sp, splits, chunk;
 };
 
+// Units to go over at most: those of the page table and one more, which stands for
+// all tokens past its end (none is there: rows that see it are NaN).
+__device__ __forceinline__ int units_of_table(const SeqView& s) {
+  return (int)min(((int64_t)s.max_pages << s.log2P) / 32 + 1, (int64_t)1 << 27);
+}
+
 // This lane's sequence: its rows from row 0 on (row t is token len - end + t
 // wherever its first row lies).
 struct LaneSeq {
@@ -84,7 +90,7 @@ struct LaneSeq {
     len = s.kv_len[i];
     const int64_t n = i0 + lane_id() < s.n_seq ? min((int64_t)end, T) - start : 0;
     tiles = n > 0 ? (int)((uint32_t)((int)n * G + size - 1) / (uint32_t)size) : 0;
-    units = n > 0 && len > 0 ? (len - 1) / 32 + 1 : 0;
+    units = n > 0 && len > 0 ? min((len - 1) / 32 + 1, units_of_table(s)) : 0;
   }
 };
 
@@ -149,14 +155,14 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
 struct TilePlan {
   int64_t hi;  // last token that any row of the tile sees (-1: none)
   int64_t lo;  // last token that all of them see
-  int units;   // 32-token units up to hi
+  int units;   // 32-token units up to hi, but units_of_table
 };
-__device__ __forceinline__ TilePlan tile_plan(const Item& it, int G, int size) {
+__device__ __forceinline__ TilePlan tile_plan(const SeqView& s, const Item& it, int G, int size) {
   TilePlan p;
   const int last = min((int)((uint32_t)(it.tile * size + size - 1) / (uint32_t)G), it.inside - 1);
   p.hi = max((int64_t)it.len - it.rows + last, (int64_t)-1);
   p.lo = (int64_t)it.len - it.rows + (int)((uint32_t)(it.tile * size) / (uint32_t)G);
-  p.units = (int)((p.hi + 32) >> 5);
+  p.units = min((int)((p.hi + 32) >> 5), units_of_table(s));
   return p;
 }
 
@@ -632,7 +638,7 @@ __global__ __launch_bounds__(64 * kWaves, kDecodeOcc(FMT, D, NT)) void k_attn_de
   const size_t page_bytes = (size_t)a.n_kv * lay.head;
   const uint8_t* heads = a.pool + (size_t)kvh * lay.head;
   const typename Unit<FMT, D>::Lane at(n, g, P);
-  const TilePlan plan = tile_plan(it, a.G, 16 * NT);
+  const TilePlan plan = tile_plan(a.s, it, a.G, 16 * NT);
   const int u_begin = sp > 0 ? sp * it.chunk : 0;
   const int u_end = min((int64_t)plan.units, (int64_t)u_begin + it.chunk);
   if (sp > 0 && u_begin >= u_end) {  // (split 0 also answers rows that see nothing)

@@ -280,3 +280,36 @@ def test_append_of_a_long_prompt_in_place_and_apart(fmt):
         got.append((x[:, :n_q * D], x[:, n_q * D:n_q * D + kw], cache.pool) if in_place else (qo, ko, cache.pool))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 10 ** 9, "a token more", "a page more"])
+def test_decode_lengths_past_the_page_table(fmt, length):
+    """The rows that see a token past the table are NaN, at once (the tokens past it
+    are not gone over one by one); those of the same sequence that end before it and
+    other sequences are right, with the table's last page held or not."""
+    print("past the table", FMT[fmt], length, flush=True)
+    for rows, P, lens in (([1, 1, 3], 32, [700, 70, 96]), ([2, 1, 4], 64, [128, 1, 900])):
+        s = Setup(fmt, 2, 64, P, lens, rows, seed=9)
+        end = P * s.width  # tokens that the table has places for
+        L = {"a token more": end + 1, "a page more": end + P}.get(length, length)
+        s.lens[0] = L
+        s.to_device()
+        qv = ref.bf16_bits(s.rng.standard_normal((s.T, 4 * 64)))
+        for m in (max(lens), 1 << 20):
+            got = run_decode(s, 4, qv, max_len=m)
+            seen = np.isnan(ref.bf16_val(got[:rows[0]]))
+            assert seen.all(), (m, seen.all(1))  # (all see the places behind its own tokens)
+            check_decode(s, 4, qv, got, skip=(0,))
+        # the last row of a sequence sees past the table, the ones before it end inside
+        full = Setup(fmt, 2, 64, P, [P * 3, 40], [3, 1], seed=10)
+        full.table = full.table[:, :3]
+        full.width, full.lens = 3, [P * 3 + 1, 40]
+        full.table = np.ascontiguousarray(full.table)
+        full.to_device()
+        qv = ref.bf16_bits(full.rng.standard_normal((full.T, 4 * 64)))
+        got = run_decode(full, 4, qv)
+        assert np.isnan(ref.bf16_val(got[2])).all()
+        full.lens, full.rows, full.start = [P * 3, 40], [2, 1], np.array([0, 2, 3])
+        keep = got[[0, 1, 3]]
+        check_decode(full, 4, qv[[0, 1, 3]], keep)
