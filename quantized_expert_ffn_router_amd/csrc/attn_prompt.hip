@@ -15,7 +15,7 @@
 // Bound by the matrix units at the clock they hold under load: 8192 rows behind
 // 8192 keys (32 heads of 128) 1350 to 1450 us over runs and cards, 1.14 to 1.22 PFLOP/s
 // of visible pairs, where a large bf16 library product reaches 1.17.  16384 rows of
-// nine prompts of 630 to 3150 rows: 323 to 342 us (359 as single launches under a
+// nine prompts of 630 to 3150 rows: 323 to 347 us (359 as single launches under a
 // profiler), 0.9 to 0.95; there every tile's start, the part of its last keys that is
 // masked, and the output weigh more.  333 rows take 12 us: six tiles of keys one
 // after the other, 1.1 us each, on a card that is mostly empty.  8192 rows at heads

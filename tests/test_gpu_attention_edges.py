@@ -313,3 +313,28 @@ def test_decode_lengths_past_the_page_table(fmt, length):
         full.lens, full.rows, full.start = [P * 3, 40], [2, 1], np.array([0, 2, 3])
         keep = got[[0, 1, 3]]
         check_decode(full, 4, qv[[0, 1, 3]], keep)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+def test_rows_claimed_beyond_t_are_left_out(fmt):
+    """The last sequence claims more rows than the step has: those inside are at the
+    positions that its claim gives them, in appends and in decode steps with and
+    without a split."""
+    for L in (60, 900):
+        print("rows beyond T", FMT[fmt], L, flush=True)
+        s = Setup(fmt, 2, 64, 32, [33, L], [2, 20], seed=12, pad_rows=0)
+        T, inside = 9, 7
+        qv = ref.bf16_bits(s.rng.standard_normal((T, 4 * 64)))
+        s.T = T
+        got = run_decode(s, 4, qv)
+        lens, rows, start = list(s.lens), list(s.rows), s.start
+        # (row i of the claim sees up to token L - 20 + i: as if the sequence ended with the 7th)
+        s.lens, s.rows, s.start = [33, L - 20 + inside], [2, inside], np.array([0, 2, T])
+        check_decode(s, 4, qv, got)
+        s.lens, s.rows, s.start = lens, rows, start
+        qkv = append_inputs(s, 4, 9)
+        freq, _ = q.moe_rope_freqs(q.MOE_ROPE_PLAIN, 32, 10000.0)
+        norm = [np.ones(64, np.float32)] * 2
+        got_q, got_k, _ = run_append(s, 4, qkv, norm, 32, 0, freq, 1.0)
+        s.lens, s.rows, s.start = [33, L - 20 + inside], [2, inside], np.array([0, 2, T])
+        check_append(s, 4, qkv, norm, 32, 0, freq, 1.0, got_q, got_k)
