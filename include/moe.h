@@ -505,9 +505,10 @@ moe_status moe_kv_append(const moe_kv_cache* c, const moe_qkv_desc* p, const moe
  * need it), for prompt chunks that attend to a cached prefix.  Token j of
  * sequence b, first[b] <= j < kv_len[b], goes to row out_start[b] + j -
  * first[b] of k_out and v_out (n_kv * D wide), as long as there is such a token
- * (0 <= j) and row (0 <= row < R) and the row is below out_start[b+1].  first: device int32 [n_seq], or NULL: 0.  out_start:
- * device int32 [n_seq + 1], ascending.  k_out or v_out may be NULL.  row_start
- * of the batch is not read. */
+ * (0 <= j) and row (0 <= row < R) and the row is below out_start[b+1].  first:
+ * device int32 [n_seq], or NULL: 0.  out_start: device int32 [n_seq + 1],
+ * ascending.  k_out or v_out may be NULL; they must not overlap.  row_start of
+ * the batch is not read. */
 moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int32_t* first,
                        const int32_t* out_start, int64_t R, uint16_t* k_out, int64_t k_stride,
                        uint16_t* v_out, int64_t v_stride, hipStream_t stream);
@@ -520,7 +521,8 @@ moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int3
  * sums and softmax in fp32; out bf16, zero for a row that sees no token.  The
  * keys, values and softmax weights meet the matrix units as fp16 (block
  * formats; the query rows scaled by a power of two each; a weight below 2^-32
- * of the largest counts as none) or bf16 (16-bit cache).  What a row does not see has no influence on it, also if it is NaN or infinite.
+ * of the largest counts as none) or bf16 (16-bit cache).  What a row does not
+ * see has no influence on it, also if it is NaN or infinite.
  * q, out: bf16 [T] rows of n_q * D (out may be q, with the same stride; other
  * overlaps are refused).  max_len: the longest
  * kv_len expected; it decides how the work is split, never the result's

@@ -94,10 +94,10 @@ struct LaneSeq {
   }
 };
 
-// The item of workgroup id.  S 1: sequences are not split.  chunk: a multiple of the waves, as small as keeps
-// the items within `room` more than the tiles (what the grid holds), and kWhole
-// units or more unless the 256 CUs need shorter ones (8 slots of 1000 to 60000
-// tokens: 33 us; as many chunks of each sequence as of any other, 37).
+// The item of workgroup id.  S 1: sequences are not split.  chunk: a multiple of the
+// waves, as small as keeps the items within `room` more than the tiles (what the grid
+// holds), and kWhole units or more unless the 256 CUs need shorter ones (8 slots of
+// 1000 to 60000 tokens: 33 us; as many chunks of each sequence as of any other, 37).
 constexpr int kWhole = 4 * kWaves;
 __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, int size, int n_kv,
                                           int room, int S, int id) {
