@@ -557,6 +557,90 @@ moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
                            uint16_t* out, int64_t out_stride, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Around the attention and the experts: norms and dense projections         */
+/* ------------------------------------------------------------------------ */
+/*
+ * The pages keep a pack's dense projections in a format of their own beside the
+ * experts' (basalt.jgulfo.com, "All the numbers", the engine notes); the pages
+ * give no formula.  Here they are 4-bit microscaled matrices, which the matrix
+ * units take as they are, and the rows that meet them are 4- or 8-bit
+ * microscaled: along a row, each 32 values have one scale, a power of two.
+ *   MOE_FMT_MXFP4  E2M1 codes, element 2i in the low half of byte i
+ *   MOE_FMT_MXFP8  E4M3 codes, one a byte
+ * Rows of K elements: codes u8 [T][K/2] or [T][K], scales u8 [T][K/32], dense;
+ * value = code * 2^(s - 127), s = 255 (NaN) making its 32 values NaN.
+ * Quantisation of the 32 bf16 values of a block whose largest magnitude is A:
+ *   s = max(floor(log2 A) - (2 or 8), -127) + 127, code = the nearest of
+ *   x / 2^(s - 127), ties to the even code, held to +-6 or +-448
+ * (the block format of the Open Compute Project's microscaling specification);
+ * A = 0 gives s = 0, an infinity or a NaN in the block s = 255 and codes 0.
+ *
+ * Shapes: K and H multiples of 128; H up to 16384, K up to 32768, N 1..2^20,
+ * T up to 2^20.  Strides: multiples of 8 elements, the row's width or more;
+ * pointers 16-byte aligned.
+ */
+#define MOE_FMT_MXFP4 7
+#define MOE_FMT_MXFP8 8
+
+/* The residual's addition and the root-mean-square norm, in one pass over the
+ * rows:
+ *   h = bf16(x + residual)  (x without a residual),
+ *   z = bf16(h / sqrt(mean(h^2) + eps) * weight),
+ * the sum of squares and the products in fp64 (so that codes do not depend on
+ * the order of a sum), rounded to fp32 and then to bf16; the additions in fp32.
+ * x, residual (or NULL): bf16 [T][H]; weight: fp32 [H].
+ * sum: h, bf16 [T][H], or NULL; out: z, bf16 [T][H], or NULL; codes, scales: z
+ * in fmt (MOE_FMT_MXFP4 or _MXFP8), or NULL with fmt 0: what moe_mx_quant makes
+ * of out.  sum and out may each be x or residual (the same address and stride);
+ * other overlaps are refused.  At least one output is given. */
+moe_status moe_add_norm(int32_t H, int64_t T, const uint16_t* x, int64_t x_stride,
+                        const uint16_t* residual, int64_t residual_stride, const float* weight,
+                        float eps, uint16_t* sum, int64_t sum_stride, uint16_t* out,
+                        int64_t out_stride, int32_t fmt, uint8_t* codes, uint8_t* scales,
+                        hipStream_t stream);
+
+/* bf16 rows [T][K] in fmt (MOE_FMT_MXFP4 or MOE_FMT_MXFP8). */
+moe_status moe_mx_quant(int32_t fmt, int32_t K, int64_t T, const uint16_t* x, int64_t x_stride,
+                        uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* A dense projection's weights W[N][K] in MOE_FMT_MXFP4, packed once at load
+ * from codes u8 [N][K/2] and scales u8 [N][K/32] (moe_mx_quant makes them from
+ * bf16 rows) into `packed`, moe_mx_matrix_bytes(N, K) bytes, 256-byte aligned.
+ * Host struct holding device pointers. */
+typedef struct moe_mx_matrix {
+  int32_t N, K;
+  const void* packed;
+  const float* bias;  /* fp32 [N], or NULL */
+} moe_mx_matrix;
+
+/* Bytes of a packed matrix (a multiple of 256); 0 if unsupported. */
+size_t moe_mx_matrix_bytes(int32_t N, int32_t K);
+moe_status moe_mx_pack(int32_t N, int32_t K, const uint8_t* codes, const uint8_t* scales,
+                       void* packed, hipStream_t stream);
+
+/* y[t][n] = sum_k a[t][k] W[n][k] + bias[n], rows a in fmt as codes and scales;
+ * y: [T] rows of N, y_stride apart, of y_dtype (MOE_DTYPE_F32 or _BF16).  The
+ * products meet the matrix units as codes and are summed in fp32; with
+ * MOE_FMT_MXFP8 rows the units cut each product to a multiple of 2^-13 of the
+ * power of two of the largest one among its 8 neighbours (elements 8i..8i+7) on
+ * the way.  The result is rounded once.  A NaN scale makes the outputs that meet
+ * it NaN.  The order of the sums depends on T,
+ * N and K, not on scheduling. */
+moe_status moe_mx_linear(const moe_mx_matrix* w, int32_t fmt, const uint8_t* codes,
+                         const uint8_t* scales, int64_t T, void* y, int64_t y_stride,
+                         int32_t y_dtype, hipStream_t stream);
+
+/* moe_mx_quant of bf16 rows x [T][K], then moe_mx_linear, with the same results
+ * bit for bit; a few rows are quantised inside the product's launch.  ws:
+ * moe_mx_workspace_bytes of this fmt and K, with this T or a larger one; nothing
+ * in it needs to start at zero.  Calls that may overlap need workspaces of
+ * their own. */
+size_t moe_mx_workspace_bytes(int32_t fmt, int32_t K, int64_t T);
+moe_status moe_mx_linear_rows(const moe_mx_matrix* w, int32_t fmt, const uint16_t* x,
+                              int64_t x_stride, int64_t T, void* y, int64_t y_stride,
+                              int32_t y_dtype, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Optional cold-expert tier: pinned host RAM -> HBM slots                   */
 /* ------------------------------------------------------------------------ */
 /*

@@ -29,6 +29,8 @@ MOE_FMT_Q8_0 = 3
 MOE_FMT_IQ3G = 4
 MOE_FMT_IQ1G = 5
 MOE_FMT_BF16 = 6  # key/value cache only
+MOE_FMT_MXFP4 = 7  # dense projections and their rows
+MOE_FMT_MXFP8 = 8  # rows only
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 
@@ -107,6 +109,13 @@ class QkvDesc(ctypes.Structure):
                 ("rope_scale", ctypes.c_float)]
 
 
+class MxMatrix(ctypes.Structure):
+    """moe_mx_matrix: a dense projection's packed weights (device pointers)."""
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("packed", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+assert ctypes.sizeof(MxMatrix) == 24
 assert ctypes.sizeof(KvCacheDesc) == 40
 assert ctypes.sizeof(SeqBatch) == 32
 assert ctypes.sizeof(QkvDesc) == 48
@@ -121,6 +130,7 @@ _LP = ctypes.POINTER(LayerDesc)
 _BP = ctypes.POINTER(Buckets)
 _CP = ctypes.POINTER(KvCacheDesc)
 _SP = ctypes.POINTER(SeqBatch)
+_MP = ctypes.POINTER(MxMatrix)
 _f32, _f64 = ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "moe_abi_version": (ctypes.c_int, []),
@@ -153,6 +163,14 @@ SIGNATURES = {
                                        _sz, _vp]),
     "moe_attn_prompt": (ctypes.c_int, [_i32, _i32, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp,
                                        _i64, _vp, _i64, _f32, _vp, _i64, _vp]),
+    "moe_add_norm": (ctypes.c_int, [_i32, _i64, _vp, _i64, _vp, _i64, _vp, _f32, _vp, _i64, _vp, _i64,
+                                    _i32, _vp, _vp, _vp]),
+    "moe_mx_quant": (ctypes.c_int, [_i32, _i32, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "moe_mx_matrix_bytes": (_sz, [_i32, _i32]),
+    "moe_mx_pack": (ctypes.c_int, [_i32, _i32, _vp, _vp, _vp, _vp]),
+    "moe_mx_linear": (ctypes.c_int, [_MP, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _vp]),
+    "moe_mx_workspace_bytes": (_sz, [_i32, _i32, _i64]),
+    "moe_mx_linear_rows": (ctypes.c_int, [_MP, _i32, _vp, _i64, _i64, _vp, _i64, _i32, _vp, _sz, _vp]),
     "moe_tier_create": (ctypes.c_int, [ctypes.POINTER(TierDesc), ctypes.POINTER(ctypes.c_void_p)]),
     "moe_tier_prepare": (ctypes.c_int, [_vp, _i32, _BP, _vp, _vp]),
     "moe_tier_prepare_async": (ctypes.c_int, [_vp, _i32, _BP, _vp, _vp]),
@@ -332,6 +350,39 @@ def moe_attn_prompt(n_q, n_kv, D, n_seq, q_start, kv_start, T, Tk, q, q_stride, 
     _check(lib().moe_attn_prompt(n_q, n_kv, D, n_seq, _ptr(q_start), _ptr(kv_start), T, Tk, _ptr(q),
                                  q_stride, _ptr(k), k_stride, _ptr(v), v_stride, scale, _ptr(out),
                                  out_stride, _stream(stream)))
+
+
+def moe_add_norm(H, T, x, x_stride, residual, residual_stride, weight, eps, sum, sum_stride, out,
+                 out_stride, fmt=0, codes=None, scales=None, stream=None):
+    _check(lib().moe_add_norm(H, T, _ptr(x), x_stride, _ptr(residual), residual_stride, _ptr(weight), eps,
+                              _ptr(sum), sum_stride, _ptr(out), out_stride, fmt, _ptr(codes),
+                              _ptr(scales), _stream(stream)))
+
+
+def moe_mx_quant(fmt, K, T, x, x_stride, codes, scales, stream=None):
+    _check(lib().moe_mx_quant(fmt, K, T, _ptr(x), x_stride, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_mx_matrix_bytes(N, K) -> int:
+    return lib().moe_mx_matrix_bytes(N, K)
+
+
+def moe_mx_pack(N, K, codes, scales, packed, stream=None):
+    _check(lib().moe_mx_pack(N, K, _ptr(codes), _ptr(scales), _ptr(packed), _stream(stream)))
+
+
+def moe_mx_linear(w, fmt, codes, scales, T, y, y_stride, y_dtype, stream=None):
+    _check(lib().moe_mx_linear(ctypes.byref(w), fmt, _ptr(codes), _ptr(scales), T, _ptr(y), y_stride,
+                               y_dtype, _stream(stream)))
+
+
+def moe_mx_workspace_bytes(fmt, K, T) -> int:
+    return lib().moe_mx_workspace_bytes(fmt, K, T)
+
+
+def moe_mx_linear_rows(w, fmt, x, x_stride, T, y, y_stride, y_dtype, ws, ws_bytes, stream=None):
+    _check(lib().moe_mx_linear_rows(ctypes.byref(w), fmt, _ptr(x), x_stride, T, _ptr(y), y_stride, y_dtype,
+                                    _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def moe_tier_create(desc: TierDesc) -> int:

@@ -11,6 +11,7 @@
 
 #include "attn_common.h"
 #include "gemv_common.h"
+#include "mx.h"
 
 // Workspace of moe_expert_ffn_noalloc: one copy per GPU, held until the
 // process ends.  Host code never passes this name to a kernel or a copy (on
@@ -848,6 +849,221 @@ moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,
   return hip_status(W, moe::launch_attn_prompt(n_q, n_kv, D, n_seq, q_start, kv_start, T, Tk, q,
                                                q_stride, k, k_stride, v, v_stride, scale, out,
                                                out_stride, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Norms and dense projections
+// ---------------------------------------------------------------------------
+
+namespace {
+
+moe_status check_mx_fmt(int fmt, const char* where) {
+  if (fmt != MOE_FMT_MXFP4 && fmt != MOE_FMT_MXFP8)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: row format %d (MXFP4 or MXFP8)", where, fmt);
+  return MOE_OK;
+}
+
+moe_status check_width(int n, int most, const char* name, const char* where) {
+  if (n < 1 || n % 128 != 0 || n > most)
+    return fail(n < 1 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED,
+                "%s: %s=%d must be a multiple of 128 in 128..%d", where, name, n, most);
+  return MOE_OK;
+}
+
+moe_status check_matrix(int N, int K, const char* where) {
+  if (N < 1 || N > (1 << 20))
+    return fail(N < 1 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED, "%s: N=%d must be in 1..2^20", where, N);
+  return check_width(K, 32768, "K", where);
+}
+
+moe_status check_count(int64_t T, const char* where) {
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T=%lld < 0", where, (long long)T);
+  if (T > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "%s: T=%lld > 2^20", where, (long long)T);
+  return MOE_OK;
+}
+
+// T rows of `bytes` bytes each, one after the other.
+RowBlock dense(const void* p, int64_t bytes, int64_t T) { return RowBlock{p, bytes / 2, bytes / 2, T}; }
+int64_t code_bytes(int fmt, int64_t K) { return fmt == MOE_FMT_MXFP4 ? K / 2 : K; }
+
+moe_status check_codes(const uint8_t* codes, const uint8_t* scales, const char* where) {
+  CHECK_PTR(codes, where);
+  CHECK_PTR(scales, where);
+  moe_status st = check_aligned(codes, "codes", where);
+  return st != MOE_OK ? st : check_aligned(scales, "scales", where);
+}
+
+struct Named {
+  RowBlock rows;
+  const char* name;
+};
+// `out` shares no element with any of these (in_place: but may be one of them).
+template <size_t N>
+moe_status check_all_apart(Named out, const Named (&in)[N], bool in_place, const char* where) {
+  if (!out.rows.p) return MOE_OK;
+  for (const Named& i : in) {
+    if (!i.rows.p) continue;
+    const moe_status st = check_apart(out.rows, i.rows, in_place, out.name, i.name, where);
+    if (st != MOE_OK) return st;
+  }
+  return MOE_OK;
+}
+
+moe_status check_product(const moe_mx_matrix* w, int fmt, int64_t T, const char* where) {
+  CHECK_PTR(w, where);
+  moe_status st = check_matrix(w->N, w->K, where);
+  if (st != MOE_OK) return st;
+  if ((st = check_mx_fmt(fmt, where)) != MOE_OK) return st;
+  if ((st = check_count(T, where)) != MOE_OK) return st;
+  CHECK_PTR(w->packed, where);
+  if ((uintptr_t)w->packed % moe::kAlign != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: packed not 256-byte aligned", where);
+  return check_aligned(w->bias, "bias", where);
+}
+
+// The outputs of a product, in 16-bit elements.
+moe_status check_result(const moe_mx_matrix* w, int64_t T, const void* y, int64_t y_stride, int y_dtype,
+                        Named* out, const char* where) {
+  if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "%s: y_dtype=%d", where, y_dtype);
+  const moe_status st = check_rows(y, y_stride, w->N, "y", where);
+  if (st != MOE_OK) return st;
+  const int64_t e = y_dtype == MOE_DTYPE_F32 ? 2 : 1;
+  *out = Named{RowBlock{y, y_stride * e, w->N * e, T}, "y"};
+  const Named weights[] = {{dense(w->packed, (int64_t)moe::mx_layout(w->N, w->K).total, 1), "the weights"},
+                           {dense(w->bias, 4 * (int64_t)w->N, 1), "bias"}};
+  return check_all_apart(*out, weights, false, where);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_add_norm(int32_t H, int64_t T, const uint16_t* x, int64_t x_stride,
+                        const uint16_t* residual, int64_t residual_stride, const float* weight,
+                        float eps, uint16_t* sum, int64_t sum_stride, uint16_t* out,
+                        int64_t out_stride, int32_t fmt, uint8_t* codes, uint8_t* scales,
+                        hipStream_t stream) {
+  const char* W = "moe_add_norm";
+  moe_status st = check_width(H, 16384, "H", W);
+  if (st != MOE_OK) return st;
+  if ((st = check_count(T, W)) != MOE_OK) return st;
+  if (!(eps >= 0.0f && isfinite(eps))) return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g", W, (double)eps);
+  if (fmt != 0 && (st = check_mx_fmt(fmt, W)) != MOE_OK) return st;
+  if (fmt == 0 && (codes || scales)) return fail(MOE_ERR_INVALID_ARG, "%s: codes or scales without a format", W);
+  if (!sum && !out && fmt == 0) return fail(MOE_ERR_INVALID_ARG, "%s: no output", W);
+  if (T == 0) return MOE_OK;
+  if ((st = check_rows(x, x_stride, H, "x", W)) != MOE_OK) return st;
+  if (residual && (st = check_rows(residual, residual_stride, H, "residual", W)) != MOE_OK) return st;
+  if (sum && (st = check_rows(sum, sum_stride, H, "sum", W)) != MOE_OK) return st;
+  if (out && (st = check_rows(out, out_stride, H, "out", W)) != MOE_OK) return st;
+  CHECK_PTR(weight, W);
+  if ((st = check_aligned(weight, "weight", W)) != MOE_OK) return st;
+  if (fmt != 0 && (st = check_codes(codes, scales, W)) != MOE_OK) return st;
+  const Named in[] = {{{x, x_stride, H, T}, "x"}, {{residual, residual_stride, H, T}, "residual"}};
+  const Named w{dense(weight, 4 * (int64_t)H, 1), "weight"};
+  const Named s{{sum, sum_stride, H, T}, "sum"}, o{{out, out_stride, H, T}, "out"};
+  const Named c{dense(codes, code_bytes(fmt, H), T), "codes"}, f{dense(scales, H / 32, T), "scales"};
+  const Named after_sum[] = {w}, after_out[] = {w, s}, after_codes[] = {in[0], in[1], w, s, o},
+              after_scales[] = {in[0], in[1], w, s, o, c};
+  if ((st = check_all_apart(s, in, true, W)) != MOE_OK) return st;
+  if ((st = check_all_apart(s, after_sum, false, W)) != MOE_OK) return st;
+  if ((st = check_all_apart(o, in, true, W)) != MOE_OK) return st;
+  if ((st = check_all_apart(o, after_out, false, W)) != MOE_OK) return st;
+  if ((st = check_all_apart(c, after_codes, false, W)) != MOE_OK) return st;
+  if ((st = check_all_apart(f, after_scales, false, W)) != MOE_OK) return st;
+  return hip_status(W, moe::launch_add_norm(H, T, x, x_stride, residual, residual_stride, weight, eps, sum,
+                                            sum_stride, out, out_stride, fmt, codes, scales, stream));
+}
+
+moe_status moe_mx_quant(int32_t fmt, int32_t K, int64_t T, const uint16_t* x, int64_t x_stride,
+                        uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  const char* W = "moe_mx_quant";
+  moe_status st = check_mx_fmt(fmt, W);
+  if (st != MOE_OK) return st;
+  if ((st = check_width(K, 32768, "K", W)) != MOE_OK) return st;
+  if ((st = check_count(T, W)) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if ((st = check_rows(x, x_stride, K, "x", W)) != MOE_OK) return st;
+  if ((st = check_codes(codes, scales, W)) != MOE_OK) return st;
+  const Named in[] = {{{x, x_stride, K, T}, "x"}};
+  const Named c[] = {{dense(codes, code_bytes(fmt, K), T), "codes"}};
+  const Named f{dense(scales, K / 32, T), "scales"};
+  if ((st = check_all_apart(c[0], in, false, W)) != MOE_OK) return st;
+  if ((st = check_all_apart(f, in, false, W)) != MOE_OK) return st;
+  if ((st = check_all_apart(f, c, false, W)) != MOE_OK) return st;
+  return hip_status(W, moe::launch_mx_quant(fmt, K, T, x, x_stride, codes, scales, stream));
+}
+
+size_t moe_mx_matrix_bytes(int32_t N, int32_t K) {
+  if (check_matrix(N, K, "moe_mx_matrix_bytes") != MOE_OK) return 0;
+  return moe::mx_layout(N, K).total;
+}
+
+moe_status moe_mx_pack(int32_t N, int32_t K, const uint8_t* codes, const uint8_t* scales,
+                       void* packed, hipStream_t stream) {
+  const char* W = "moe_mx_pack";
+  moe_status st = check_matrix(N, K, W);
+  if (st != MOE_OK) return st;
+  if ((st = check_codes(codes, scales, W)) != MOE_OK) return st;
+  CHECK_PTR(packed, W);
+  if ((uintptr_t)packed % moe::kAlign != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: packed not 256-byte aligned", W);
+  const Named in[] = {{dense(codes, K / 2, N), "codes"}, {dense(scales, K / 32, N), "scales"}};
+  const Named p{dense(packed, (int64_t)moe::mx_layout(N, K).total, 1), "packed"};
+  if ((st = check_all_apart(p, in, false, W)) != MOE_OK) return st;
+  return hip_status(W, moe::launch_mx_pack(N, K, codes, scales, packed, stream));
+}
+
+moe_status moe_mx_linear(const moe_mx_matrix* w, int32_t fmt, const uint8_t* codes,
+                         const uint8_t* scales, int64_t T, void* y, int64_t y_stride,
+                         int32_t y_dtype, hipStream_t stream) {
+  const char* W = "moe_mx_linear";
+  moe_status st = check_product(w, fmt, T, W);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if ((st = check_codes(codes, scales, W)) != MOE_OK) return st;
+  Named out;
+  if ((st = check_result(w, T, y, y_stride, y_dtype, &out, W)) != MOE_OK) return st;
+  const Named in[] = {{dense(codes, code_bytes(fmt, w->K), T), "codes"}, {dense(scales, w->K / 32, T), "scales"}};
+  if ((st = check_all_apart(out, in, false, W)) != MOE_OK) return st;
+  return hip_status(W, moe::launch_mx_linear(w, fmt, nullptr, 0, codes, scales, T, y, y_stride, y_dtype, stream));
+}
+
+size_t moe_mx_workspace_bytes(int32_t fmt, int32_t K, int64_t T) {
+  const char* W = "moe_mx_workspace_bytes";
+  if (check_mx_fmt(fmt, W) != MOE_OK || check_width(K, 32768, "K", W) != MOE_OK || check_count(T, W) != MOE_OK)
+    return 0;
+  return moe::align_up((size_t)T * code_bytes(fmt, K)) + moe::align_up((size_t)T * (K / 32));
+}
+
+moe_status moe_mx_linear_rows(const moe_mx_matrix* w, int32_t fmt, const uint16_t* x,
+                              int64_t x_stride, int64_t T, void* y, int64_t y_stride,
+                              int32_t y_dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const char* W = "moe_mx_linear_rows";
+  moe_status st = check_product(w, fmt, T, W);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if ((st = check_rows(x, x_stride, w->K, "x", W)) != MOE_OK) return st;
+  Named out;
+  if ((st = check_result(w, T, y, y_stride, y_dtype, &out, W)) != MOE_OK) return st;
+  const size_t need = moe_mx_workspace_bytes(fmt, w->K, T);
+  CHECK_PTR(ws, W);
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu", W, ws_bytes, need);
+  if ((st = check_aligned(ws, "ws", W)) != MOE_OK) return st;
+  const Named in[] = {{{x, x_stride, w->K, T}, "x"}, {dense(ws, (int64_t)need, 1), "ws"}};
+  if ((st = check_all_apart(out, in, false, W)) != MOE_OK) return st;
+  if (moe::mx_linear_takes_rows(fmt, w->N, w->K, T))
+    return hip_status(W, moe::launch_mx_linear(w, fmt, x, x_stride, nullptr, nullptr, T, y, y_stride, y_dtype, stream));
+  const Named rows[] = {in[0]};
+  if ((st = check_all_apart(in[1], rows, false, W)) != MOE_OK) return st;
+  uint8_t* const codes = (uint8_t*)ws;
+  uint8_t* const scales = codes + moe::align_up((size_t)T * code_bytes(fmt, w->K));
+  const hipError_t e = moe::launch_mx_quant(fmt, w->K, T, x, x_stride, codes, scales, stream);
+  if (e != hipSuccess) return hip_status(W, e);
+  return hip_status(W, moe::launch_mx_linear(w, fmt, nullptr, 0, codes, scales, T, y, y_stride, y_dtype, stream));
 }
 
 }  // extern "C"
