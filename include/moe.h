@@ -537,6 +537,24 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
                            float scale, uint16_t* out, int64_t out_stride, void* ws,
                            size_t ws_bytes, hipStream_t stream);
 
+/* The same attention for steps with many rows of a sequence: a prompt's chunks
+ * behind what is cached of it, alone or beside other slots' decode steps, long
+ * verification batches.  Arguments, results for rows that see nothing, bad pages
+ * and rows outside the sequences as for moe_attn_decode; the two differ in how
+ * they cut the work (here a cached token is decoded once for all rows of a tile
+ * of 128 (row, head) pairs) and in rounding: keys, values and softmax weights
+ * meet the matrix units as bf16 for every format (NVFP4 values, code times scale,
+ * are exact in it; Q8_0 values are rounded once, as moe_kv_read does), the
+ * query rows as they are.
+ * ws: moe_attn_chunk_workspace_bytes of the same cache, heads and n_seq, with
+ * this T and max_len or larger ones. */
+size_t moe_attn_chunk_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_seq, int64_t T,
+                                      int64_t max_len);
+moe_status moe_attn_chunk(const moe_kv_cache* c, const moe_seq_batch* s, int32_t n_q,
+                          const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
+                          float scale, uint16_t* out, int64_t out_stride, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+
 /* Causal attention over whole prompts (or chunks of them), packed: sequence b
  * has the query rows q_start[b] .. q_start[b+1]-1 and the key and value rows
  * kv_start[b] .. kv_start[b+1]-1, the queries being the last of the keys'

@@ -161,6 +161,9 @@ SIGNATURES = {
     "moe_attn_workspace_bytes": (_sz, [_CP, _i32, _i32, _i64, _i64]),
     "moe_attn_decode": (ctypes.c_int, [_CP, _SP, _i32, _vp, _i64, _i64, _i64, _f32, _vp, _i64, _vp,
                                        _sz, _vp]),
+    "moe_attn_chunk_workspace_bytes": (_sz, [_CP, _i32, _i32, _i64, _i64]),
+    "moe_attn_chunk": (ctypes.c_int, [_CP, _SP, _i32, _vp, _i64, _i64, _i64, _f32, _vp, _i64, _vp,
+                                      _sz, _vp]),
     "moe_attn_prompt": (ctypes.c_int, [_i32, _i32, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp,
                                        _i64, _vp, _i64, _f32, _vp, _i64, _vp]),
     "moe_add_norm": (ctypes.c_int, [_i32, _i64, _vp, _i64, _vp, _i64, _vp, _f32, _vp, _i64, _vp, _i64,
@@ -343,6 +346,17 @@ def moe_attn_decode(cache, seqs, n_q, q, q_stride, T, max_len, scale, out, out_s
     _check(lib().moe_attn_decode(ctypes.byref(cache), ctypes.byref(seqs), n_q, _ptr(q), q_stride, T,
                                  max_len, scale, _ptr(out), out_stride, _ptr(ws), ws_bytes,
                                  _stream(stream)))
+
+
+def moe_attn_chunk_workspace_bytes(cache, n_q, n_seq, T, max_len=0) -> int:
+    return lib().moe_attn_chunk_workspace_bytes(ctypes.byref(cache), n_q, n_seq, T, max_len)
+
+
+def moe_attn_chunk(cache, seqs, n_q, q, q_stride, T, max_len, scale, out, out_stride, ws, ws_bytes,
+                   stream=None):
+    _check(lib().moe_attn_chunk(ctypes.byref(cache), ctypes.byref(seqs), n_q, _ptr(q), q_stride, T,
+                                max_len, scale, _ptr(out), out_stride, _ptr(ws), ws_bytes,
+                                _stream(stream)))
 
 
 def moe_attn_prompt(n_q, n_kv, D, n_seq, q_start, kv_start, T, Tk, q, q_stride, k, k_stride, v,

@@ -649,6 +649,18 @@ moe_status check_scale(float scale, const char* where) {
   return MOE_OK;
 }
 
+// The arguments that a workspace's size goes by.
+moe_status check_attn_sizes(const moe_kv_cache* c, int n_q, int n_seq, int64_t T, int64_t max_len,
+                                   const char* where) {
+  if (!c) return fail(MOE_ERR_INVALID_ARG, "%s: c is NULL", where);
+  moe_status st = check_cache_shape(c->fmt, c->n_kv, c->D, c->page_tokens, where);
+  if (st != MOE_OK) return st;
+  if ((st = check_heads(n_q, c->n_kv, T, n_seq, where)) != MOE_OK) return st;
+  if (n_seq < 0 || max_len < 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: n_seq=%d max_len=%lld", where, n_seq, (long long)max_len);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -763,17 +775,7 @@ moe_status moe_kv_read(const moe_kv_cache* c, const moe_seq_batch* s, const int3
 
 size_t moe_attn_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_seq, int64_t T,
                                 int64_t max_len) {
-  const char* W = "moe_attn_workspace_bytes";
-  if (!c) {
-    fail(MOE_ERR_INVALID_ARG, "%s: c is NULL", W);
-    return 0;
-  }
-  if (check_cache_shape(c->fmt, c->n_kv, c->D, c->page_tokens, W) != MOE_OK) return 0;
-  if (check_heads(n_q, c->n_kv, T, n_seq, W) != MOE_OK) return 0;
-  if (n_seq < 0 || max_len < 0) {
-    fail(MOE_ERR_INVALID_ARG, "%s: n_seq=%d max_len=%lld", W, n_seq, (long long)max_len);
-    return 0;
-  }
+  if (check_attn_sizes(c, n_q, n_seq, T, max_len, "moe_attn_workspace_bytes") != MOE_OK) return 0;
   // max_len 0 stands for the page table's capacity, which is not known here:
   // the longest cache gives the largest split.  Fewer rows can need more (they
   // are split finer); beyond kSplitPairs there are no splits.
@@ -809,6 +811,43 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
   if ((st = check_apart({out, out_stride, qw, T}, {q, q_stride, qw, T}, true, "out", "q", W)) != MOE_OK) return st;
   return hip_status(W, moe::launch_attn_decode(c, s, n_q, q, q_stride, T, max_len, scale, out,
                                                out_stride, ws, stream));
+}
+
+size_t moe_attn_chunk_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_seq, int64_t T,
+                                      int64_t max_len) {
+  if (check_attn_sizes(c, n_q, n_seq, T, max_len, "moe_attn_chunk_workspace_bytes") != MOE_OK) return 0;
+  // (as above: the longest cache gives the largest split, and fewer rows can need more)
+  size_t most = 0;
+  for (int64_t t = 1; t <= T && t * n_q <= moe::kChunkPairs; ++t)
+    most = std::max(most, moe::attn_chunk_ws_bytes(c->n_kv, c->D, n_q, n_seq, t, max_len ? max_len : INT32_MAX));
+  return most;
+}
+
+moe_status moe_attn_chunk(const moe_kv_cache* c, const moe_seq_batch* s, int32_t n_q,
+                          const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
+                          float scale, uint16_t* out, int64_t out_stride, void* ws,
+                          size_t ws_bytes, hipStream_t stream) {
+  const char* W = "moe_attn_chunk";
+  moe_status st = check_cache(c, W);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(s, true, W)) != MOE_OK) return st;
+  if ((st = check_heads(n_q, c->n_kv, T, s->n_seq, W)) != MOE_OK) return st;
+  if ((st = check_scale(scale, W)) != MOE_OK) return st;
+  if (max_len < 0) return fail(MOE_ERR_INVALID_ARG, "%s: max_len=%lld < 0", W, (long long)max_len);
+  if (T == 0 || s->n_seq == 0) return MOE_OK;
+  const int64_t qw = (int64_t)n_q * c->D;
+  if ((st = check_rows(q, q_stride, qw, "q", W)) != MOE_OK) return st;
+  if ((st = check_rows(out, out_stride, qw, "out", W)) != MOE_OK) return st;
+  if (max_len == 0) max_len = (int64_t)s->max_pages * c->page_tokens;
+  const size_t need = moe::attn_chunk_ws_bytes(c->n_kv, c->D, n_q, s->n_seq, T, max_len);
+  if (need > 0) {
+    CHECK_PTR(ws, W);
+    if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu", W, ws_bytes, need);
+    if ((st = check_aligned(ws, "ws", W)) != MOE_OK) return st;
+  }
+  if ((st = check_apart({out, out_stride, qw, T}, {q, q_stride, qw, T}, true, "out", "q", W)) != MOE_OK) return st;
+  return hip_status(W, moe::launch_attn_chunk(c, s, n_q, q, q_stride, T, max_len, scale, out,
+                                              out_stride, ws, stream));
 }
 
 moe_status moe_attn_prompt(int32_t n_q, int32_t n_kv, int32_t D, int32_t n_seq,

@@ -15,6 +15,9 @@
 
 namespace moe {
 
+constexpr float kNone = -3.0e38f;  // running maximum before any token
+constexpr float kGrow = 8.0f;      // log2 headroom before the accumulators are rescaled
+
 // Two values as bf16, rounded to nearest even.
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   typedef __bf16 v2b __attribute__((ext_vector_type(2)));
@@ -154,6 +157,13 @@ hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int
                               const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
                               float scale, uint16_t* out, int64_t out_stride, void* ws,
                               hipStream_t stream);
+// The same in moe_attn_chunk, whose tiles of rows are larger.
+constexpr int64_t kChunkPairs = 1 << 16;
+size_t attn_chunk_ws_bytes(int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len);
+hipError_t launch_attn_chunk(const moe_kv_cache* c, const moe_seq_batch* s, int n_q,
+                             const uint16_t* q, int64_t q_stride, int64_t T, int64_t max_len,
+                             float scale, uint16_t* out, int64_t out_stride, void* ws,
+                             hipStream_t stream);
 hipError_t launch_attn_prompt(int n_q, int n_kv, int D, int n_seq, const int32_t* q_start,
                               const int32_t* kv_start, int64_t T, int64_t Tk, const uint16_t* q,
                               int64_t q_stride, const uint16_t* k, int64_t k_stride,

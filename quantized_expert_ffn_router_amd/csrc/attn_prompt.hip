@@ -20,20 +20,11 @@
 // masked, and the output weigh more.  333 rows take 12 us: six tiles of keys one
 // after the other, 1.1 us each, on a card that is mostly empty.  8192 rows at heads
 // of 64, 128 and 256: 280, 478 and 1030 us (0.98, 1.15 and 1.07 PFLOP/s).
-#include "attn_common.h"
+#include "attn_tile.h"
 
 namespace moe {
 
 namespace {
-
-typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef short v4s __attribute__((ext_vector_type(4)));
-
-constexpr int kBN = 64;            // keys of a tile
-constexpr float kNone = -3.0e38f;  // running maximum before any token
-constexpr float kGrow = 8.0f;      // log2 headroom before the accumulators are rescaled
 
 struct PromptArgs {
   const int32_t* q_start;
@@ -46,29 +37,6 @@ struct PromptArgs {
   int n_q, G, n_seq;
   float c;  // scale * log2(e)
 };
-
-__device__ __forceinline__ v16f mma(v4u a, v4u b, v16f c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a),
-                                                 __builtin_bit_cast(v8b, b), c, 0, 0, 0);
-}
-
-// Place of 16-byte chunk `chunk` of row `row` in an LDS tile of D-wide rows:
-// chunks are permuted within their row so that neither the row-wise reads of K
-// (32 rows, one chunk column) nor the transposed reads of V (4 rows, 4 chunk
-// columns) meet twice in a bank.
-template <int D>
-__device__ __forceinline__ int swz(int row, int chunk) {
-  if constexpr (D == 64) return chunk ^ (((row & 1) << 2) | ((row >> 1) & 3));
-  else return chunk ^ (((row & 3) << 2) | ((row >> 2) & 3));
-}
-
-// Waits until at most N of the wave's loads are on their way (its newest ones).
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0f70);
-#endif
-}
 
 // One head's key or value rows of a sequence, as tiles of 64 rows that go
 // straight from global memory into LDS: lane i of a load fills the 16 bytes at
@@ -107,26 +75,14 @@ struct Tiles {
   }
 };
 
-// Two softmax weights as bf16, rounded to nearest even (half a step, 2^-8: the
-// operand type of the second product), and their sum added to l -- of the
-// rounded weights, so that rounding does not shift a row's mean.
-__device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
-  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
-  const v2b w = {(__bf16)a, (__bf16)b};
-  const v2b one = {(__bf16)1.0f, (__bf16)1.0f};
-  *l = __builtin_amdgcn_fdot2_f32_bf16(w, one, *l, false);
-  return __builtin_bit_cast(uint32_t, w);
-}
-
 // One wave's 32 query rows of one head; a lane column is a row.
 template <int D>
-struct Rows {
+struct Rows : TileRows<D> {
   static constexpr int KS = D / 16, NJ = D / 32;
-  v4u qf[KS];
-  v16f o[NJ];
-  float m, l;
-  int64_t limit;               // this lane's row: last key it sees
-  int h;                       // half of the wave
+  using TileRows<D>::qf;
+  using TileRows<D>::o;
+  using TileRows<D>::h;
+  using TileRows<D>::weight;
   uint32_t ka[KS], va[NJ][2];  // this lane's places in a K and a V tile
 
   __device__ __forceinline__ void places(int lane) {
@@ -142,14 +98,6 @@ struct Rows {
         const int col = 32 * j + ((lane >> 4) & 1) * 16 + 4 * (lane & 3);
         va[j][q] = row * (2 * D) + swz<D>(row, col >> 3) * 16 + (col & 4) * 2;
       }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
-    m = kNone;
-    l = 0.0f;
   }
   // Key fragment: 16 elements (step s) of 32 keys (half t).  The permutation
   // of chunks repeats every 16 rows, so half t is a constant away.
@@ -178,38 +126,6 @@ struct Rows {
 #pragma unroll
       for (int s = 0; s < KS; ++s) x[t] = mma(key(kt, t, s), qf[s], x[t]);
     }
-  }
-  __device__ __forceinline__ void mask(v16f (&x)[2], int64_t t0) const {
-    const int left = (int)min(max(limit - t0, (int64_t)-1), (int64_t)kBN) - 4 * h;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (32 * t + 8 * (i >> 2) + (i & 3) > left) x[t][i] = -__builtin_inff();
-  }
-  // Largest scaled score of this lane's row.
-  __device__ __forceinline__ float top(const v16f (&x)[2], float c) const {
-    float mx = x[0][0];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[t][i]);
-    const uint32_t u = __float_as_uint(mx);
-    const auto w = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])) * c;
-  }
-  // The lane's sum, over both halves of the wave.
-  __device__ __forceinline__ void finish() {
-    const uint32_t u = __float_as_uint(l);
-    const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    l = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-  // Weight v of the tile's 32 per lane; a pair is rounded when its second value
-  // is there.
-  __device__ __forceinline__ void weight(v16f (&x)[2], float c, v4u (&p)[4], int v) {
-    const int t = v >> 4, i = v & 15;
-    x[t][i] = __builtin_amdgcn_exp2f(fmaf(x[t][i], c, -m));
-    if (i & 1) p[v >> 3][(i & 7) >> 1] = weight_pair(x[t][i - 1], x[t][i], &l);
   }
   // The scores y of one tile (K in kt) and the weighted values of the tile before
   // (scores x, V in vt), as one stream: a matrix instruction, then a piece of
