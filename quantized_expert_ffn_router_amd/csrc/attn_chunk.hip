@@ -53,13 +53,11 @@ __device__ __forceinline__ int vswz(int quad, int chunk) {
   else return chunk ^ ((chunk >> 4) & 7);
 }
 
-// 64 tokens of one key/value head on their way from the cache into LDS, where keys are
-// rows of D bf16 (as in the prompt kernel) and values quads [16][D][4].  Each half, 32
-// tokens, lies within one page.
-struct Half {
+// Where the 32 tokens of a unit lie.
+struct Unit32 {
   const uint8_t* block;  // the (page, head) block
   int bytes;             // of it: 0 where there is none
-  int o;                 // the half's first token within the page
+  int o;                 // the unit's first token within the page
   __device__ __forceinline__ Rsrc rsrc() const {
 #if defined(__HIP_DEVICE_COMPILE__)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(block), 0, bytes, 0x00020000);
@@ -68,29 +66,43 @@ struct Half {
 #endif
   }
 };
-struct Halves {
-  Half a, b;
-  __device__ __forceinline__ Half of(int token) const {  // (token: the same for the whole wave)
+// Where the 64 tokens of a tile lie.
+struct Place {
+  Unit32 a, b;
+  __device__ __forceinline__ Unit32 of(int token) const {  // (token: the same for the whole wave)
     const bool second = token >= 32;
-    return Half{second ? b.block : a.block, second ? b.bytes : a.bytes, second ? b.o : a.o};
+    return Unit32{second ? b.block : a.block, second ? b.bytes : a.bytes, second ? b.o : a.o};
   }
 };
+
+// A tile's codes on their way from the cache into LDS, where keys are rows of D bf16 (as
+// in the prompt kernel) and values quads [16][D][4]: as they were loaded, decoded piece by
+// piece.  A piece is one 16-byte store of a lane.
 template <int FMT, int D, int W>
-struct CacheTile {
-  static constexpr bool FP4 = FMT == MOE_FMT_NVFP4, Q8 = FMT == MOE_FMT_Q8_0;
+struct Codes {
+  static constexpr bool FP4 = FMT == MOE_FMT_NVFP4;
+  static constexpr int ROW = FP4 ? D / 2 : D;  // bytes of a token's codes
   // Keys: 16 bytes of a token a lane, PT of them a token; TL neighbouring lanes take
   // neighbouring tokens (so that 16 lanes' writes fall into different banks), a load of
   // the wave PB pieces of 64 / PB tokens.
-  static constexpr int ROW = FP4 ? D / 2 : Q8 ? D : 2 * D;  // bytes of a token's codes
   static constexpr int PT = ROW / 16;
   static constexpr int TL = FP4 ? (D == 64 ? 8 : 16) : D == 64 ? 4 : 8;
   static constexpr int PB = PT < 64 / TL ? PT : 64 / TL;
   static constexpr int KI = (PT + W - 1) / W;  // loads of a wave (PT in all)
-  // Values: UQ pieces of a quad, a piece of UW words of a lane
+  // Values: UQ parts of a quad, a part of UW words of a lane; where the keys do not need
+  // all waves, the others take the values.
   static constexpr int UQ = FP4 ? (D == 64 ? 8 : 16) : D / 4;
   static constexpr int UW = FP4 && D == 256 ? 8 : 4;
-  static constexpr int VL = UQ / 4, VI = (VL + W - 1) / W;
-  uint32_t kq[KI][4], ks[KI], vq[VI][UW], vs[VI][2];
+  static constexpr int VL = UQ / 4, VI = (VL + W - 1) / W, VOFF = PT < W ? W - PT : 0;
+  static constexpr int KC = FP4 ? 4 : 2, VC = FP4 ? UW : 2;  // pieces of a load
+  static constexpr int PIECES = KI * KC + VI * VC;
+  // What a wave holds of load i of keys or of values; no wave holds both where their loads
+  // together are no more than the waves.
+  static constexpr bool EITHER = PT + VL <= W;
+  static constexpr int LOADS = EITHER ? 1 : KI + VI;
+  uint32_t code[LOADS][UW], scale[LOADS][2];
+  static constexpr int of_key(int i) { return i; }
+  static constexpr int of_value(int i) { return EITHER ? i : KI + i; }
 
   __device__ __forceinline__ static uint32_t load(Rsrc r, uint32_t at, uint32_t base, int bytes) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -106,165 +118,156 @@ struct CacheTile {
     d[0] = x[0]; d[1] = x[1]; d[2] = x[2]; d[3] = x[3];
 #endif
   }
-  // Of key load i: its first token, this lane's token behind it and piece.
+  // Load i of a wave among all loads of keys (of values); one from PT (VL) on is none.
+  __device__ __forceinline__ static int key_load(int i, int wave) { return i * W + wave; }
+  __device__ __forceinline__ static int value_load(int i, int wave) { return i * W + (wave + VOFF) % W; }
+  // Of key load wi: its first token, this lane's token behind it and part.
   __device__ __forceinline__ static int key_block(int wi) { return wi / (PT / PB) * (64 / PB); }
   __device__ __forceinline__ static int key_token(int lane) { return lane % TL + TL * (lane / TL / PB); }
-  __device__ __forceinline__ static int key_piece(int wi, int lane) { return wi % (PT / PB) * PB + lane / TL % PB; }
+  __device__ __forceinline__ static int key_part(int wi, int lane) { return wi % (PT / PB) * PB + lane / TL % PB; }
 
-  __device__ __forceinline__ void fetch(const Halves& half, const KvLayout lay, int P, int wave, int lane) {
+  __device__ __forceinline__ void fetch_keys(const Place& from, const KvLayout lay, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
-      const int wi = i * W + wave;
-      if (PT % W != 0 && wi >= PT) break;
+      const int wi = key_load(i, wave);
+      if (wi >= PT) break;
       const int tb = key_block(wi);
-      const Half hf = half.of(tb);
-      const Rsrc block = hf.rsrc();
-      const int tok = hf.o + (tb & 31) + key_token(lane), piece = key_piece(wi, lane);
-      load_16(block, kq[i], tok * ROW + piece * 16, 0);
-      if constexpr (FP4) ks[i] = load(block, tok * (D / 16) + piece * 2, lay.ks, 2);
-      else ks[i] = load(block, 2 * (tok * (D / 32) + piece / 2), lay.ks, 2);
+      const Unit32 u = from.of(tb);
+      const Rsrc block = u.rsrc();
+      const int tok = u.o + (tb & 31) + key_token(lane), part = key_part(wi, lane);
+      load_16(block, code[of_key(i)], tok * ROW + part * 16, 0);
+      if constexpr (FP4) scale[of_key(i)][0] = load(block, tok * (D / 16) + part * 2, lay.ks, 2);
+      else scale[of_key(i)][0] = load(block, 2 * (tok * (D / 32) + part / 2), lay.ks, 2);
     }
+  }
+  __device__ __forceinline__ void fetch_values(const Place& from, const KvLayout lay, int P, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
-      const int wi = i * W + wave;
-      if (VL % W != 0 && wi >= VL) break;
+      const int wi = value_load(i, wave);
+      if (wi >= VL) break;
       const int first = wi * 64 / UQ;  // quad
-      const Half hf = half.of(4 * first);
-      const Rsrc block = hf.rsrc();
-      const int quad = first + lane / UQ, piece = lane % UQ, tok = hf.o + (quad & 7) * 4;
-      const uint32_t at = tok * ROW + piece * (UW * 4);
-      load_16(block, vq[i], at, lay.vq);
-      if constexpr (UW == 8) load_16(block, vq[i] + 4, at + 16, lay.vq);
-      const int e = piece * (D / UQ);  // first element
+      const Unit32 u = from.of(4 * first);
+      const Rsrc block = u.rsrc();
+      const int quad = first + lane / UQ, part = lane % UQ, tok = u.o + (quad & 7) * 4;
+      const uint32_t at = tok * ROW + part * (UW * 4);
+      load_16(block, code[of_value(i)], at, lay.vq);
+      if constexpr (UW == 8) load_16(block, code[of_value(i)] + 4, at + 16, lay.vq);
+      const int e = part * (D / UQ);  // first element
       if constexpr (FP4) {
-        vs[i][0] = load(block, e / 16 * P + tok, lay.vs, 4);
+        scale[of_value(i)][0] = load(block, e / 16 * P + tok, lay.vs, 4);
       } else {
         const uint32_t s = 2 * (e / 32 * P + tok);
-        vs[i][0] = load(block, s, lay.vs, 4);
-        vs[i][1] = load(block, s + 4, lay.vs, 4);
+        scale[of_value(i)][0] = load(block, s, lay.vs, 4);
+        scale[of_value(i)][1] = load(block, s + 4, lay.vs, 4);
       }
     }
   }
 
+  __device__ __forceinline__ void put_key(int i, int w, uint8_t* kt, int wave, int lane) const {
+    const int wi = key_load(i, wave);
+    if (wi >= PT) return;
+    const int row = key_block(wi) + key_token(lane), part = key_part(wi, lane);
+    uint32_t c[4];
+    if constexpr (FP4) {
+      const v2f s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(scale[of_key(i)][0], 1.0f, false);
+      const float f = w < 2 ? s[0] : s[1];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const v2f v = fp4_pair(code[of_key(i)][w], k);
+        c[k] = bf16_pair(v[0] * f, v[1] * f);
+      }
+    } else {
+      const float f = half_value(scale[of_key(i)][0], 0), minus = -128.0f * f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t b = code[of_key(i)][2 * w + (k >> 1)] ^ 0x80808080u;
+        c[k] = bf16_pair(q8_value(b, 2 * (k & 1), f, minus), q8_value(b, 2 * (k & 1) + 1, f, minus));
+      }
+    }
+    *reinterpret_cast<uint4*>(kt + row * (2 * D) + swz<D>(row, part * KC + w) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+  }
   // left: the tile's tokens that some row sees; values from there on count as 0, whatever
   // the cache holds.
-  __device__ __forceinline__ void put(uint8_t* kt, uint8_t* vt, int left, int wave, int lane) {
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const int wi = i * W + wave;
-      if (PT % W != 0 && wi >= PT) break;
-      const int row = key_block(wi) + key_token(lane), piece = key_piece(wi, lane);
-      uint8_t* const d = kt + row * (2 * D);
-      if constexpr (FP4) {
-        const v2f s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(ks[i], 1.0f, false);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float f = w < 2 ? s[0] : s[1];
-          uint32_t c[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const v2f v = fp4_pair(kq[i][w], k);
-            c[k] = bf16_pair(v[0] * f, v[1] * f);
-          }
-          *reinterpret_cast<uint4*>(d + swz<D>(row, piece * 4 + w) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-        }
-      } else {
-        const float f = half_value(ks[i], 0), minus = -128.0f * f;
-#pragma unroll
-        for (int w = 0; w < 4; w += 2) {
-          uint32_t c[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t b = kq[i][w + (k >> 1)] ^ 0x80808080u;
-            c[k] = bf16_pair(q8_value(b, 2 * (k & 1), f, minus), q8_value(b, 2 * (k & 1) + 1, f, minus));
-          }
-          *reinterpret_cast<uint4*>(d + swz<D>(row, piece * 2 + w / 2) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-        }
-      }
-    }
+  __device__ __forceinline__ void cut_values(int left, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
-      const int wi = i * W + wave;
-      if (VL % W != 0 && wi >= VL) break;
-      const int quad = wi * 64 / UQ + lane / UQ, piece = lane % UQ;
-      uint8_t* const d = vt + quad * (8 * D);
-      if (left < kBN) {
-        const int n = min(max(left - 4 * quad, 0), 4);
-        if constexpr (FP4) {
-          vs[i][0] = n >= 4 ? vs[i][0] : vs[i][0] & ((1u << (8 * n)) - 1u);
-        } else {
-          vs[i][0] &= n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
-          vs[i][1] &= n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
-        }
-      }
-      float s[4];
+      const int wi = value_load(i, wave), n = min(max(left - 4 * (wi * 64 / UQ + lane / UQ), 0), 4);
+      if (wi >= VL) break;
       if constexpr (FP4) {
-        const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs[i][0], 1.0f, false);
-        const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs[i][0], 1.0f, true);
-        s[0] = a[0]; s[1] = a[1]; s[2] = b[0]; s[3] = b[1];
-        constexpr int NC = D == 256 ? 8 : 4;  // chunks of a piece
-#pragma unroll
-        for (int e = 0; e < NC; ++e) {
-          v2f p[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            // byte e of token t: [4][4 bytes], [4][8 bytes], or twice [4][2 bytes]
-            if constexpr (D == 128) p[t] = fp4_pair(vq[i][t], e);
-            else if constexpr (D == 256) p[t] = fp4_pair(vq[i][2 * t + e / 4], e % 4);
-            else p[t] = fp4_pair(vq[i][e / 2 * 2 + t / 2], 2 * (t & 1) + (e & 1));
-          }
-          *reinterpret_cast<uint4*>(d + vswz<D>(quad, piece * NC + e) * 16) =
-              make_uint4(bf16_pair(p[0][0] * s[0], p[1][0] * s[1]), bf16_pair(p[2][0] * s[2], p[3][0] * s[3]),
-                         bf16_pair(p[0][1] * s[0], p[1][1] * s[1]), bf16_pair(p[2][1] * s[2], p[3][1] * s[3]));
-        }
+        scale[of_value(i)][0] = n >= 4 ? scale[of_value(i)][0] : scale[of_value(i)][0] & ((1u << (8 * n)) - 1u);
       } else {
-        float minus[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          s[t] = half_value(vs[i][t >> 1], t & 1);
-          minus[t] = -128.0f * s[t];
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t c[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t b = vq[i][2 * e + (k >> 1)] ^ 0x80808080u;
-            const int t = 2 * (k & 1);
-            c[k] = bf16_pair(q8_value(b, t, s[t], minus[t]), q8_value(b, t + 1, s[t + 1], minus[t + 1]));
-          }
-          *reinterpret_cast<uint4*>(d + vswz<D>(quad, piece * 2 + e) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-        }
+        scale[of_value(i)][0] &= n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
+        scale[of_value(i)][1] &= n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
       }
     }
+  }
+  __device__ __forceinline__ void put_value(int i, int e, uint8_t* vt, int wave, int lane) const {
+    const int wi = value_load(i, wave);
+    if (wi >= VL) return;
+    const int quad = wi * 64 / UQ + lane / UQ, part = lane % UQ;
+    uint32_t c[4];
+    if constexpr (FP4) {
+      const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(scale[of_value(i)][0], 1.0f, false);
+      const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(scale[of_value(i)][0], 1.0f, true);
+      v2f p[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        // byte e of token t: [4][4 bytes], [4][8 bytes], or twice [4][2 bytes]
+        if constexpr (D == 128) p[t] = fp4_pair(code[of_value(i)][t], e);
+        else if constexpr (D == 256) p[t] = fp4_pair(code[of_value(i)][2 * t + e / 4], e % 4);
+        else p[t] = fp4_pair(code[of_value(i)][e / 2 * 2 + t / 2], 2 * (t & 1) + (e & 1));
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        c[2 * k] = bf16_pair(p[0][k] * a[0], p[1][k] * a[1]);
+        c[2 * k + 1] = bf16_pair(p[2][k] * b[0], p[3][k] * b[1]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t b = code[of_value(i)][2 * e + (k >> 1)] ^ 0x80808080u;
+        const float s0 = half_value(scale[of_value(i)][k & 1], 0), s1 = half_value(scale[of_value(i)][k & 1], 1);
+        c[k] = bf16_pair(q8_value(b, 2 * (k & 1), s0, -128.0f * s0), q8_value(b, 2 * (k & 1) + 1, s1, -128.0f * s1));
+      }
+    }
+    *reinterpret_cast<uint4*>(vt + quad * (8 * D) + vswz<D>(quad, part * VC + e) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+  }
+  // Piece n of this wave's: the keys' first.
+  __device__ __forceinline__ void put(int n, uint8_t* kt, uint8_t* vt, int wave, int lane) const {
+    if (n < KI * KC) put_key(n / KC, n % KC, kt, wave, lane);
+    else put_value((n - KI * KC) / VC, (n - KI * KC) % VC, vt, wave, lane);
   }
 };
 
 // 16-bit caches need no decoding: straight from global memory into LDS, lane i of a load
 // filling the 16 bytes at slot i with the chunk that belongs there.
 template <int D, int W>
-struct CacheTile<MOE_FMT_BF16, D, W> {
-  static constexpr int CPR = D / 8;       // loads of 1 KB: keys, and as many of values
-  static constexpr int N = CPR / W;
-  __device__ __forceinline__ static void fetch(const Halves& half, const KvLayout lay, uint8_t* kt, uint8_t* vt,
-                                               int wave, int lane) {
+struct Codes<MOE_FMT_BF16, D, W> {
+  static constexpr int CPR = D / 8;  // loads of 1 KB: of keys, and as many of values
+  static constexpr int N = CPR / W, PIECES = 0;
+  __device__ __forceinline__ void put(int, uint8_t*, uint8_t*, int, int) const {}
+  static_assert(CPR % W == 0, "waves share the loads evenly");
+  __device__ __forceinline__ static void load(Rsrc r, uint8_t* lds, uint32_t at, uint32_t base) {
 #if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, base, 0, 0);
+#endif
+  }
+  __device__ __forceinline__ static void keys(const Place& from, uint8_t* kt, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int wi = i * W + wave, slot = wi * 64 + lane;
-      const int first = wi * 64 / CPR, row = slot / CPR;  // token
-      const Half hk = half.of(first);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          hk.rsrc(), (__attribute__((address_space(3))) void*)(kt + wi * 1024), 16,
-          (hk.o + (row & 31)) * (2 * D) + swz<D>(row, slot % CPR) * 16, 0, 0, 0);
-      constexpr int CPQ = D / 2;  // chunks of a quad
-      const int q0 = wi * 64 / CPQ, quad = slot / CPQ;
-      const Half hv = half.of(4 * q0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          hv.rsrc(), (__attribute__((address_space(3))) void*)(vt + wi * 1024), 16,
-          (hv.o / 4 + (quad & 7)) * (8 * D) + vswz<D>(quad, slot % CPQ) * 16, lay.vq, 0, 0);
+      const int wi = i * W + wave, slot = wi * 64 + lane, row = slot / CPR;
+      const Unit32 u = from.of(wi * 64 / CPR);
+      load(u.rsrc(), kt + wi * 1024, (u.o + (row & 31)) * (2 * D) + swz<D>(row, slot % CPR) * 16, 0);
     }
-#endif
+  }
+  __device__ __forceinline__ static void values(const Place& from, const KvLayout lay, uint8_t* vt, int wave, int lane) {
+    constexpr int CPQ = D / 2;  // chunks of a quad
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int wi = i * W + wave, slot = wi * 64 + lane, quad = slot / CPQ;
+      const Unit32 u = from.of(4 * (wi * 64 / CPQ));
+      load(u.rsrc(), vt + wi * 1024, (u.o / 4 + (quad & 7)) * (8 * D) + vswz<D>(quad, slot % CPQ) * 16, lay.vq);
+    }
   }
 };
 
@@ -309,7 +312,10 @@ struct ChunkRows : TileRows<D> {
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[t][i] = 0.0f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) x[t] = mma(key(kt, t, s), qf[s], x[t]);
+      for (int s = 0; s < KS; ++s) {
+        x[t] = mma(key(kt, t, s), qf[s], x[t]);
+        if (s % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (few fragments at a time)
+      }
     }
   }
   // A new maximum for the rows whose weights would leave 2^kGrow (the others' answers do
@@ -328,8 +334,16 @@ struct ChunkRows : TileRows<D> {
   }
   // The weighted values of a tile with infinities or NaN among them that some row may not
   // see: a zero weight would not silence them, so one key at a time, added only to the
-  // rows that see it.
-  __device__ __forceinline__ void gather_seen(const uint8_t* vt, const v4u (&p)[4], int64_t t0) {
+  // rows that see it.  (The weights are in the rows' sums already.)
+  __device__ __forceinline__ void gather_seen(const uint8_t* kt, const uint8_t* vt, int64_t t0, float c) {
+    v16f x[2];
+    v4u p[4];
+    scores(kt, x);
+    this->mask(x, t0);
+    const float sum = l;
+#pragma unroll
+    for (int v = 0; v < 32; ++v) this->weight(x, c, p, v);
+    l = sum;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -367,9 +381,14 @@ __device__ __forceinline__ bool wild(const uint8_t* vt, int lane) {
   return __any(any);
 }
 
+// Tile t's scores are computed while the weights of tile t - 1 go through the exponential
+// and, in the shadow of the same matrix instructions, the codes of keys t + 2 and values
+// t + 1 are decoded into the LDS buffers that were read before; those of two tiles further
+// on are on their way meanwhile.
 template <int FMT, int D, int W>
 __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitArgs a) {
   constexpr int KS = D / 16, NJ = D / 32, SIZE = 32 * W, TILE = kBN * D * 2;
+  constexpr bool DECODED = FMT != MOE_FMT_BF16;
   __shared__ __align__(16) uint8_t k_even[TILE], k_odd[TILE], v_even[TILE], v_odd[TILE];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id(), n = lane & 31;
@@ -410,52 +429,26 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
   const int wave_row = (int)((uint32_t)min((it.tile * W + wave) * 32 + 31, last_slot) / (uint32_t)a.G);
   const int64_t hi_wave = (it.tile * W + wave) * 32 <= last_slot ? (int64_t)len - rows + wave_row : -1;
 
-  // Pages of the two halves of tile t (units 2t, 2t + 1), by scalar loads; a unit past the
-  // table's end has none, and one past the last token that is looked at is not looked for.
+  // Pages, by scalar loads; a unit past the table's end has none, one past the last token
+  // that is looked at is not looked for.  Rows that see a token of a page that is not there
+  // have no answer.
   const int* const table = a.s.page_table + (int64_t)it.b * a.s.max_pages;
-  const auto page_at = [&](int u) {
-    if (u >= u_end) return -1;
+  const auto unit = [&](int u) {
     const int i = (int)(((int64_t)u * 32) >> a.s.log2P);
-    const int p = *(const int __attribute__((address_space(4)))*)(uintptr_t)(table + min(i, a.s.max_pages - 1));
-    return i < a.s.max_pages && (unsigned)p < (unsigned)a.s.n_pages ? p : -1;
-  };
-  const auto half_of = [&](int u) {
-    const int p = page_at(u);
-    return Half{heads + (size_t)max(p, 0) * page_bytes, p < 0 ? 0 : (int)lay.head, (u * 32) & (P - 1)};
-  };
-
-  const int first = u_begin / 2, end = (u_end + 1) / 2;
-  CacheTile<FMT, D, W> raw;
-  const auto fetch = [&](int t, uint8_t* kt, uint8_t* vt) {
-    const Halves hf{half_of(2 * t), half_of(2 * t + 1)};
-    if constexpr (FMT == MOE_FMT_BF16) raw.fetch(hf, lay, kt, vt, wave, lane);
-    else raw.fetch(hf, lay, P, wave, lane);
-  };
-  const auto left_of = [&](int t) { return (int)min(plan.hi + 1 - (int64_t)t * kBN, (int64_t)kBN); };
-  // Tile t against this wave's rows.
-  const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
-    const int64_t t0 = (int64_t)t * kBN;
-    if (t0 > hi_wave) return;
-    const bool edge = t0 + kBN - 1 > plan.lo;
-    v16f x[2];
-    v4u p[4];
-    w.scores(kt, x);
-    if (edge) w.mask(x, t0);
-    w.raise(x, a.scale_log2);
-#pragma unroll
-    for (int v = 0; v < 32; ++v) w.weight(x, a.scale_log2, p, v);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)  // nothing to read: rows that see a token of it have no answer
-      if (page_at(2 * t + k) < 0 && w.limit >= t0 + 32 * k && 2 * t + k < u_end) w.l = __uint_as_float(0x7fc00000u);
-    if (edge && wild<D>(vt, lane)) {
-      w.gather_seen(vt, p, t0);
-      return;
+    int p = -1;
+    if (u < u_end) {
+      p = *(const int __attribute__((address_space(4)))*)(uintptr_t)(table + min(i, a.s.max_pages - 1));
+      if (i >= a.s.max_pages || (unsigned)p >= (unsigned)a.s.n_pages) p = -1;
+      if (p < 0 && w.limit >= (int64_t)u * 32) w.l = __uint_as_float(0x7fc00000u);
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) w.o[j] = mma(w.value(vt, s, j), p[s], w.o[j]);
+    return Unit32{heads + (size_t)max(p, 0) * page_bytes, p < 0 ? 0 : (int)lay.head, (u * 32) & (P - 1)};
   };
+  const auto place = [&](int t) { return Place{unit(2 * t), unit(2 * t + 1)}; };
+  const int first = u_begin / 2, end = (u_end + 1) / 2;
+  // tiles before this one are seen by all rows
+  const int full = (int)min(max((plan.lo + 1) >> 6, (int64_t)0), (int64_t)end);
+  const auto left_of = [&](int t) { return (int)min(plan.hi + 1 - (int64_t)t * kBN, (int64_t)kBN); };
+
   // 16-bit values behind the last one that is seen, cleared in LDS.
   const auto clear_behind = [&](int t, uint8_t* vt) {
     const int left = left_of(t);
@@ -470,38 +463,140 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
     }
     __syncthreads();
   };
+
+  bool some_wild = false;
+  typedef Codes<FMT, D, W> C;
+  const auto put_all = [&](const C& c, uint8_t* kt, uint8_t* vt) {
+    each<0, C::PIECES>([&](auto p) { c.put(p(), kt, vt, wave, lane); });
+  };
   if (first < end) {
-    if constexpr (FMT == MOE_FMT_BF16) {
-      fetch(first, k_even, v_even);
-      const auto turn = [&](int t, uint8_t* kt, uint8_t* vt, uint8_t* kn, uint8_t* vn) {
+    // What an even and what an odd turn decode, fetched two turns ahead; heads of 256 have
+    // registers for one.
+    constexpr bool TWO = D <= 128;
+    C c_even, c_two;
+    C& c_odd = TWO ? c_two : c_even;
+    Place next;  // of the keys fetched last: the values' one turn later
+    // keys of tile t, values of tile t - 1
+    const auto fetch = [&](C& c, int t, uint8_t* kt, uint8_t* vt) {
+      const Place before = next;
+      next = place(t);
+      if constexpr (DECODED) {
+        c.fetch_keys(next, lay, wave, lane);
+        c.fetch_values(before, lay, P, wave, lane);
+      } else {
+        c.keys(next, kt, wave, lane);
+        c.values(before, lay, vt, wave, lane);
+      }
+    };
+    // The first tile's keys and values, the second one's keys; what the first two turns
+    // decode (16 bits: load).
+    const Place p0 = place(first);
+    next = place(first + 1);
+    if constexpr (DECODED) {
+      C c0;
+      c0.fetch_keys(p0, lay, wave, lane);
+      c0.fetch_values(p0, lay, P, wave, lane);
+      c_odd.fetch_keys(next, lay, wave, lane);
+      if (left_of(first) < kBN) c0.cut_values(left_of(first), wave, lane);
+      put_all(c0, k_even, v_even);
+      each<0, C::KI * C::KC>([&](auto p) { c_odd.put(p(), k_odd, v_odd, wave, lane); });
+      fetch(c_even, first + 2, nullptr, nullptr);
+      if constexpr (TWO) fetch(c_odd, first + 3, nullptr, nullptr);
+    } else {
+      C::keys(p0, k_even, wave, lane);
+      C::values(p0, lay, v_even, wave, lane);
+      C::keys(next, k_odd, wave, lane);
+      wait_loads<0>();
+    }
+    __syncthreads();
+    v16f x[2];
+    w.scores(k_even, x);
+    if (first >= full) w.mask(x, (int64_t)first * kBN);
+
+    // Turn t: x holds tile t's scores, k1 the keys of t + 1, v0 the values of t; the keys
+    // of t + 2 go to k0, the values of t + 1 to v1.
+    const auto begin = [&](int t, C& c, uint8_t* k0, uint8_t* v0, uint8_t* v1) {
+      if constexpr (!DECODED) wait_loads<0>();
+      __syncthreads();  // what this turn reads is there, what it overwrites has been read
+      if constexpr (DECODED) {
+        if (left_of(t + 1) < kBN) c.cut_values(left_of(t + 1), wave, lane);
+      } else {
+        clear_behind(t, v0);
+        fetch(c, t + 2, k0, v1);
+      }
+    };
+    const auto finish = [&](int t, C& c, const v16f (&y)[2]) {
+      x[0] = y[0];
+      x[1] = y[1];
+      if constexpr (DECODED) fetch(c, t + (TWO ? 4 : 3), nullptr, nullptr);
+    };
+    const auto step = [&](int t, C& c, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1) {
+      begin(t, c, k0, v0, v1);
+      v16f y[2];
+      w.raise(x, a.scale_log2);
+      w.template stream<true>([&](int h, int s) { return w.key(k1, h, s); }, [&](int s, int j) { return w.value(v0, s, j); },
+                              a.scale_log2, x, y, [&](auto I) {
+        constexpr int N = 2 * KS + 4 * NJ, i = I();
+        each<C::PIECES * i / N, C::PIECES * (i + 1) / N>([&](auto p) { c.put(p(), k0, v1, wave, lane); });
+      });
+      finish(t, c, y);
+    };
+    // Tiles that not every row sees, and the last ones: a wave leaves out those none of its
+    // rows does.
+    const auto edge_step = [&](int t, C& c, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1) {
+      begin(t, c, k0, v0, v1);
+      put_all(c, k0, v1);
+      const int64_t t0 = (int64_t)t * kBN;
+      v16f y[2];
+      if (t0 <= hi_wave) {
+        uint32_t keep = ~0u;
+        if (t >= full && wild<D>(v0, lane)) {
+          keep = 0u;  // (left for later)
+          some_wild = true;
+        }
+        w.raise(x, a.scale_log2);
+        w.template stream<false>([&](int, int) { return v4u{0, 0, 0, 0}; },
+                                 [&](int s, int j) { return w.value(v0, s, j) & keep; }, a.scale_log2, x, y, [](auto) {});
+      }
+      if (t + 1 < end) {
+        w.scores(k1, y);
+        if (t + 1 >= full) w.mask(y, t0 + kBN);
+      }
+      finish(t, c, y);
+    };
+    int t = first;
+#pragma unroll 1
+    for (; t + 2 < full; t += 2) {
+      step(t, c_even, k_even, k_odd, v_even, v_odd);
+      step(t + 1, c_odd, k_odd, k_even, v_odd, v_even);
+    }
+#pragma unroll 1
+    for (; t < end; t += 2) {
+      edge_step(t, c_even, k_even, k_odd, v_even, v_odd);
+      if (t + 1 < end) edge_step(t + 1, c_odd, k_odd, k_even, v_odd, v_even);
+    }
+  }
+  // Tiles with infinities or NaN among values that some row may not see, once more.
+  if (__syncthreads_or(some_wild)) {
+#pragma unroll 1
+    for (int t = max(first, full); t < end; ++t) {
+      const Place from = place(t);
+      __syncthreads();
+      if constexpr (DECODED) {
+        C c;
+        c.fetch_keys(from, lay, wave, lane);
+        c.fetch_values(from, lay, P, wave, lane);
+        c.cut_values(left_of(t), wave, lane);
+        put_all(c, k_even, v_even);
+        __syncthreads();
+      } else {
+        C::keys(from, k_even, wave, lane);
+        C::values(from, lay, v_even, wave, lane);
         wait_loads<0>();
         __syncthreads();
-        clear_behind(t, vt);
-        if (t + 1 < end) fetch(t + 1, kn, vn);
-        work(t, kt, vt);
-      };
-#pragma unroll 1
-      for (int t = first; t < end; t += 2) {
-        turn(t, k_even, v_even, k_odd, v_odd);
-        if (t + 1 < end) turn(t + 1, k_odd, v_odd, k_even, v_even);
+        clear_behind(t, v_even);
       }
-    } else {
-      fetch(first, nullptr, nullptr);
-      raw.put(k_even, v_even, left_of(first), wave, lane);
-      if (first + 1 < end) fetch(first + 1, nullptr, nullptr);
-      const auto turn = [&](int t, uint8_t* kt, uint8_t* vt, uint8_t* kn, uint8_t* vn) {
-        __syncthreads();
-        if (t + 1 < end) {
-          raw.put(kn, vn, left_of(t + 1), wave, lane);
-          if (t + 2 < end) fetch(t + 2, nullptr, nullptr);
-        }
-        work(t, kt, vt);
-      };
-#pragma unroll 1
-      for (int t = first; t < end; t += 2) {
-        turn(t, k_even, v_even, k_odd, v_odd);
-        if (t + 1 < end) turn(t + 1, k_odd, v_odd, k_even, v_even);
-      }
+      if ((int64_t)t * kBN <= hi_wave && wild<D>(v_even, lane)) w.gather_seen(k_even, v_even, (int64_t)t * kBN, a.scale_log2);
     }
   }
   w.finish();
@@ -542,14 +637,14 @@ struct Shape {
   int S, room, likely;
   int64_t items;
 };
-constexpr int kChunkWaves = 4;
+constexpr int chunk_waves(int D) { return D <= 128 ? 8 : 4; }
 Shape shape_of(int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) {
-  const int G = n_q / n_kv, size = 32 * kChunkWaves;
+  const int G = n_q / n_kv, size = 32 * chunk_waves(D);
   const int64_t units = (std::min(max_len, (int64_t)INT32_MAX) + 31) / 32;  // (lengths are 32-bit)
   const int64_t per_seq = (T + n_seq - 1) / n_seq;
   const int64_t tiles = T * G / size + n_seq;  // at most: one part tile a sequence
   const int64_t base = (int64_t)n_seq * n_kv * ((per_seq * G + size - 1) / size);
-  const int target = 512;
+  const int target = 256;
   Shape r;
   int64_t S = ((int64_t)256 << 20) / (T * n_q * D * 4);
   S = std::min({S, (int64_t)kMaxSplit, (units + kWaves - 1) / kWaves});
@@ -562,10 +657,9 @@ Shape shape_of(int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) 
 
 template <int FMT>
 void launch_chunk(const SplitArgs& a, int D, unsigned grid, hipStream_t stream) {
-  constexpr int W = kChunkWaves, N = 64 * W;
-  if (D == 64) k_attn_chunk<FMT, 64, W><<<grid, N, 0, stream>>>(a);
-  else if (D == 128) k_attn_chunk<FMT, 128, W><<<grid, N, 0, stream>>>(a);
-  else k_attn_chunk<FMT, 256, W><<<grid, N, 0, stream>>>(a);
+  if (D == 64) k_attn_chunk<FMT, 64, chunk_waves(64)><<<grid, 64 * chunk_waves(64), 0, stream>>>(a);
+  else if (D == 128) k_attn_chunk<FMT, 128, chunk_waves(128)><<<grid, 64 * chunk_waves(128), 0, stream>>>(a);
+  else k_attn_chunk<FMT, 256, chunk_waves(256)><<<grid, 64 * chunk_waves(256), 0, stream>>>(a);
 }
 
 }  // namespace

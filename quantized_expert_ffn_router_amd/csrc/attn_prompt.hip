@@ -82,7 +82,6 @@ struct Rows : TileRows<D> {
   using TileRows<D>::qf;
   using TileRows<D>::o;
   using TileRows<D>::h;
-  using TileRows<D>::weight;
   uint32_t ka[KS], va[NJ][2];  // this lane's places in a K and a V tile
 
   __device__ __forceinline__ void places(int lane) {
@@ -127,46 +126,11 @@ struct Rows : TileRows<D> {
       for (int s = 0; s < KS; ++s) x[t] = mma(key(kt, t, s), qf[s], x[t]);
     }
   }
-  // The scores y of one tile (K in kt) and the weighted values of the tile before
-  // (scores x, V in vt), as one stream: a matrix instruction, then a piece of
-  // the softmax in its shadow, and fragments read kAhead steps early.  A weight
-  // is ready when its step of the second product begins: 20 of a lane's 32 go
-  // with the first product, the rest with the first three quarters of the second.
-  // NEXT false: there is no next tile, only the weighted values.
   template <bool NEXT>
   __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, float c,
                                        v16f (&x)[2], v16f (&y)[2]) {
-    constexpr int N1 = 2 * KS, N2 = 4 * NJ, kAhead = 3, kRing = 4;
-    v4u f[kRing], p[4];
-    const auto fragment = [&](int i) {
-      return i < N1 ? key(kt, i / KS, i % KS) : value(vt, (i - N1) / NJ, (i - N1) % NJ);
-    };
-    const auto weights_by = [](int i) {
-      return i < 0 ? 0 : i < N1 ? 20 * (i + 1) / N1 : min(32, 20 + 12 * (i - N1 + 1) / (3 * NJ));
-    };
-    constexpr int I0 = NEXT ? 0 : N1;
-#pragma unroll
-    for (int i = I0; i < I0 + kAhead; ++i) f[i % kRing] = fragment(i);
-    if constexpr (!NEXT) {
-#pragma unroll
-      for (int v = 0; v < weights_by(N1 - 1); ++v) weight(x, c, p, v);
-    }
-#pragma unroll
-    for (int i = I0; i < N1 + N2; ++i) {
-      if (i + kAhead < N1 + N2) f[(i + kAhead) % kRing] = fragment(i + kAhead);
-      if (i < N1) {
-        v16f zero;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) zero[k] = 0.0f;
-        y[i / KS] = mma(f[i % kRing], qf[i % KS], i % KS ? y[i / KS] : zero);
-      } else {
-        const int s = (i - N1) / NJ, j = (i - N1) % NJ;
-        o[j] = mma(f[i % kRing], p[s], o[j]);
-      }
-#pragma unroll
-      for (int v = weights_by(i - 1); v < weights_by(i); ++v) weight(x, c, p, v);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    this->template stream<NEXT>([&](int t, int s) { return key(kt, t, s); },
+                                [&](int s, int j) { return value(vt, s, j); }, c, x, y, [](auto) {});
   }
 };
 

@@ -49,6 +49,16 @@ __device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
   return __builtin_bit_cast(uint32_t, w);
 }
 
+// f of the numbers I .. N - 1, each as a type: where more code depends on the number than a
+// loop's unrolling takes.
+template <int I, int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each<I + 1, N>(f);
+  }
+}
+
 // What a wave carries for 32 query rows: a lane column is one row, its accumulators and
 // statistics the lane's own.
 template <int D>
@@ -99,6 +109,48 @@ struct TileRows {
     const int t = v >> 4, i = v & 15;
     x[t][i] = __builtin_amdgcn_exp2f(fmaf(x[t][i], c, -m));
     if (i & 1) p[v >> 3][(i & 7) >> 1] = weight_pair(x[t][i - 1], x[t][i], &l);
+  }
+  // The scores y of one tile and the weighted values of the tile before (scores x), as one
+  // stream: a matrix instruction, then a piece of the softmax in its shadow, and
+  // fragments, key(half, step) and value(step, block), read kAhead steps early.  A weight
+  // is ready when its step of the second product begins: 20 of a lane's 32 go
+  // with the first product, the rest with the first three quarters of the second.
+  // NEXT false: there is no next tile, only the weighted values.  also(I): the caller's
+  // own work beside matrix instruction I (a type).
+  template <bool NEXT, typename K, typename V, typename A>
+  __device__ __forceinline__ void stream(K key, V value, float c, v16f (&x)[2], v16f (&y)[2], A also) {
+    constexpr int N1 = 2 * KS, N2 = 4 * NJ, kAhead = 3, kRing = 4;
+    v4u f[kRing], p[4];
+    const auto fragment = [&](int i) {
+      return i < N1 ? key(i / KS, i % KS) : value((i - N1) / NJ, (i - N1) % NJ);
+    };
+    const auto weights_by = [](int i) {
+      return i < 0 ? 0 : i < N1 ? 20 * (i + 1) / N1 : min(32, 20 + 12 * (i - N1 + 1) / (3 * NJ));
+    };
+    constexpr int I0 = NEXT ? 0 : N1;
+#pragma unroll
+    for (int i = I0; i < I0 + kAhead; ++i) f[i % kRing] = fragment(i);
+    if constexpr (!NEXT) {
+#pragma unroll
+      for (int v = 0; v < weights_by(N1 - 1); ++v) weight(x, c, p, v);
+    }
+    each<I0, N1 + N2>([&](auto I) {
+      constexpr int i = I();
+      if (i + kAhead < N1 + N2) f[(i + kAhead) % kRing] = fragment(i + kAhead);
+      if (i < N1) {
+        v16f zero;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) zero[k] = 0.0f;
+        y[i / KS] = mma(f[i % kRing], qf[i % KS], i % KS ? y[i / KS] : zero);
+      } else {
+        const int s = (i - N1) / NJ, j = (i - N1) % NJ;
+        o[j] = mma(f[i % kRing], p[s], o[j]);
+      }
+#pragma unroll
+      for (int v = weights_by(i - 1); v < weights_by(i); ++v) weight(x, c, p, v);
+      also(I);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   }
 };
 
