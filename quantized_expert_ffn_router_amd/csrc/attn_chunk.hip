@@ -77,145 +77,154 @@ struct Place {
 
 // A tile's codes on their way from the cache into LDS, where keys are rows of D bf16 (as
 // in the prompt kernel) and values quads [16][D][4]: as they were loaded, decoded piece by
-// piece.  A piece is one 16-byte store of a lane.
+// piece.  A piece is one 16-byte store of a lane, 8 elements of a key or 2 of four tokens'
+// values; every lane has N of each, so that no piece is behind a branch (which would let
+// the compiler move the softmax out of the matrix instructions' shadow).
 template <int FMT, int D, int W>
 struct Codes {
   static constexpr bool FP4 = FMT == MOE_FMT_NVFP4;
   static constexpr int ROW = FP4 ? D / 2 : D;  // bytes of a token's codes
-  // Keys: 16 bytes of a token a lane, PT of them a token; TL neighbouring lanes take
-  // neighbouring tokens (so that 16 lanes' writes fall into different banks), a load of
-  // the wave PB pieces of 64 / PB tokens.
-  static constexpr int PT = ROW / 16;
-  static constexpr int TL = FP4 ? (D == 64 ? 8 : 16) : D == 64 ? 4 : 8;
-  static constexpr int PB = PT < 64 / TL ? PT : 64 / TL;
-  static constexpr int KI = (PT + W - 1) / W;  // loads of a wave (PT in all)
-  // Values: UQ parts of a quad, a part of UW words of a lane; where the keys do not need
-  // all waves, the others take the values.
-  static constexpr int UQ = FP4 ? (D == 64 ? 8 : 16) : D / 4;
-  static constexpr int UW = FP4 && D == 256 ? 8 : 4;
-  static constexpr int VL = UQ / 4, VI = (VL + W - 1) / W, VOFF = PT < W ? W - PT : 0;
-  static constexpr int KC = FP4 ? 4 : 2, VC = FP4 ? UW : 2;  // pieces of a load
-  static constexpr int PIECES = KI * KC + VI * VC;
-  // What a wave holds of load i of keys or of values; no wave holds both where their loads
-  // together are no more than the waves.
-  static constexpr bool EITHER = PT + VL <= W;
-  static constexpr int LOADS = EITHER ? 1 : KI + VI;
-  uint32_t code[LOADS][UW], scale[LOADS][2];
-  static constexpr int of_key(int i) { return i; }
-  static constexpr int of_value(int i) { return EITHER ? i : KI + i; }
+  static constexpr int N = D / 8 / W, PIECES = 2 * N;
+  static_assert(D % (8 * W) == 0, "waves share the pieces evenly");
+  // Keys: a lane takes 8 N elements of one token, KW words, TL neighbouring lanes those of
+  // neighbouring tokens, so that 16 lanes' stores fall into different banks.
+  static constexpr int KW = FP4 ? N : 2 * N, PARTS = D / 8 / N, TL = D == 64 ? 1 : D == 128 ? 8 : 16;
+  // Values: a lane takes 2 N elements of a quad; those of NVFP4 heads below 256 are half of
+  // what it loads, VW words.
+  static constexpr int QL = D / 2 / N, VW = FP4 ? (D == 64 ? 2 : D == 128 ? 4 : 8) : 2 * N;
+  uint32_t kq[KW], ks, vq[VW], vs[2];
 
-  __device__ __forceinline__ static uint32_t load(Rsrc r, uint32_t at, uint32_t base, int bytes) {
+  template <int BYTES>
+  __device__ __forceinline__ static uint32_t load(Rsrc r, uint32_t at, uint32_t base) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    if (bytes == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, base, 0);
+    if constexpr (BYTES == 1) return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, at, base, 0);
+    if constexpr (BYTES == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, base, 0);
     return __builtin_amdgcn_raw_buffer_load_b32(r, at, base, 0);
 #else
     return 0;
 #endif
   }
-  __device__ __forceinline__ static void load_16(Rsrc r, uint32_t* d, uint32_t at, uint32_t base) {
+  template <int WORDS>
+  __device__ __forceinline__ static void load_words(Rsrc r, uint32_t* d, uint32_t at, uint32_t base) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    const auto x = __builtin_amdgcn_raw_buffer_load_b128(r, at, base, 0);
-    d[0] = x[0]; d[1] = x[1]; d[2] = x[2]; d[3] = x[3];
+    if constexpr (WORDS == 1) {
+      d[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, base, 0);
+    } else if constexpr (WORDS == 2) {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, at, base, 0);
+      d[0] = x[0]; d[1] = x[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 4) {
+        const auto x = __builtin_amdgcn_raw_buffer_load_b128(r, at + 4 * i, base, 0);
+        d[i] = x[0]; d[i + 1] = x[1]; d[i + 2] = x[2]; d[i + 3] = x[3];
+      }
+    }
 #endif
   }
-  // Load i of a wave among all loads of keys (of values); one from PT (VL) on is none.
-  __device__ __forceinline__ static int key_load(int i, int wave) { return i * W + wave; }
-  __device__ __forceinline__ static int value_load(int i, int wave) { return i * W + (wave + VOFF) % W; }
-  // Of key load wi: its first token, this lane's token behind it and part.
-  __device__ __forceinline__ static int key_block(int wi) { return wi / (PT / PB) * (64 / PB); }
-  __device__ __forceinline__ static int key_token(int lane) { return lane % TL + TL * (lane / TL / PB); }
-  __device__ __forceinline__ static int key_part(int wi, int lane) { return wi % (PT / PB) * PB + lane / TL % PB; }
+  // This lane's token (row of the tile) and part of it.
+  __device__ __forceinline__ static int key_row(int wave, int lane) {
+    return TL == 1 ? wave * (64 / PARTS) + lane / PARTS : wave * (64 / PARTS) + lane % TL + TL * (lane / (TL * PARTS));
+  }
+  __device__ __forceinline__ static int key_part(int lane) { return TL == 1 ? lane % PARTS : lane / TL % PARTS; }
+  // This lane's quad and place in it.
+  __device__ __forceinline__ static int quad_of(int wave, int lane) { return wave * (64 / QL) + lane / QL; }
 
   __device__ __forceinline__ void fetch_keys(const Place& from, const KvLayout lay, int wave, int lane) {
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const int wi = key_load(i, wave);
-      if (wi >= PT) break;
-      const int tb = key_block(wi);
-      const Unit32 u = from.of(tb);
-      const Rsrc block = u.rsrc();
-      const int tok = u.o + (tb & 31) + key_token(lane), part = key_part(wi, lane);
-      load_16(block, code[of_key(i)], tok * ROW + part * 16, 0);
-      if constexpr (FP4) scale[of_key(i)][0] = load(block, tok * (D / 16) + part * 2, lay.ks, 2);
-      else scale[of_key(i)][0] = load(block, 2 * (tok * (D / 32) + part / 2), lay.ks, 2);
+    const Unit32 u = from.of(wave * (64 / PARTS));
+    const Rsrc block = u.rsrc();
+    const int tok = u.o + (key_row(wave, lane) & 31), part = key_part(lane);
+    load_words<KW>(block, kq, tok * ROW + part * (4 * KW), 0);
+    if constexpr (FP4) {  // scales of 16 elements: of 8 N / 16 blocks, or the one that holds the lane's
+      constexpr int B = N >= 8 ? 4 : 1;
+      ks = load<B>(block, tok * (D / 16) + part * 8 * N / 16, lay.ks);
+    } else {
+      constexpr int B = N >= 8 ? 4 : 2;
+      ks = load<B>(block, 2 * (tok * (D / 32) + part * 8 * N / 32), lay.ks);
     }
   }
   __device__ __forceinline__ void fetch_values(const Place& from, const KvLayout lay, int P, int wave, int lane) {
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      const int wi = value_load(i, wave);
-      if (wi >= VL) break;
-      const int first = wi * 64 / UQ;  // quad
-      const Unit32 u = from.of(4 * first);
-      const Rsrc block = u.rsrc();
-      const int quad = first + lane / UQ, part = lane % UQ, tok = u.o + (quad & 7) * 4;
-      const uint32_t at = tok * ROW + part * (UW * 4);
-      load_16(block, code[of_value(i)], at, lay.vq);
-      if constexpr (UW == 8) load_16(block, code[of_value(i)] + 4, at + 16, lay.vq);
-      const int e = part * (D / UQ);  // first element
-      if constexpr (FP4) {
-        scale[of_value(i)][0] = load(block, e / 16 * P + tok, lay.vs, 4);
-      } else {
-        const uint32_t s = 2 * (e / 32 * P + tok);
-        scale[of_value(i)][0] = load(block, s, lay.vs, 4);
-        scale[of_value(i)][1] = load(block, s + 4, lay.vs, 4);
-      }
+    const Unit32 u = from.of(4 * (wave * (64 / QL)));
+    const Rsrc block = u.rsrc();
+    const int tok = u.o + (quad_of(wave, lane) & 7) * 4, ql = lane % QL, e = ql * 2 * N;  // first element
+    if constexpr (FP4) {
+      // [16][4 tokens][D/32 bytes] of a quad
+      constexpr int LANES = QL / 16;  // lanes of a group
+      load_words<VW>(block, vq, tok * ROW + ql / LANES * (4 * VW), lay.vq);
+      vs[0] = load<4>(block, e / 16 * P + tok, lay.vs);
+    } else {
+      load_words<VW>(block, vq, tok * ROW + ql * (4 * VW), lay.vq);
+      const uint32_t s = 2 * (e / 32 * P + tok);
+      vs[0] = load<4>(block, s, lay.vs);
+      vs[1] = load<4>(block, s + 4, lay.vs);
     }
   }
 
-  __device__ __forceinline__ void put_key(int i, int w, uint8_t* kt, int wave, int lane) const {
-    const int wi = key_load(i, wave);
-    if (wi >= PT) return;
-    const int row = key_block(wi) + key_token(lane), part = key_part(wi, lane);
+  __device__ __forceinline__ void put_key(int n, uint8_t* kt, int wave, int lane) const {
+    const int row = key_row(wave, lane);
     uint32_t c[4];
     if constexpr (FP4) {
-      const v2f s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(scale[of_key(i)][0], 1.0f, false);
-      const float f = w < 2 ? s[0] : s[1];
+      const v2f s = n < 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(ks, 1.0f, false)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(ks, 1.0f, true);
+      const float f = n / 2 & 1 ? s[1] : s[0];  // (pieces 2b, 2b + 1 are block b)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const v2f v = fp4_pair(code[of_key(i)][w], k);
+        const v2f v = fp4_pair(kq[n], k);
         c[k] = bf16_pair(v[0] * f, v[1] * f);
       }
     } else {
-      const float f = half_value(scale[of_key(i)][0], 0), minus = -128.0f * f;
+      const float f = half_value(ks, n / 4), minus = -128.0f * f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t b = code[of_key(i)][2 * w + (k >> 1)] ^ 0x80808080u;
+        const uint32_t b = kq[2 * n + (k >> 1)] ^ 0x80808080u;
         c[k] = bf16_pair(q8_value(b, 2 * (k & 1), f, minus), q8_value(b, 2 * (k & 1) + 1, f, minus));
       }
     }
-    *reinterpret_cast<uint4*>(kt + row * (2 * D) + swz<D>(row, part * KC + w) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<uint4*>(kt + row * (2 * D) + swz<D>(row, key_part(lane) * N + n) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
-  // left: the tile's tokens that some row sees; values from there on count as 0, whatever
-  // the cache holds.
-  __device__ __forceinline__ void cut_values(int left, int wave, int lane) {
+  // Whether a value of the lane's that counts is NaN (its scale says so; an infinite fp16
+  // scale counts too).
+  __device__ __forceinline__ bool wild() const {
+    bool any = false;
+    if constexpr (FP4) {
 #pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      const int wi = value_load(i, wave), n = min(max(left - 4 * (wi * 64 / UQ + lane / UQ), 0), 4);
-      if (wi >= VL) break;
+      for (int i = 0; i < 4; ++i) any |= ((vs[0] >> (8 * i)) & 0x7fu) == 0x7fu;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) any |= (vs[i] & 0x7c00u) == 0x7c00u || (vs[i] & 0x7c000000u) == 0x7c000000u;
+    }
+    return any;
+  }
+  // What was loaded, moved to where the pieces look for it; left: the tile's tokens that
+  // some row sees; values from there on count as 0, whatever the cache holds.
+  __device__ __forceinline__ void arrange_values(int left, int wave, int lane) {
+    if constexpr (FP4 && D < 256) {  // the lane's half of its group
+      const int by = (lane & 1) * (D == 64 ? 8 : 16);
+#pragma unroll
+      for (int i = 0; i < VW; ++i) vq[i] >>= by;
+    }
+    if (left < kBN) {
+      const int n = min(max(left - 4 * quad_of(wave, lane), 0), 4);
       if constexpr (FP4) {
-        scale[of_value(i)][0] = n >= 4 ? scale[of_value(i)][0] : scale[of_value(i)][0] & ((1u << (8 * n)) - 1u);
+        vs[0] = n >= 4 ? vs[0] : vs[0] & ((1u << (8 * n)) - 1u);
       } else {
-        scale[of_value(i)][0] &= n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
-        scale[of_value(i)][1] &= n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
+        vs[0] &= n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
+        vs[1] &= n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
       }
     }
   }
-  __device__ __forceinline__ void put_value(int i, int e, uint8_t* vt, int wave, int lane) const {
-    const int wi = value_load(i, wave);
-    if (wi >= VL) return;
-    const int quad = wi * 64 / UQ + lane / UQ, part = lane % UQ;
+  __device__ __forceinline__ void put_value(int n, uint8_t* vt, int wave, int lane) const {
+    const int quad = quad_of(wave, lane);
     uint32_t c[4];
     if constexpr (FP4) {
-      const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(scale[of_value(i)][0], 1.0f, false);
-      const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(scale[of_value(i)][0], 1.0f, true);
+      const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs[0], 1.0f, false);
+      const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs[0], 1.0f, true);
       v2f p[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        // byte e of token t: [4][4 bytes], [4][8 bytes], or twice [4][2 bytes]
-        if constexpr (D == 128) p[t] = fp4_pair(code[of_value(i)][t], e);
-        else if constexpr (D == 256) p[t] = fp4_pair(code[of_value(i)][2 * t + e / 4], e % 4);
-        else p[t] = fp4_pair(code[of_value(i)][e / 2 * 2 + t / 2], 2 * (t & 1) + (e & 1));
+        // byte n of token t's
+        if constexpr (D == 64) p[t] = fp4_pair(vq[t / 2], 2 * (t & 1));
+        else if constexpr (D == 128) p[t] = fp4_pair(vq[t], n);
+        else p[t] = fp4_pair(vq[2 * t + n / 4], n % 4);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -225,17 +234,17 @@ struct Codes {
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t b = code[of_value(i)][2 * e + (k >> 1)] ^ 0x80808080u;
-        const float s0 = half_value(scale[of_value(i)][k & 1], 0), s1 = half_value(scale[of_value(i)][k & 1], 1);
+        const uint32_t b = vq[2 * n + (k >> 1)] ^ 0x80808080u;
+        const float s0 = half_value(vs[k & 1], 0), s1 = half_value(vs[k & 1], 1);
         c[k] = bf16_pair(q8_value(b, 2 * (k & 1), s0, -128.0f * s0), q8_value(b, 2 * (k & 1) + 1, s1, -128.0f * s1));
       }
     }
-    *reinterpret_cast<uint4*>(vt + quad * (8 * D) + vswz<D>(quad, part * VC + e) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<uint4*>(vt + quad * (8 * D) + vswz<D>(quad, lane % QL * N + n) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
-  // Piece n of this wave's: the keys' first.
-  __device__ __forceinline__ void put(int n, uint8_t* kt, uint8_t* vt, int wave, int lane) const {
-    if (n < KI * KC) put_key(n / KC, n % KC, kt, wave, lane);
-    else put_value((n - KI * KC) / VC, (n - KI * KC) % VC, vt, wave, lane);
+  // Piece p: the keys' first.
+  __device__ __forceinline__ void put(int p, uint8_t* kt, uint8_t* vt, int wave, int lane) const {
+    if (p < N) put_key(p, kt, wave, lane);
+    else put_value(p - N, vt, wave, lane);
   }
 };
 
@@ -318,10 +327,9 @@ struct ChunkRows : TileRows<D> {
       }
     }
   }
-  // A new maximum for the rows whose weights would leave 2^kGrow (the others' answers do
-  // not depend on them, bit for bit).
-  __device__ __forceinline__ void raise(const v16f (&x)[2], float c) {
-    const float mx = this->top(x, c);
+  // A new maximum for the rows whose weights would leave 2^kGrow with the largest scaled
+  // score mx (the others' answers do not depend on them, bit for bit).
+  __device__ __forceinline__ void raise(float mx) {
     if (__any(mx > m + kGrow)) {
       const float mn = mx > m + kGrow ? mx : m, al = __builtin_amdgcn_exp2f(m - mn);
 #pragma unroll
@@ -368,7 +376,7 @@ struct ChunkRows : TileRows<D> {
   }
 };
 
-// Whether a tile of values holds an infinity or a NaN.
+// Whether a tile of values in LDS holds an infinity or a NaN.
 template <int D>
 __device__ __forceinline__ bool wild(const uint8_t* vt, int lane) {
   bool any = false;
@@ -390,9 +398,10 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
   constexpr int KS = D / 16, NJ = D / 32, SIZE = 32 * W, TILE = kBN * D * 2;
   constexpr bool DECODED = FMT != MOE_FMT_BF16;
   __shared__ __align__(16) uint8_t k_even[TILE], k_odd[TILE], v_even[TILE], v_odd[TILE];
+  __shared__ int wild_even[W], wild_odd[W];  // what each wave found among the values it decoded
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id(), n = lane & 31;
-  Item it = find_item(a.s, a.T, a.G, SIZE, a.n_kv, a.room, a.S, (int)blockIdx.x);
+  Item it = find_item<true>(a.s, a.T, a.G, SIZE, a.n_kv, a.room, a.S, (int)blockIdx.x, a.rounds);
   if (it.b < 0) return;
   // (a sequence's last rows, which see the most, first)
   it.tile = (int)((uint32_t)(it.inside * a.G + SIZE - 1) / (uint32_t)SIZE) - 1 - it.tile;
@@ -429,18 +438,25 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
   const int wave_row = (int)((uint32_t)min((it.tile * W + wave) * 32 + 31, last_slot) / (uint32_t)a.G);
   const int64_t hi_wave = (it.tile * W + wave) * 32 <= last_slot ? (int64_t)len - rows + wave_row : -1;
 
-  // Pages, by scalar loads; a unit past the table's end has none, one past the last token
-  // that is looked at is not looked for.  Rows that see a token of a page that is not there
-  // have no answer.
+  // Pages of 64 units at a time, one a lane: -1 where the table or the pool has none, and
+  // from the last token that is looked at on.  Rows that see a token of a page that is not
+  // there have no answer.
   const int* const table = a.s.page_table + (int64_t)it.b * a.s.max_pages;
+  int batch = u_begin, pages;
+  const auto next_pages = [&] {
+    const int64_t u = (int64_t)batch + lane, i = (u * 32) >> a.s.log2P;
+    pages = -1;
+    if (u < u_end && i < a.s.max_pages) pages = table[i];
+    if ((unsigned)pages >= (unsigned)a.s.n_pages) pages = -1;
+  };
+  next_pages();
   const auto unit = [&](int u) {
-    const int i = (int)(((int64_t)u * 32) >> a.s.log2P);
-    int p = -1;
-    if (u < u_end) {
-      p = *(const int __attribute__((address_space(4)))*)(uintptr_t)(table + min(i, a.s.max_pages - 1));
-      if (i >= a.s.max_pages || (unsigned)p >= (unsigned)a.s.n_pages) p = -1;
-      if (p < 0 && w.limit >= (int64_t)u * 32) w.l = __uint_as_float(0x7fc00000u);
+    if (u - batch >= 64) {
+      batch += 64;
+      next_pages();
     }
+    const int p = __builtin_amdgcn_readlane(pages, u - batch);
+    if (p < 0 && u < u_end && w.limit >= (int64_t)u * 32) w.l = __uint_as_float(0x7fc00000u);
     return Unit32{heads + (size_t)max(p, 0) * page_bytes, p < 0 ? 0 : (int)lay.head, (u * 32) & (P - 1)};
   };
   const auto place = [&](int t) { return Place{unit(2 * t), unit(2 * t + 1)}; };
@@ -476,6 +492,21 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
     C c_even, c_two;
     C& c_odd = TWO ? c_two : c_even;
     Place next;  // of the keys fetched last: the values' one turn later
+    // In a tile that not every row sees, infinities and NaN are looked for.
+    const auto look = [&](const C& c, int t, int* found) {
+      if constexpr (DECODED) {
+        if (t < full) return;
+        const bool any = __any(c.wild());
+        if (lane == 0) found[wave] = any;
+      }
+    };
+    const auto is_wild = [&](const uint8_t* vt, const int* found) {
+      if constexpr (!DECODED) return wild<D>(vt, lane);
+      int any = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) any |= found[i];
+      return any != 0;
+    };
     // keys of tile t, values of tile t - 1
     const auto fetch = [&](C& c, int t, uint8_t* kt, uint8_t* vt) {
       const Place before = next;
@@ -497,9 +528,10 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
       c0.fetch_keys(p0, lay, wave, lane);
       c0.fetch_values(p0, lay, P, wave, lane);
       c_odd.fetch_keys(next, lay, wave, lane);
-      if (left_of(first) < kBN) c0.cut_values(left_of(first), wave, lane);
+      c0.arrange_values(left_of(first), wave, lane);
+      look(c0, first, wild_even);
       put_all(c0, k_even, v_even);
-      each<0, C::KI * C::KC>([&](auto p) { c_odd.put(p(), k_odd, v_odd, wave, lane); });
+      each<0, C::N>([&](auto p) { c_odd.put(p(), k_odd, v_odd, wave, lane); });
       fetch(c_even, first + 2, nullptr, nullptr);
       if constexpr (TWO) fetch(c_odd, first + 3, nullptr, nullptr);
     } else {
@@ -512,14 +544,16 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
     v16f x[2];
     w.scores(k_even, x);
     if (first >= full) w.mask(x, (int64_t)first * kBN);
+    w.raise(w.top(x, a.scale_log2));
 
-    // Turn t: x holds tile t's scores, k1 the keys of t + 1, v0 the values of t; the keys
+    // Turn t: x holds tile t's scores, which the maxima cover, k1 the keys of t + 1, v0 the values of t; the keys
     // of t + 2 go to k0, the values of t + 1 to v1.
-    const auto begin = [&](int t, C& c, uint8_t* k0, uint8_t* v0, uint8_t* v1) {
+    const auto begin = [&](int t, C& c, uint8_t* k0, uint8_t* v0, uint8_t* v1, int* found) {
       if constexpr (!DECODED) wait_loads<0>();
       __syncthreads();  // what this turn reads is there, what it overwrites has been read
       if constexpr (DECODED) {
-        if (left_of(t + 1) < kBN) c.cut_values(left_of(t + 1), wave, lane);
+        c.arrange_values(left_of(t + 1), wave, lane);
+        look(c, t + 1, found);
       } else {
         clear_behind(t, v0);
         fetch(c, t + 2, k0, v1);
@@ -530,54 +564,62 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
       x[1] = y[1];
       if constexpr (DECODED) fetch(c, t + (TWO ? 4 : 3), nullptr, nullptr);
     };
-    const auto step = [&](int t, C& c, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1) {
-      begin(t, c, k0, v0, v1);
+    const auto step = [&](int t, C& c, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1, int* f1) {
+      begin(t, c, k0, v0, v1, f1);
       v16f y[2];
-      w.raise(x, a.scale_log2);
+      float most = -__builtin_inff();
       w.template stream<true>([&](int h, int s) { return w.key(k1, h, s); }, [&](int s, int j) { return w.value(v0, s, j); },
                               a.scale_log2, x, y, [&](auto I) {
         constexpr int N = 2 * KS + 4 * NJ, i = I();
         each<C::PIECES * i / N, C::PIECES * (i + 1) / N>([&](auto p) { c.put(p(), k0, v1, wave, lane); });
+        // the next scores' maximum, beside the second product
+        constexpr int F = 2 * KS + 1, L = N - F;
+        if constexpr (i >= F)
+#pragma unroll
+          for (int v = 32 * (i - F) / L; v < 32 * (i - F + 1) / L; ++v) most = fmaxf(most, y[v >> 4][v & 15]);
       });
+      w.raise(w.over_halves(most) * a.scale_log2);
       finish(t, c, y);
     };
     // Tiles that not every row sees, and the last ones: a wave leaves out those none of its
     // rows does.
-    const auto edge_step = [&](int t, C& c, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1) {
-      begin(t, c, k0, v0, v1);
-      put_all(c, k0, v1);
+    const auto edge_step = [&](int t, C& c, uint8_t* k0, uint8_t* k1, uint8_t* v0, uint8_t* v1, int* f0, int* f1) {
+      begin(t, c, k0, v0, v1, f1);
       const int64_t t0 = (int64_t)t * kBN;
       v16f y[2];
+      put_all(c, k0, v1);
       if (t0 <= hi_wave) {
         uint32_t keep = ~0u;
-        if (t >= full && wild<D>(v0, lane)) {
+        if (t >= full && is_wild(v0, f0)) {
           keep = 0u;  // (left for later)
           some_wild = true;
         }
-        w.raise(x, a.scale_log2);
         w.template stream<false>([&](int, int) { return v4u{0, 0, 0, 0}; },
                                  [&](int s, int j) { return w.value(v0, s, j) & keep; }, a.scale_log2, x, y, [](auto) {});
       }
-      if (t + 1 < end) {
+      if (t + 1 < end && t0 + kBN <= hi_wave) {
         w.scores(k1, y);
         if (t + 1 >= full) w.mask(y, t0 + kBN);
+        w.raise(w.top(y, a.scale_log2));
       }
       finish(t, c, y);
     };
     int t = first;
 #pragma unroll 1
     for (; t + 2 < full; t += 2) {
-      step(t, c_even, k_even, k_odd, v_even, v_odd);
-      step(t + 1, c_odd, k_odd, k_even, v_odd, v_even);
+      step(t, c_even, k_even, k_odd, v_even, v_odd, wild_odd);
+      step(t + 1, c_odd, k_odd, k_even, v_odd, v_even, wild_even);
     }
 #pragma unroll 1
     for (; t < end; t += 2) {
-      edge_step(t, c_even, k_even, k_odd, v_even, v_odd);
-      if (t + 1 < end) edge_step(t + 1, c_odd, k_odd, k_even, v_odd, v_even);
+      edge_step(t, c_even, k_even, k_odd, v_even, v_odd, wild_even, wild_odd);
+      if (t + 1 < end) edge_step(t + 1, c_odd, k_odd, k_even, v_odd, v_even, wild_odd, wild_even);
     }
   }
   // Tiles with infinities or NaN among values that some row may not see, once more.
   if (__syncthreads_or(some_wild)) {
+    batch = 2 * max(first, full);
+    next_pages();
 #pragma unroll 1
     for (int t = max(first, full); t < end; ++t) {
       const Place from = place(t);
@@ -586,7 +628,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
         C c;
         c.fetch_keys(from, lay, wave, lane);
         c.fetch_values(from, lay, P, wave, lane);
-        c.cut_values(left_of(t), wave, lane);
+        c.arrange_values(left_of(t), wave, lane);
         put_all(c, k_even, v_even);
         __syncthreads();
       } else {
@@ -634,7 +676,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
 // Launch shape: splits there is room for in the workspace (1: no split), and for each
 // key/value head chunks and items (the grid).
 struct Shape {
-  int S, room, likely;
+  int S, room, likely, rounds;
   int64_t items;
 };
 constexpr int chunk_waves(int D) { return D <= 128 ? 8 : 4; }
@@ -644,14 +686,18 @@ Shape shape_of(int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) 
   const int64_t per_seq = (T + n_seq - 1) / n_seq;
   const int64_t tiles = T * G / size + n_seq;  // at most: one part tile a sequence
   const int64_t base = (int64_t)n_seq * n_kv * ((per_seq * G + size - 1) / size);
-  const int target = 256;
   Shape r;
   int64_t S = ((int64_t)256 << 20) / (T * n_q * D * 4);
   S = std::min({S, (int64_t)kMaxSplit, (units + kWaves - 1) / kWaves});
-  r.S = T * n_q > kChunkPairs || S < 2 || (n_seq == 1 && base >= 2 * target) || units <= 31 ? 1 : (int)S;
-  r.likely = (int)std::min({(int64_t)std::max(units / kWhole, (int64_t)1), std::max(target / base, (int64_t)1), (int64_t)r.S});
-  r.room = (int)std::max((int64_t)1, std::min((int64_t)target / n_kv, tiles * r.S));
-  r.items = tiles + (r.S > 1 ? r.room + 1 : 0);
+  r.room = std::max(256 / n_kv, 1);
+  // (of one sequence it is known whether fit_chunk will split it)
+  const int64_t once = std::max((tiles * units + r.room - 1) / r.room, (int64_t)kWaves) + 2 * kStart;
+  const bool whole = n_seq == 1 && tiles <= r.room && units + kStart <= once;
+  r.S = T * n_q > kChunkPairs || S < 2 || (n_seq == 1 && base >= 512) || units <= 8 || whole ? 1 : (int)S;
+  r.likely = (int)std::min({std::max(units / kWaves, (int64_t)1), std::max(256 / base, (int64_t)1), (int64_t)r.S});
+  // (workgroups without an item take their place on a CU too: no more than may be needed)
+  r.rounds = tiles <= r.room ? 1 : 2;
+  r.items = r.S == 1 ? tiles : n_seq > 64 ? tiles + r.room + 1 : std::max(tiles, (int64_t)r.rounds * r.room);
   return r;
 }
 
@@ -685,7 +731,7 @@ hipError_t launch_attn_chunk(const moe_kv_cache* c, const moe_seq_batch* s, int 
   const SplitArgs a{(const uint8_t*)c->pool, q, out, (float*)ws, (float2*)ml,
                     (int*)(ml + align_up(n * sizeof(float2))), q_stride, out_stride, T,
                     SeqView{s->row_start, s->kv_len, s->page_table, s->n_seq, s->max_pages, c->n_pages, l2},
-                    n_q, c->n_kv, n_q / c->n_kv, sp.S, sp.room, sp.likely,
+                    n_q, c->n_kv, n_q / c->n_kv, sp.S, sp.room, sp.likely, sp.rounds,
                     scale * 1.4426950408889634f * (fp4 ? c->k_scale : 1.0f), fp4 ? c->v_scale : 1.0f};
   const unsigned grid = (unsigned)(sp.items * c->n_kv);
   switch (c->fmt) {

@@ -770,7 +770,7 @@ hipError_t launch_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int
   SplitArgs a{(const uint8_t*)c->pool, q, out, (float*)ws, (float2*)ml,
                (int*)(ml + align_up(n * sizeof(float2))), q_stride, out_stride, T,
                SeqView{s->row_start, s->kv_len, s->page_table, s->n_seq, s->max_pages, c->n_pages, l2},
-               n_q, c->n_kv, n_q / c->n_kv, sp.S, sp.room, sp.likely,
+               n_q, c->n_kv, n_q / c->n_kv, sp.S, sp.room, sp.likely, 1,
                scale * 1.4426950408889634f * (fp4 ? c->k_scale : 1.0f), fp4 ? c->v_scale : 1.0f};
   const unsigned grid = (unsigned)(sp.items * c->n_kv);
   switch (c->fmt) {

@@ -19,7 +19,7 @@ struct SplitArgs {
   int* part_n;     // [T * n_q]: splits (1: the output is there already)
   int64_t q_stride, out_stride, T;
   SeqView s;
-  int n_q, n_kv, G, S, room, likely;
+  int n_q, n_kv, G, S, room, likely, rounds;
   float scale_log2, v_ts;
 };
 
@@ -60,8 +60,45 @@ struct LaneSeq {
 // holds), and kWhole units or more unless the 256 CUs need shorter ones (8 slots of
 // 1000 to 60000 tokens: 33 us; as many chunks of each sequence as of any other, 37).
 constexpr int kWhole = 4 * kWaves;
+
+// The same for workgroups of which one fits a CU: as long as there are no more than 64
+// sequences, the shortest chunks whose items fit the room (workgroups that run at once, of
+// one key/value head) once, or up to `rounds` times, whichever is done first: a round
+// lasts as long as its longest item, a chunk and what a workgroup needs before and behind
+// it, about kStart units; joining costs as much again.
+constexpr int kStart = 8;
+__device__ __forceinline__ int fit_chunk(const LaneSeq& q, float work, int most, int room, int rounds,
+                                         int least) {
+  const auto items = [&](int c) {
+    return wave_sum((float)q.tiles * (float)(q.units ? (int)((uint32_t)(q.units - 1) / (uint32_t)c) + 1 : 1));
+  };
+  const int whole = max((most + 1) & ~1, 2);
+  const float tiles = items(whole);
+  int chunk = whole;
+  float cost = ceilf(tiles / (float)room) * (float)(most + kStart);
+  for (int k = 1; k <= rounds; ++k) {
+    const float cap = (float)(k * room);
+    if (tiles > cap) continue;
+    int lo = max((int)fminf(work / cap, 0x1p30f) & ~1, max(least, kWaves)), hi = whole;  // (too many items below lo)
+    while (hi - lo > max(lo / 16, 2)) {
+      const int c = (lo + (hi - lo) / 2) & ~1;
+      if (items(c) <= cap) hi = c;
+      else lo = c;
+    }
+    if (lo < hi && items(lo) <= cap) hi = lo;
+    const float needs = (float)k * (float)(hi + kStart) + (float)kStart;
+    if (needs < cost) {
+      cost = needs;
+      chunk = hi;
+    }
+  }
+  return chunk;
+}
+
+// FIT: see fit_chunk.
+template <bool FIT = false>
 __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, int size, int n_kv,
-                                          int room, int S, int id) {
+                                          int room, int S, int id, int rounds = 1) {
   Item r;
   r.b = -1;
   r.chunk = INT32_MAX;
@@ -76,11 +113,15 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
     }
     work = wave_sum(work);
     most = wave_max(most);
-    // (a sequence has less than 2^27 units: held to 2^30, it stays an int)
-    int chunk = (int)fminf(ceilf(work / (float)room), 0x1p30f);
-    if (chunk < kWhole) chunk = max(chunk, min((int)ceilf(work * n_kv / 256.0f), kWhole));
-    chunk = (max(chunk, (most + S - 1) / S) + kWaves - 1) / kWaves * kWaves;
-    r.chunk = max(__builtin_amdgcn_readfirstlane(chunk), kWaves);
+    if (FIT && s.n_seq <= 64) {
+      r.chunk = __builtin_amdgcn_readfirstlane(fit_chunk(first, work, most, room, rounds, ((most + S - 1) / S + 1) & ~1));
+    } else {
+      // (a sequence has less than 2^27 units: held to 2^30, it stays an int)
+      int chunk = (int)fminf(ceilf(work / (float)room), 0x1p30f);
+      if (chunk < kWhole) chunk = max(chunk, min((int)ceilf(work * n_kv / 256.0f), kWhole));
+      chunk = (max(chunk, (most + S - 1) / S) + kWaves - 1) / kWaves * kWaves;
+      r.chunk = max(__builtin_amdgcn_readfirstlane(chunk), kWaves);
+    }
   }
   int before = 0;
   for (int i0 = 0; i0 < s.n_seq; i0 += 64) {

@@ -93,9 +93,13 @@ struct TileRows {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[t][i]);
+    return over_halves(mx) * c;
+  }
+  // The larger of a row's two lanes.
+  __device__ __forceinline__ static float over_halves(float mx) {
     const uint32_t u = __float_as_uint(mx);
     const auto w = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])) * c;
+    return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
   }
   // The lane's sum, over both halves of the wave.
   __device__ __forceinline__ void finish() {
@@ -137,13 +141,13 @@ struct TileRows {
     each<I0, N1 + N2>([&](auto I) {
       constexpr int i = I();
       if (i + kAhead < N1 + N2) f[(i + kAhead) % kRing] = fragment(i + kAhead);
-      if (i < N1) {
+      if constexpr (i < N1) {
         v16f zero;
 #pragma unroll
         for (int k = 0; k < 16; ++k) zero[k] = 0.0f;
         y[i / KS] = mma(f[i % kRing], qf[i % KS], i % KS ? y[i / KS] : zero);
       } else {
-        const int s = (i - N1) / NJ, j = (i - N1) % NJ;
+        constexpr int s = (i - N1) / NJ, j = (i - N1) % NJ;
         o[j] = mma(f[i % kRing], p[s], o[j]);
       }
 #pragma unroll
