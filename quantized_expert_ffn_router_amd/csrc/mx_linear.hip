@@ -279,7 +279,10 @@ void launch_few(const LinearArgs& a, hipStream_t stream) {
 
 // One workgroup: WT x WN waves, each FT x FN squares of 32 rows by 32 outputs.  Per
 // step of 128 elements the rows' and the weights' codes and scales go from global
-// memory into one of three LDS buffers, two steps ahead.
+// memory into one of three LDS buffers, up to three steps ahead.  The waves meet in the
+// midst of a step, between its two halves: the operands of the half behind the barrier
+// are in registers by then, those of the next step's first half are read beside it, so
+// that the matrix units do not wait for LDS.
 template <int FMT, int WT, int WN, int FT, int FN>
 struct Gemm {
   static constexpr int WAVES = WT * WN, BT = WT * FT * 32, BN = WN * FN * 32;
@@ -290,7 +293,8 @@ struct Gemm {
   static_assert(NA % WAVES == 0 && NB % WAVES == 0 && NS <= WAVES, "waves share the loads evenly");
 
   const LinearArgs& a;
-  Rsrc rows, weights, scales;  // scales: of rows or weights, as this wave loads them
+  const uint8_t *rows, *weights, *scales;  // scales: of rows or weights, as this wave loads them
+  int64_t row_bytes, weight_bytes, scale_bytes;
   int wave, lane, r, h, wt, wn, scale_step;
   uint32_t at[PER];
 
@@ -301,8 +305,10 @@ struct Gemm {
     wn = wave % WN;
     const int64_t pitch = mx_bytes<FMT>(a.K), n = min(a.T - t0, (int64_t)BT);
     const int64_t m = min(a.tiles - tile0, BN / 16);
-    rows = buffer_of(a.codes + t0 * pitch, n * pitch);
-    weights = buffer_of(a.w + (int64_t)tile0 * a.steps * 1024, m * a.steps * 1024);
+    rows = a.codes + t0 * pitch;
+    row_bytes = n * pitch;
+    weights = a.w + (int64_t)tile0 * a.steps * 1024;
+    weight_bytes = m * a.steps * 1024;
 #pragma unroll
     for (int i = 0; i < PER - 1; ++i) {
       const int u = i * WAVES + wave;
@@ -319,20 +325,26 @@ struct Gemm {
     }
     const int u = wave % NS, width = a.K / kMxBlock;  // (waves past the last load repeat one)
     const bool of_rows = u < BT / 64;
-    scales = of_rows ? buffer_of(a.scales + t0 * width, n * width)
-                     : buffer_of(a.w_scales + (int64_t)tile0 * a.steps * 64, m * a.steps * 64);
+    scales = of_rows ? a.scales + t0 * width : a.w_scales + (int64_t)tile0 * a.steps * 64;
+    scale_bytes = of_rows ? n * width : m * a.steps * 64;
     scale_step = of_rows ? 4 : 64;
     at[PER - 1] = of_rows ? (uint32_t)((u * 64 + lane) * width)
                           : (uint32_t)(((u - BT / 64) * 4 + (lane >> 4)) * a.steps * 64 + (lane & 15) * 4);
   }
+  // (Of a step behind the last one nothing is read: its loads are there so that as many are
+  // always on their way, without a branch, past which the matrix instructions would move.)
   __device__ __forceinline__ void load(uint8_t* lds, int ks) const {
+    const bool in = ks < a.steps;
+    const Rsrc x = buffer_of(rows, in ? row_bytes : 0), w = buffer_of(weights, in ? weight_bytes : 0);
+    const Rsrc s = buffer_of(scales, in ? scale_bytes : 0);
+    const int k = in ? ks : 0;
 #pragma unroll
     for (int i = 0; i < PER - 1; ++i) {
       const int u = i * WAVES + wave;
-      if (i < NA / WAVES) load_lds<16>(rows, lds + OA + u * 1024, at[i], ks * CB);
-      else load_lds<16>(weights, lds + OB + (u - NA) * 1024, at[i], ks * 1024);
+      if (i < NA / WAVES) load_lds<16>(x, lds + OA + u * 1024, at[i], k * CB);
+      else load_lds<16>(w, lds + OB + (u - NA) * 1024, at[i], k * 1024);
     }
-    load_lds<4>(scales, lds + OS + (wave % NS) * 256, at[PER - 1], ks * scale_step);
+    load_lds<4>(s, lds + OS + (wave % NS) * 256, at[PER - 1], k * scale_step);
   }
   __device__ __forceinline__ v8i row_part(const uint8_t* lds, int f, int j) const {
     const int row = (wt * FT + f) * 32 + r;
@@ -357,31 +369,37 @@ struct Gemm {
     for (int i = 0; i < 8; ++i) v[i] = i < 4 ? (int)q[i] : 0;
     return v;
   }
-  template <int J>
-  __device__ __forceinline__ void half(const uint8_t* lds, const int (&rs)[FT], const int (&ws)[FN], v16f (&o)[FT][FN]) const {
+  // The operands of half a step, J: 64 elements of each row and output.
+  struct Parts {
     v8i p[FT], q[FN];
+  };
+  __device__ __forceinline__ void parts(const uint8_t* lds, int j, Parts& f) const {
 #pragma unroll
-    for (int f = 0; f < FN; ++f) q[f] = weight_part(lds, f, J);
+    for (int n = 0; n < FN; ++n) f.q[n] = weight_part(lds, n, j);
 #pragma unroll
-    for (int f = 0; f < FT; ++f) p[f] = row_part(lds, f, J);
+    for (int t = 0; t < FT; ++t) f.p[t] = row_part(lds, t, j);
+  }
+  // The step's scales: that of block 2 J + h of a row is byte 2 J of its word shifted by h
+  // bytes.
+  struct Scales {
+    int p[FT], q[FN];
+  };
+  __device__ __forceinline__ void scales_of(const uint8_t* lds, Scales& s) const {
 #pragma unroll
-    for (int f = 0; f < FT; ++f)
+    for (int t = 0; t < FT; ++t)
+      s.p[t] = (int)(*reinterpret_cast<const uint32_t*>(lds + OS + ((wt * FT + t) * 32 + r) * 4) >> (8 * h));
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      s.q[n] = (int)(*reinterpret_cast<const uint32_t*>(lds + OS + (BT + (wn * FN + n) * 32 + r) * 4) >> (8 * h));
+  }
+  template <int J>
+  __device__ __forceinline__ void product(const Parts& f, const Scales& s, v16f (&o)[FT][FN]) const {
+#pragma unroll
+    for (int t = 0; t < FT; ++t)
 #pragma unroll
       for (int n = 0; n < FN; ++n)
-        o[f][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[n], p[f], o[f][n], kFp4, kOperand<FMT>,
-                                                                  2 * J, ws[n], 2 * J, rs[f]);
-  }
-  // (the scale of block 2 J + h of a row: byte 2 J of its word shifted by h bytes)
-  __device__ __forceinline__ void step(const uint8_t* lds, v16f (&o)[FT][FN]) const {
-    int rs[FT], ws[FN];
-#pragma unroll
-    for (int f = 0; f < FT; ++f)
-      rs[f] = (int)(*reinterpret_cast<const uint32_t*>(lds + OS + ((wt * FT + f) * 32 + r) * 4) >> (8 * h));
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-      ws[f] = (int)(*reinterpret_cast<const uint32_t*>(lds + OS + (BT + (wn * FN + f) * 32 + r) * 4) >> (8 * h));
-    half<0>(lds, rs, ws, o);
-    half<1>(lds, rs, ws, o);
+        o[t][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.q[n], f.p[t], o[t][n], kFp4, kOperand<FMT>,
+                                                                  2 * J, s.q[n], 2 * J, s.p[t]);
   }
 };
 
@@ -414,23 +432,40 @@ __global__ __launch_bounds__(64 * WT * WN) void k_mx_gemm(LinearArgs a, int tile
       for (int f = 0; f < FT; ++f) o[f][n][i] = v;
     }
   const int steps = a.steps;
-  const auto turn = [&](int ks, uint8_t* now, uint8_t* then) {
-    if (ks + 1 < steps) wait_loads<G::PER>();
-    else wait_loads<0>();
+  typename G::Parts f0, f1;
+  typename G::Scales sc;
+  const auto meet = [&] {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (ks + 2 < steps) m.load(then, ks + 2);
-    m.step(now, o);
+  };
+  // Step ks: its first half's operands and its scales are there.
+  const auto turn = [&](int ks, uint8_t* now, uint8_t* next) {
+    m.parts(now, 1, f1);
+    m.template product<0>(f0, sc, o);
+    wait_loads<G::PER>();  // the next step's, of those that are on their way
+    meet();
+    m.load(now, ks + 3);
+    typename G::Scales after;  // (behind the last step: of nothing that is used)
+    m.scales_of(next, after);
+    m.parts(next, 0, f0);
+    m.template product<1>(f1, sc, o);
+    sc = after;
   };
   m.load(b0, 0);
-  if (steps > 1) m.load(b1, 1);
+  m.load(b1, 1);
+  m.load(b2, 2);
+  wait_loads<2 * G::PER>();
+  meet();
+  m.scales_of(b0, sc);
+  m.parts(b0, 0, f0);
 #pragma unroll 1
   for (int ks = 0; ks < steps; ks += 3) {
-    turn(ks, b0, b2);
-    if (ks + 1 < steps) turn(ks + 1, b1, b0);
-    if (ks + 2 < steps) turn(ks + 2, b2, b1);
+    turn(ks, b0, b1);
+    if (ks + 1 < steps) turn(ks + 1, b1, b2);
+    if (ks + 2 < steps) turn(ks + 2, b2, b0);
   }
+  wait_loads<0>();
 
   if (a.f32) {
 #pragma unroll
