@@ -1094,7 +1094,7 @@ moe_status moe_mx_linear_rows(const moe_mx_matrix* w, int32_t fmt, const uint16_
   if ((st = check_aligned(ws, "ws", W)) != MOE_OK) return st;
   const Named in[] = {{{x, x_stride, w->K, T}, "x"}, {dense(ws, (int64_t)need, 1), "ws"}};
   if ((st = check_all_apart(out, in, false, W)) != MOE_OK) return st;
-  if (moe::mx_linear_takes_rows(fmt, w->N, w->K, T))
+  if (moe::mx_linear_takes_rows(w->N, w->K, T))
     return hip_status(W, moe::launch_mx_linear(w, fmt, x, x_stride, nullptr, nullptr, T, y, y_stride, y_dtype, stream));
   const Named rows[] = {in[0]};
   if ((st = check_all_apart(in[1], rows, false, W)) != MOE_OK) return st;

@@ -43,47 +43,49 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t top) {
   constexpr int drop = FMT == MOE_FMT_MXFP4 ? 2 : 8;
   return top >= 0x7f80u ? 255u : (uint32_t)max((int)(top >> 7) - drop, 0);
 }
-// 2^(127 - s), what the block's values are multiplied by (0 for the NaN scale).
-__device__ __forceinline__ float mx_up(uint32_t s) {
-  return s == 255u ? 0.0f : __uint_as_float((254u - s) << 23);
-}
 // The largest magnitude of 8 bf16 values, as bits.
 __device__ __forceinline__ uint32_t mx_top(uint4 x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-  return m;
+  typedef uint16_t v2us __attribute__((ext_vector_type(2)));
+  const auto pair = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2us, a), __builtin_bit_cast(v2us, b)));
+  };
+  constexpr uint32_t mag = 0x7fff7fffu;
+  const uint32_t m = pair(pair(x.x & mag, x.y & mag), pair(x.z & mag, x.w & mag));
+  return max(m & 0xffffu, m >> 16);
 }
 // Codes of 8 bf16 values: one word of E2M1 or two of E4M3, to nearest even.  The
-// 4-bit conversion holds what is too large to 6 by itself, the 8-bit one would make
-// a NaN of it.
+// conversions divide by the scale; the 4-bit one holds what is too large to 6 by itself,
+// for the 8-bit one, which would make a NaN of it, the magnitudes are held to 448 times the
+// scale first (as bits, which order as the values do).
 template <int FMT>
 __device__ __forceinline__ uint2 mx_codes(uint4 x, uint32_t s) {
-  const float up = mx_up(s);
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  typedef short v2s __attribute__((ext_vector_type(2)));
+  typedef uint16_t v2us __attribute__((ext_vector_type(2)));
+  const float scale = __uint_as_float(s ? s << 23 : 0x00400000u);  // 2^(s - 127)
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16) * up;
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * up;
-  }
   uint2 q = make_uint2(0u, 0u);
   if constexpr (FMT == MOE_FMT_MXFP4) {
-    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q.x, v[0], v[1], 1.0f, 0);
-    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q.x, v[2], v[3], 1.0f, 1);
-    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q.x, v[4], v[5], 1.0f, 2);
-    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q.x, v[6], v[7], 1.0f, 3);
+    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q.x, __builtin_bit_cast(v2b, w[0]), scale, 0);
+    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q.x, __builtin_bit_cast(v2b, w[1]), scale, 1);
+    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q.x, __builtin_bit_cast(v2b, w[2]), scale, 2);
+    q.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q.x, __builtin_bit_cast(v2b, w[3]), scale, 3);
   } else {
+    const uint16_t most = (uint16_t)((s + 8) << 7 | 0x60u);  // 1.75 * 2^(s + 8 - 127)
+    v2b v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(v[i], -448.0f, 448.0f);
-    q.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-    q.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], (int)q.x, true);
-    q.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
-    q.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], (int)q.y, true);
+    for (int i = 0; i < 4; ++i) {
+      const v2us m = __builtin_elementwise_min(__builtin_bit_cast(v2us, w[i] & 0x7fff7fffu), v2us{most, most});
+      v[i] = __builtin_bit_cast(v2b, __builtin_bit_cast(uint32_t, m) | (w[i] & 0x80008000u));
+    }
+    v2s a = {0, 0}, b = {0, 0};
+    a = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(a, v[0], scale, false);
+    a = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(a, v[1], scale, true);
+    b = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(b, v[2], scale, false);
+    b = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(b, v[3], scale, true);
+    q = make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
   }
-  // (infinities and NaN: 0 * them is not 0)
-  return s == 255u ? make_uint2(0u, 0u) : q;
+  return s == 255u ? make_uint2(0u, 0u) : q;  // (whatever an infinity or a NaN has made)
 }
 
 // Maximum over each 4 neighbouring lanes (a block whose lanes hold 8 values each).
@@ -104,7 +106,7 @@ hipError_t launch_mx_pack(int N, int K, const uint8_t* codes, const uint8_t* sca
                           hipStream_t stream);
 // Whether a product of T rows quantises its 16-bit rows itself (else they have to be
 // quantised first).
-bool mx_linear_takes_rows(int fmt, int64_t N, int64_t K, int64_t T);
+bool mx_linear_takes_rows(int64_t N, int64_t K, int64_t T);
 // x: 16-bit rows, or NULL: codes and scales.
 hipError_t launch_mx_linear(const moe_mx_matrix* w, int fmt, const uint16_t* x, int64_t x_stride,
                             const uint8_t* codes, const uint8_t* scales, int64_t T, void* y,

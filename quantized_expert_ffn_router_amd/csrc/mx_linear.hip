@@ -56,12 +56,21 @@ __device__ __forceinline__ uint32_t load_4(Rsrc r, uint32_t at, uint32_t base) {
   return 0;
 #endif
 }
+// N bytes a lane from global memory straight into LDS: lane i's to lds + N i.  Written as
+// the instruction itself: with the builtin the compiler, which does not tell the turns of a
+// ring of buffers apart at the head of their loop, waits there for every load (256 rows, K
+// 4096, 8 bits: 17.7 us, so 14.8).  It has no output but LDS; who reads that waits with
+// wait_loads and a barrier.
 template <int N>
 __device__ __forceinline__ void load_lds(Rsrc r, uint8_t* lds, uint32_t at, uint32_t base) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  const auto to = (__attribute__((address_space(3))) void*)lds;
-  if constexpr (N == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, at, base, 0, 0);
-  else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 4, at, base, 0, 0);
+  static_assert(N == 4 || N == 16, "");
+  const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);
+  base = __builtin_amdgcn_readfirstlane(base);
+  if constexpr (N == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(at), "s"(r), "s"(base) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to), "v"(at), "s"(r), "s"(base) : "memory", "m0");
 #endif
 }
 // Waits until at most N of the wave's loads are on their way, and for all its LDS reads.
@@ -248,31 +257,35 @@ __global__ __launch_bounds__(NT == 1 ? 1024 : 512) void k_mx_few(LinearArgs a, i
 struct Few {
   int nt, ks, waves, passes;
 };
-// How a product of few rows is cut, by the steps of K and the tiles of N.
-constexpr int64_t kFewRows = 64;
+// How a product of few rows is cut, by the steps of K and the tiles of N.  (N 5120, K 2048,
+// 8 bits: 16 rows 4.9 us, 32 rows 7.5; as tiles of 64 rows 7.0 and 7.1, and 64 rows 8.6
+// where this kernel took 13.)
+constexpr int64_t kFewRows = 32;
 Few few_of(int64_t T, int steps, int tiles) {
   Few f;
-  f.nt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  f.nt = T <= 16 ? 1 : 2;
   const int most = f.nt == 1 ? 16 : 8;
-  f.ks = tiles < 256 && steps <= 2 * most ? 2 : 4;
+  // two steps of K a wave while the waves of a workgroup reach over all of it (20 x 30000 x
+  // 1024, 8 bits: 8.3 us, with four 12.7), four for many outputs of a longer K (5 x 100003 x
+  // 2048 20.9 us, with two 22.3)
+  f.ks = steps <= 8 || (steps <= 2 * most && tiles < 1024) ? 2 : 4;
   f.waves = std::min((steps + f.ks - 1) / f.ks, most);
   f.passes = (steps + f.ks * f.waves - 1) / (f.ks * f.waves);
   return f;
 }
 
-template <int FMT, bool ROWS>
+template <int FMT>
 void launch_few(const LinearArgs& a, hipStream_t stream) {
   const Few f = few_of(a.T, a.steps, a.tiles);
   // (what runs at once: 16 waves a CU)
   const unsigned grid = (unsigned)std::min(a.tiles, 256 * std::max(16 / f.waves, 1));
   const unsigned block = 64 * f.waves;
   const size_t lds = (size_t)2 * f.waves * f.nt * 1024;
-  if (f.nt == 1 && f.ks == 2) k_mx_few<FMT, ROWS, 1, 2><<<grid, block, lds, stream>>>(a, f.passes);
-  else if (f.nt == 1) k_mx_few<FMT, ROWS, 1, 4><<<grid, block, lds, stream>>>(a, f.passes);
-  else if (f.nt == 2 && f.ks == 2) k_mx_few<FMT, ROWS, 2, 2><<<grid, block, lds, stream>>>(a, f.passes);
-  else if (f.nt == 2) k_mx_few<FMT, ROWS, 2, 4><<<grid, block, lds, stream>>>(a, f.passes);
-  else if (f.ks == 2) k_mx_few<FMT, ROWS, 4, 2><<<grid, block, lds, stream>>>(a, f.passes);
-  else k_mx_few<FMT, ROWS, 4, 4><<<grid, block, lds, stream>>>(a, f.passes);
+  if (a.x) k_mx_few<FMT, true, 1, 2><<<grid, block, lds, stream>>>(a, f.passes);
+  else if (f.nt == 1 && f.ks == 2) k_mx_few<FMT, false, 1, 2><<<grid, block, lds, stream>>>(a, f.passes);
+  else if (f.nt == 1) k_mx_few<FMT, false, 1, 4><<<grid, block, lds, stream>>>(a, f.passes);
+  else if (f.ks == 2) k_mx_few<FMT, false, 2, 2><<<grid, block, lds, stream>>>(a, f.passes);
+  else k_mx_few<FMT, false, 2, 4><<<grid, block, lds, stream>>>(a, f.passes);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -528,14 +541,23 @@ void launch_gemm(const LinearArgs& a, hipStream_t stream) {
 template <int FMT>
 void linear(const LinearArgs& a, hipStream_t stream) {
   if (a.T <= kFewRows) {
-    if (a.x) launch_few<FMT, true>(a, stream);
-    else launch_few<FMT, false>(a, stream);
+    launch_few<FMT>(a, stream);
     return;
   }
-  const auto tiles = [&](int bt, int bn) { return ((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 256) launch_gemm<FMT, 2, 4, 4, 2>(a, stream);
-  else if (tiles(128, 128) >= 256) launch_gemm<FMT, 2, 2, 2, 2>(a, stream);
-  else launch_gemm<FMT, 1, 4, 2, 1>(a, stream);
+  // The tile whose rounds over the 256 CUs take the least, with the time of a round of each
+  // kind as measured (8 bits, K 4096: 64 us of 256 x 256, 38 of 128 x 256, 26 of 128 x 128, 16
+  // of 64 x 128).  16384 x 5120 x 2048: 170, 205, 220, 254 us; 4096 rows 58, 53, 56, 64; 1024
+  // rows 30, 18, 23, 21; 2048 x 2048 x 4096 55, 32, 26, 27; 256 x 5120 x 2048 28, 16, 14, 9.5.
+  const auto rounds = [&](int bt, int bn) {
+    return (((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn) + 255) / 256;
+  };
+  const int64_t cost[4] = {100 * rounds(256, 256), 60 * rounds(128, 256), 41 * rounds(128, 128), 26 * rounds(64, 128)};
+  switch (std::min_element(cost, cost + 4) - cost) {
+    case 0: launch_gemm<FMT, 2, 4, 4, 2>(a, stream); break;
+    case 1: launch_gemm<FMT, 2, 4, 2, 2>(a, stream); break;
+    case 2: launch_gemm<FMT, 2, 2, 2, 2>(a, stream); break;
+    default: launch_gemm<FMT, 1, 4, 2, 1>(a, stream);
+  }
 }
 
 // One thread: 16 bytes of codes, or a row's scales of a step.
@@ -566,9 +588,13 @@ hipError_t launch_mx_pack(int N, int K, const uint8_t* codes, const uint8_t* sca
   return hipGetLastError();
 }
 
-bool mx_linear_takes_rows(int fmt, int64_t N, int64_t K, int64_t T) {
+// Up to 16 rows whose codes a workgroup's waves hold: each workgroup makes them again (16 x
+// 5120 x 2048, 8 bits: 6.2 us, where a launch of its own takes 1.8 beside the product's 4.9
+// and a gap; 32 rows 11.6 against 1.8 and 7.5; 5 x 100003 24.9 against 1.8 and 20.9).
+bool mx_linear_takes_rows(int64_t N, int64_t K, int64_t T) {
   const MxLayout l = mx_layout(N, K);
-  return T <= kFewRows && few_of(T, (int)l.steps, (int)l.tiles).passes == 1;
+  const Few f = few_of(T, (int)l.steps, (int)std::min(l.tiles, (int64_t)INT32_MAX));
+  return T <= 16 && f.ks == 2 && f.passes == 1;
 }
 
 hipError_t launch_mx_linear(const moe_mx_matrix* w, int fmt, const uint16_t* x, int64_t x_stride,
