@@ -578,9 +578,10 @@ class KvCache:
 class AttnBuffers:
     """Per-step device buffers for up to T_max rows of n_seq sequences with page
     tables of max_pages pages; the host fills row_start, kv_len and page_table
-    (int32 device tensors) before a step."""
+    (int32 device tensors) before a step.  chunk: with the workspace of
+    attention_forward's chunk steps."""
 
-    def __init__(self, cache: KvCache, n_seq: int, T_max: int, max_pages: int, device="cuda"):
+    def __init__(self, cache: KvCache, n_seq: int, T_max: int, max_pages: int, device="cuda", chunk=False):
         import torch
         dev = torch.device(device)
         self.T_max = T_max
@@ -593,21 +594,22 @@ class AttnBuffers:
         self.max_len = max_pages * cache.desc.page_tokens
         self.q, self.k, self.out = bf16(cache.n_q), bf16(cache.n_kv), bf16(cache.n_q)
         self.ws_bytes = moe_attn_workspace_bytes(cache.desc, cache.n_q, n_seq, T_max, self.max_len)
-        self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=dev)
+        self.chunk_bytes = moe_attn_chunk_workspace_bytes(cache.desc, cache.n_q, n_seq, T_max, self.max_len) if chunk else None
+        self.ws = torch.empty(max(self.ws_bytes, self.chunk_bytes or 0, 1), dtype=torch.uint8, device=dev)
 
 
-def _check_rows(t, numel, device, name):
-    """t: contiguous bf16 values (or their bits) on the cache's device, numel of
-    them or more.  (An address cannot be checked.)"""
+def _check_rows(t, numel, device, name, call="attention_forward", other="the cache"):
+    """t: contiguous bf16 values (or their bits) on the device of `other`, numel
+    of them or more.  (An address cannot be checked.)"""
     import torch
     if isinstance(t, int):
         return
     if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or not t.is_contiguous():
-        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: {name} must be bf16 and contiguous")
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{call}: {name} must be bf16 and contiguous")
     if t.numel() < numel:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: {name} has {t.numel()} elements of {numel}")
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{call}: {name} has {t.numel()} elements of {numel}")
     if t.device != device:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: {name} is on {t.device}, the cache on {device}")
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{call}: {name} is on {t.device}, {other} on {device}")
 
 
 def _launches_on(device, stream):
@@ -620,16 +622,23 @@ def _launches_on(device, stream):
 
 
 def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: float, prompt=None,
-                      max_len=0, stream=None):
+                      max_len=0, stream=None, chunk=False):
     """One layer's attention over the step's rows qkv (bf16 [T][n_q + 2 n_kv][D],
     the projections' output): norms, rotation and cache write, then attention
     over the cache.  prompt: None for decode and verification steps; for
     prompts kv_start (int32 device [n_seq + 1], the running sum of kv_len), the
     total Tk and buffers k, v (bf16 [Tk][n_kv][D]) as a tuple: the keys and
     values, those cached earlier included, are read back into k, v first, so
-    that every chunk of a prompt attends to what the cache holds."""
+    that every chunk of a prompt attends to what the cache holds.  chunk, in
+    place of prompt: the same straight over the cache, without k and v
+    (buffers made with chunk=True; decode rows of other slots may be among the
+    step's)."""
     c, D = cache.desc, cache.D
     qw, kw = cache.n_q * D, cache.n_kv * D
+    if chunk and prompt is not None:
+        raise MoeError(MOE_ERR_INVALID_ARG, "attention_forward: chunk steps take no prompt buffers")
+    if chunk and buf.chunk_bytes is None:
+        raise MoeError(MOE_ERR_INVALID_ARG, "attention_forward: buffers made without chunk=True")
     if T > buf.T_max:
         raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: T={T} > T_max={buf.T_max}")
     if prompt is not None and min(prompt[2].numel(), prompt[3].numel()) < prompt[1] * kw:
@@ -651,7 +660,10 @@ def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: floa
     if T > 0 and not _launches_on(dev, stream):
         raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: the cache is on {dev}, not the current GPU")
     moe_kv_append(c, cache.qkv_desc, buf.seqs, qkv, qw + 2 * kw, T, None, buf.q, qw, buf.k, kw, stream)
-    if prompt is None:
+    if chunk:
+        moe_attn_chunk(c, buf.seqs, cache.n_q, buf.q, qw, T, max_len, scale, buf.out, qw, buf.ws,
+                       buf.chunk_bytes, stream)
+    elif prompt is None:
         moe_attn_decode(c, buf.seqs, cache.n_q, buf.q, qw, T, max_len, scale, buf.out, qw, buf.ws,
                         buf.ws_bytes, stream)
     else:
@@ -660,3 +672,114 @@ def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: floa
         moe_attn_prompt(cache.n_q, cache.n_kv, D, buf.seqs.n_seq, buf.row_start, kv_start, T, Tk,
                         buf.q, qw, k, kw, v, kw, scale, buf.out, qw, stream)
     return buf.out
+
+
+class MxLinear:
+    """A dense projection's weights in 4-bit microscaled form, packed for
+    moe_mx_linear: from bf16 weight [N][K] on the GPU (quantised there), or from
+    codes uint8 [N][K/2] with scales uint8 [N][K/32].  bias: float32 [N] or None."""
+
+    def __init__(self, weight, scales=None, bias=None, stream=None):
+        import torch
+        bad = lambda msg: MoeError(MOE_ERR_INVALID_ARG, f"MxLinear: {msg}")  # noqa: E731
+        if weight.dim() != 2 or not weight.is_contiguous():
+            raise bad("weight must be [N][K] and contiguous")
+        if weight.dtype != (torch.bfloat16 if scales is None else torch.uint8):
+            raise bad("weight must be bf16 without scales and uint8 codes with them")
+        dev = weight.device
+        N, K = weight.shape[0], weight.shape[1] * (1 if scales is None else 2)
+        nb = moe_mx_matrix_bytes(N, K)
+        if nb == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
+        if scales is not None and (scales.dtype != torch.uint8 or tuple(scales.shape) != (N, K // 32) or
+                                   not scales.is_contiguous() or scales.device != dev):
+            raise bad(f"scales must be uint8 [{N}][{K // 32}] on {dev}")
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or
+                                 not bias.is_contiguous() or bias.device != dev):
+            raise bad(f"bias must be float32 [{N}] on {dev}")
+        if not _launches_on(dev, stream):
+            raise bad(f"weight is on {dev}, not the current GPU")
+        self.N, self.K, self.device = N, K, dev
+        codes = weight
+        if scales is None:
+            codes = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
+            scales = torch.empty((N, K // 32), dtype=torch.uint8, device=dev)
+            moe_mx_quant(MOE_FMT_MXFP4, K, N, weight, K, codes, scales, stream)
+        self.packed = torch.empty(nb, dtype=torch.uint8, device=dev)
+        moe_mx_pack(N, K, codes, scales, self.packed, stream)
+        torch.cuda.current_stream().synchronize() if stream is None else stream.synchronize()
+        self.bias = bias
+        self.mat = MxMatrix(N, K, self.packed.data_ptr(), None if bias is None else bias.data_ptr())
+
+
+class BlockWeights:
+    """What stands around a layer's attention and experts: the norms before them
+    (float32 [H]), the projections qkv (MxLinear H -> (n_q + 2 n_kv) D) and out
+    (n_q D -> H), and the form fmt that rows take before a projection
+    (MOE_FMT_MXFP8 or MOE_FMT_MXFP4)."""
+
+    def __init__(self, attn_norm, qkv: MxLinear, out: MxLinear, ffn_norm, eps=1e-6, fmt=MOE_FMT_MXFP8):
+        import torch
+        bad = lambda msg: MoeError(MOE_ERR_INVALID_ARG, f"BlockWeights: {msg}")  # noqa: E731
+        H, dev = qkv.K, qkv.device
+        if fmt not in (MOE_FMT_MXFP4, MOE_FMT_MXFP8):
+            raise bad(f"fmt {fmt} is no form of rows")
+        if out.N != H or out.device != dev:
+            raise bad(f"out gives {out.N} values on {out.device}, qkv takes {H} on {dev}")
+        for name, w in (("attn_norm", attn_norm), ("ffn_norm", ffn_norm)):
+            if w.dtype != torch.float32 or tuple(w.shape) != (H,) or not w.is_contiguous() or w.device != dev:
+                raise bad(f"{name} must be float32 [{H}] on {dev}")
+        self.H, self.device, self.eps, self.fmt = H, dev, eps, fmt
+        self.attn_norm, self.ffn_norm, self.qkv, self.out = attn_norm, ffn_norm, qkv, out
+
+
+class BlockBuffers:
+    """Per-step device buffers of block_forward for up to T_max rows."""
+
+    def __init__(self, w: BlockWeights, T_max: int):
+        import torch
+        u8 = lambda *shape: torch.empty(shape, dtype=torch.uint8, device=w.device)  # noqa: E731
+        bf16 = lambda n: torch.empty((T_max, n), dtype=torch.bfloat16, device=w.device)  # noqa: E731
+        self.T_max, self.shape = T_max, (w.H, w.qkv.N, w.out.K, w.fmt)
+        self.codes = u8(T_max, w.H if w.fmt == MOE_FMT_MXFP8 else w.H // 2)
+        self.scales = u8(T_max, w.H // 32)
+        self.qkv, self.proj, self.sum, self.z = bf16(w.qkv.N), bf16(w.H), bf16(w.H), bf16(w.H)
+        self.ws_bytes = moe_mx_workspace_bytes(w.fmt, w.out.K, T_max)
+        self.ws = u8(max(self.ws_bytes, 1))
+
+
+def block_forward(w: BlockWeights, layer: DeviceLayer, cache: KvCache, buf: BlockBuffers, attn: AttnBuffers,
+                  step: StepBuffers, x, T: int, scale: float, prompt=None, max_len=0, stream=None, chunk=False,
+                  **layer_options):
+    """One layer from residual to residual over the step's rows x (bf16 [T][H]):
+      a = attention_forward(qkv(norm(x))), h = x + out(a), h + layer_forward(norm(h)),
+    the norms' rows going to the projection as codes.  attn, prompt, max_len and
+    chunk as for attention_forward, step and layer_options as for layer_forward.
+    Returns step.out (bf16 bits [T_max][H]; the first T rows are the step's)."""
+    call = "block_forward"
+    bad = lambda msg: MoeError(MOE_ERR_INVALID_ARG, f"{call}: {msg}")  # noqa: E731
+    H, width, kwidth = w.H, w.qkv.N, w.out.K
+    if layer.H != H:
+        raise bad(f"the experts' rows have {layer.H} values, the norms' {H}")
+    if width != (cache.n_q + 2 * cache.n_kv) * cache.D or kwidth != cache.n_q * cache.D:
+        raise bad(f"projections to {width} and from {kwidth} do not fit the cache's heads")
+    if buf.shape != (H, width, kwidth, w.fmt):
+        raise bad("buffers of other weights")
+    if (step.out.shape[1], step.logits.shape[1], step.idx.shape[1]) != (H, layer.E, layer.k):
+        raise bad("step's buffers of another layer")
+    if T < 0 or T > min(buf.T_max, attn.T_max, step.T_max):
+        raise bad(f"T={T} for buffers of {buf.T_max}, {attn.T_max} and {step.T_max} rows")
+    dev = cache.pool.device
+    for name, d in (("weights", w.device), ("buffers", buf.z.device), ("experts", layer.blobs.device),
+                    ("step's buffers", step.out.device)):
+        if d != dev:
+            raise bad(f"the {name} are on {d}, the cache on {dev}")
+    _check_rows(x, T * H, dev, "x", call)
+    if T > 0 and not _launches_on(dev, stream):
+        raise bad(f"the cache is on {dev}, not the current GPU")
+    moe_add_norm(H, T, x, H, None, 0, w.attn_norm, w.eps, None, 0, None, 0, w.fmt, buf.codes, buf.scales, stream)
+    moe_mx_linear(w.qkv.mat, w.fmt, buf.codes, buf.scales, T, buf.qkv, width, MOE_DTYPE_BF16, stream)
+    a = attention_forward(cache, attn, buf.qkv, T, scale, prompt, max_len, stream, chunk)
+    moe_mx_linear_rows(w.out.mat, w.fmt, a, kwidth, T, buf.proj, H, MOE_DTYPE_BF16, buf.ws, buf.ws_bytes, stream)
+    moe_add_norm(H, T, buf.proj, H, x, H, w.ffn_norm, w.eps, buf.sum, H, buf.z, H, 0, None, None, stream)
+    return layer_forward(layer, step, buf.z, T, buf.sum, stream=stream, **layer_options)
