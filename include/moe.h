@@ -4,8 +4,9 @@
  * router logits, softmax top-k gating, token-to-expert bucketing, block-
  * quantized (NVFP4, Q6_K-style, Q8_0, IQ3-style) SwiGLU expert FFNs with the dequantization
  * fused into the matmuls, the gate-weighted combine, and the per-step expert
- * usage histogram that decides which experts stay resident; and of the same
- * layer's attention over a paged key/value cache.
+ * usage histogram that decides which experts stay resident; of the same
+ * layer's attention over a paged key/value cache; and of the norms and
+ * microscaled dense projections around both.
  *
  * What the pages fix, and where:
  *   - each token uses a few experts chosen from many; the busiest experts stay
@@ -539,13 +540,10 @@ moe_status moe_attn_decode(const moe_kv_cache* c, const moe_seq_batch* s, int32_
 
 /* The same attention for steps with many rows of a sequence: a prompt's chunks
  * behind what is cached of it, alone or beside other slots' decode steps, long
- * verification batches.  Arguments, results for rows that see nothing, bad pages
- * and rows outside the sequences as for moe_attn_decode; the two differ in how
- * they cut the work (here a cached token is decoded once for all rows of a tile
- * of 128 (row, head) pairs) and in rounding: keys, values and softmax weights
- * meet the matrix units as bf16 for every format (NVFP4 values, code times scale,
- * are exact in it; Q8_0 values are rounded once, as moe_kv_read does), the
- * query rows as they are.
+ * verification batches.  Arguments, types, results for rows that see nothing, bad
+ * pages and rows outside the sequences as for moe_attn_decode; the two differ in how
+ * they cut the work: here a cached token is decoded once for all rows of a tile
+ * of 256 (row, head) pairs (heads of 256: 128).
  * ws: moe_attn_chunk_workspace_bytes of the same cache, heads and n_seq, with
  * this T and max_len or larger ones. */
 size_t moe_attn_chunk_workspace_bytes(const moe_kv_cache* c, int32_t n_q, int32_t n_seq, int64_t T,

@@ -5,7 +5,7 @@
 // context unless you pay for more cache").  The cache is read where it lies, without a
 // 16-bit copy: a workgroup takes one key/value head and a tile of its group's query rows
 // (the heads of a group together, so that a tile needs few tokens), decodes each 64
-// tokens once into LDS as bf16 and goes over them with
+// tokens once into LDS (codes as fp16, 16-bit caches as they are) and goes over them with
 //   scores^T (64 tokens x 32 rows of a wave) = K Q^T,  out^T (D x 32) += V^T P^T
 // as 32x32x16 matrix instructions, the running maximum and sum of the softmax in
 // registers.  Where the tiles are fewer than the CUs hold, sequences are split along the
@@ -20,7 +20,7 @@ namespace moe {
 
 namespace {
 
-typedef float v2f __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 #if defined(__HIP_DEVICE_COMPILE__)  // (the host pass does not know the builtins)
 typedef __amdgpu_buffer_rsrc_t Rsrc;
@@ -28,20 +28,26 @@ typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef const void* Rsrc;
 #endif
 
-__device__ __forceinline__ v2f fp4_pair(uint32_t w, int k) {  // byte k: two E2M1 codes
+__device__ __forceinline__ uint32_t bits(v2h v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ v2h halves(uint32_t w) { return __builtin_bit_cast(v2h, w); }
+__device__ __forceinline__ v2h fp4_pair(uint32_t w, int k) {  // byte k: two E2M1 codes
   switch (k) {
-    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    default: return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
   }
 }
-__device__ __forceinline__ float half_value(uint32_t w, int k) {  // fp16 in half k of a word
-  return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> (16 * k)));
+__device__ __forceinline__ v2h fp8_pair(uint32_t w, int k) {  // half-word k: two E4M3 scales
+  return k ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
+           : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
 }
-// int8 code k of a word whose sign bits are flipped (128 + q), times s, rounded once.
-__device__ __forceinline__ float q8_value(uint32_t biased, int k, float s, float minus) {
-  return fmaf((float)((biased >> (8 * k)) & 0xffu), s, minus);
+// int8 codes 2k, 2k + 1 of a word whose sign bits are flipped: byte b + 128 under the
+// exponent byte of 1024 is 1024 + 128 + b in fp16, exactly.
+__device__ __forceinline__ v2h i8_pair(uint32_t biased, int k) {
+  const uint32_t w = __builtin_amdgcn_perm(0x64646464u, biased, k ? 0x07030702u : 0x05010400u);
+  const v2h c = {(_Float16)1152.0f, (_Float16)1152.0f};
+  return halves(w) - c;
 }
 
 // Place of 16-byte chunk `chunk` (2 elements of 4 tokens) of a quad's values in LDS:
@@ -163,26 +169,19 @@ struct Codes {
     const int row = key_row(wave, lane);
     uint32_t c[4];
     if constexpr (FP4) {
-      const v2f s = n < 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(ks, 1.0f, false)
-                          : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(ks, 1.0f, true);
-      const float f = n / 2 & 1 ? s[1] : s[0];  // (pieces 2b, 2b + 1 are block b)
+      const v2h s = fp8_pair(ks, n / 4);  // (pieces 2b, 2b + 1 are block b)
+      const v2h f = n / 2 & 1 ? v2h{s.y, s.y} : v2h{s.x, s.x};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const v2f v = fp4_pair(kq[n], k);
-        c[k] = bf16_pair(v[0] * f, v[1] * f);
-      }
+      for (int k = 0; k < 4; ++k) c[k] = bits(fp4_pair(kq[n], k) * f);
     } else {
-      const float f = half_value(ks, n / 4), minus = -128.0f * f;
+      const v2h s = halves(ks), f = n / 4 ? v2h{s.y, s.y} : v2h{s.x, s.x};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t b = kq[2 * n + (k >> 1)] ^ 0x80808080u;
-        c[k] = bf16_pair(q8_value(b, 2 * (k & 1), f, minus), q8_value(b, 2 * (k & 1) + 1, f, minus));
-      }
+      for (int k = 0; k < 4; ++k) c[k] = bits(i8_pair(kq[2 * n + (k >> 1)] ^ 0x80808080u, k & 1) * f);
     }
     *reinterpret_cast<uint4*>(kt + row * (2 * D) + swz<D>(row, key_part(lane) * N + n) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
-  // Whether a value of the lane's that counts is NaN (its scale says so; an infinite fp16
-  // scale counts too).
+  // Whether a value of the lane's that counts may be infinite or NaN: its scale says so
+  // (fp16 scales below 512 make 65504 at most).
   __device__ __forceinline__ bool wild() const {
     bool any = false;
     if constexpr (FP4) {
@@ -190,7 +189,7 @@ struct Codes {
       for (int i = 0; i < 4; ++i) any |= ((vs[0] >> (8 * i)) & 0x7fu) == 0x7fu;
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) any |= (vs[i] & 0x7c00u) == 0x7c00u || (vs[i] & 0x7c000000u) == 0x7c000000u;
+      for (int i = 0; i < 2; ++i) any |= (vs[i] & 0x7fffu) >= 0x6000u || (vs[i] & 0x7fff0000u) >= 0x60000000u;
     }
     return any;
   }
@@ -201,6 +200,28 @@ struct Codes {
       const int by = (lane & 1) * (D == 64 ? 8 : 16);
 #pragma unroll
       for (int i = 0; i < VW; ++i) vq[i] >>= by;
+    }
+    if constexpr (FP4) {
+      // element j of two neighbouring tokens in one byte: even elements from the low
+      // nibbles, odd ones from the high ones
+      constexpr uint32_t L = 0x0f0f0f0fu;
+      if constexpr (D == 64) {  // (a word: one byte of a token, one byte of the next above 16 bits)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a = vq[i], b = a >> 16, even = (a & 0xfu) | (b << 4 & 0xf0u), odd = (a >> 4 & 0xfu) | (b & 0xf0u);
+          vq[i] = even | odd << 8;
+        }
+      } else {
+        constexpr int Q = VW / 4;  // words of a token
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < Q; ++j) {
+            const uint32_t a = vq[2 * i * Q + j], b = vq[(2 * i + 1) * Q + j];
+            vq[2 * i * Q + j] = (a & L) | (b << 4 & ~L);
+            vq[(2 * i + 1) * Q + j] = (a >> 4 & L) | (b & ~L);
+          }
+      }
     }
     if (left < kBN) {
       const int n = min(max(left - 4 * quad_of(wave, lane), 0), 4);
@@ -216,28 +237,15 @@ struct Codes {
     const int quad = quad_of(wave, lane);
     uint32_t c[4];
     if constexpr (FP4) {
-      const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs[0], 1.0f, false);
-      const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs[0], 1.0f, true);
-      v2f p[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        // byte n of token t's
-        if constexpr (D == 64) p[t] = fp4_pair(vq[t / 2], 2 * (t & 1));
-        else if constexpr (D == 128) p[t] = fp4_pair(vq[t], n);
-        else p[t] = fp4_pair(vq[2 * t + n / 4], n % 4);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        c[2 * k] = bf16_pair(p[0][k] * a[0], p[1][k] * a[1]);
-        c[2 * k + 1] = bf16_pair(p[2][k] * b[0], p[3][k] * b[1]);
+      for (int k = 0; k < 4; ++k) {  // elements 2n (k < 2), 2n + 1 of tokens 0, 1 or 2, 3
+        constexpr int Q = VW / 4;
+        const v2h e = D == 64 ? fp4_pair(vq[k & 1], k >> 1) : fp4_pair(vq[(2 * (k & 1) + (k >> 1)) * Q + n / 4], n % 4);
+        c[k] = bits(e * fp8_pair(vs[0], k & 1));
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t b = vq[2 * n + (k >> 1)] ^ 0x80808080u;
-        const float s0 = half_value(vs[k & 1], 0), s1 = half_value(vs[k & 1], 1);
-        c[k] = bf16_pair(q8_value(b, 2 * (k & 1), s0, -128.0f * s0), q8_value(b, 2 * (k & 1) + 1, s1, -128.0f * s1));
-      }
+      for (int k = 0; k < 4; ++k) c[k] = bits(i8_pair(vq[2 * n + (k >> 1)] ^ 0x80808080u, k & 1) * halves(vs[k & 1]));
     }
     *reinterpret_cast<uint4*>(vt + quad * (8 * D) + vswz<D>(quad, lane % QL * N + n) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
@@ -280,15 +288,18 @@ struct Codes<MOE_FMT_BF16, D, W> {
   }
 };
 
-// The rows of a wave against tiles whose values lie as quads.
-template <int D>
-struct ChunkRows : TileRows<D> {
+// The rows of a wave against tiles whose values lie as quads.  HALF: codes were decoded to
+// fp16; the maximum is then held less kRaise (log2), so that weights are 2^15 at most and
+// vanish only below 2^-32 of the largest.
+template <int D, bool HALF>
+struct ChunkRows : TileRows<D, HALF> {
+  static constexpr float kRaise = HALF ? 7.0f : 0.0f;
   static constexpr int KS = D / 16, NJ = D / 32;
-  using TileRows<D>::qf;
-  using TileRows<D>::o;
-  using TileRows<D>::h;
-  using TileRows<D>::m;
-  using TileRows<D>::l;
+  using TileRows<D, HALF>::qf;
+  using TileRows<D, HALF>::o;
+  using TileRows<D, HALF>::h;
+  using TileRows<D, HALF>::m;
+  using TileRows<D, HALF>::l;
   uint32_t ka[KS], va[NJ];  // this lane's places in a K and a V tile
 
   __device__ __forceinline__ void places(int lane) {
@@ -322,16 +333,36 @@ struct ChunkRows : TileRows<D> {
       for (int i = 0; i < 16; ++i) x[t][i] = 0.0f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        x[t] = mma(key(kt, t, s), qf[s], x[t]);
+        x[t] = mma<HALF>(key(kt, t, s), qf[s], x[t]);
         if (s % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (few fragments at a time)
       }
     }
   }
+  // bf16 -> fp16, scaled by the power of two that puts the row's largest magnitude into
+  // [2^14, 2^15): exact for values above 2^-29 of it (of rows whose largest one is below
+  // 2^-82, less, which no score shows).  Returns what undoes it.
+  __device__ __forceinline__ float halve() {
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(qf[s][i] & 0x7fffu, (qf[s][i] >> 16) & 0x7fffu));
+    const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+    const int e = min(max(141 - (int)(max(both[0], both[1]) >> 7), -113), 96);
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        qf[s][i] = bits(v2h{(_Float16)(__uint_as_float(qf[s][i] << 16) * up),
+                            (_Float16)(__uint_as_float(qf[s][i] & 0xffff0000u) * up)});
+    return __uint_as_float((uint32_t)(127 - e) << 23);
+  }
   // A new maximum for the rows whose weights would leave 2^kGrow with the largest scaled
   // score mx (the others' answers do not depend on them, bit for bit).
   __device__ __forceinline__ void raise(float mx) {
-    if (__any(mx > m + kGrow)) {
-      const float mn = mx > m + kGrow ? mx : m, al = __builtin_amdgcn_exp2f(m - mn);
+    if (__any(mx > m + (kRaise + kGrow))) {
+      const float mn = mx > m + (kRaise + kGrow) ? mx - kRaise : m, al = __builtin_amdgcn_exp2f(m - mn);
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -368,7 +399,7 @@ struct ChunkRows : TileRows<D> {
           for (int i = 0; i < 4; ++i) one[i] = i == at ? f[i] & keep : 0u;
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-          z = mma(one, p[s], z);
+          z = mma<HALF>(one, p[s], z);
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[j][i] += seen ? z[i] : 0.0f;
         }
@@ -423,7 +454,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
   // this lane's query row; a lane without one takes the tile's last (its answer goes
   // nowhere: another tile's row may be overwritten meanwhile, where the output takes the
   // queries' place)
-  ChunkRows<D> w;
+  ChunkRows<D, DECODED> w;
   const int slot = (it.tile * W + wave) * 32 + n, last_slot = inside * a.G - 1;
   const int mine = min(slot, last_slot), row = (int)((uint32_t)mine / (uint32_t)a.G);
   const int64_t at = (int64_t)(r0 + row);
@@ -432,6 +463,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
   const uint16_t* qp = a.q + at * a.q_stride + (int64_t)head * D + 8 * (lane >> 5);
 #pragma unroll
   for (int s = 0; s < KS; ++s) w.qf[s] = *reinterpret_cast<const v4u*>(qp + 16 * s);
+  const float c_log2 = DECODED ? a.scale_log2 * w.halve() : a.scale_log2;
   w.places(lane);
   w.clear();
   // last token that some row of the wave sees
@@ -480,6 +512,13 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
     __syncthreads();
   };
 
+      const auto is_wild = [&](const uint8_t* vt, const int* found) {
+        if constexpr (!DECODED) return wild<D>(vt, lane);
+        int any = 0;
+  #pragma unroll
+        for (int i = 0; i < W; ++i) any |= found[i];
+        return any != 0;
+      };
   bool some_wild = false;
   typedef Codes<FMT, D, W> C;
   const auto put_all = [&](const C& c, uint8_t* kt, uint8_t* vt) {
@@ -499,13 +538,6 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
         const bool any = __any(c.wild());
         if (lane == 0) found[wave] = any;
       }
-    };
-    const auto is_wild = [&](const uint8_t* vt, const int* found) {
-      if constexpr (!DECODED) return wild<D>(vt, lane);
-      int any = 0;
-#pragma unroll
-      for (int i = 0; i < W; ++i) any |= found[i];
-      return any != 0;
     };
     // keys of tile t, values of tile t - 1
     const auto fetch = [&](C& c, int t, uint8_t* kt, uint8_t* vt) {
@@ -544,7 +576,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
     v16f x[2];
     w.scores(k_even, x);
     if (first >= full) w.mask(x, (int64_t)first * kBN);
-    w.raise(w.top(x, a.scale_log2));
+    w.raise(w.top(x, c_log2));
 
     // Turn t: x holds tile t's scores, which the maxima cover, k1 the keys of t + 1, v0 the values of t; the keys
     // of t + 2 go to k0, the values of t + 1 to v1.
@@ -569,7 +601,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
       v16f y[2];
       float most = -__builtin_inff();
       w.template stream<true>([&](int h, int s) { return w.key(k1, h, s); }, [&](int s, int j) { return w.value(v0, s, j); },
-                              a.scale_log2, x, y, [&](auto I) {
+                              c_log2, x, y, [&](auto I) {
         constexpr int N = 2 * KS + 4 * NJ, i = I();
         each<C::PIECES * i / N, C::PIECES * (i + 1) / N>([&](auto p) { c.put(p(), k0, v1, wave, lane); });
         // the next scores' maximum, beside the second product
@@ -578,7 +610,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
 #pragma unroll
           for (int v = 32 * (i - F) / L; v < 32 * (i - F + 1) / L; ++v) most = fmaxf(most, y[v >> 4][v & 15]);
       });
-      w.raise(w.over_halves(most) * a.scale_log2);
+      w.raise(w.over_halves(most) * c_log2);
       finish(t, c, y);
     };
     // Tiles that not every row sees, and the last ones: a wave leaves out those none of its
@@ -595,12 +627,12 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
           some_wild = true;
         }
         w.template stream<false>([&](int, int) { return v4u{0, 0, 0, 0}; },
-                                 [&](int s, int j) { return w.value(v0, s, j) & keep; }, a.scale_log2, x, y, [](auto) {});
+                                 [&](int s, int j) { return w.value(v0, s, j) & keep; }, c_log2, x, y, [](auto) {});
       }
       if (t + 1 < end && t0 + kBN <= hi_wave) {
         w.scores(k1, y);
         if (t + 1 >= full) w.mask(y, t0 + kBN);
-        w.raise(w.top(y, a.scale_log2));
+        w.raise(w.top(y, c_log2));
       }
       finish(t, c, y);
     };
@@ -629,6 +661,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
         c.fetch_keys(from, lay, wave, lane);
         c.fetch_values(from, lay, P, wave, lane);
         c.arrange_values(left_of(t), wave, lane);
+        wild_even[wave] = __any(c.wild());
         put_all(c, k_even, v_even);
         __syncthreads();
       } else {
@@ -638,7 +671,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
         __syncthreads();
         clear_behind(t, v_even);
       }
-      if ((int64_t)t * kBN <= hi_wave && wild<D>(v_even, lane)) w.gather_seen(k_even, v_even, (int64_t)t * kBN, a.scale_log2);
+      if ((int64_t)t * kBN <= hi_wave && is_wild(v_even, wild_even)) w.gather_seen(k_even, v_even, (int64_t)t * kBN, c_log2);
     }
   }
   w.finish();

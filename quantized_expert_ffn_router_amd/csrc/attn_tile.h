@@ -9,15 +9,20 @@ namespace moe {
 namespace {
 
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
 constexpr int kBN = 64;  // keys of a tile
 
+// HALF: operands of fp16, not bf16.
+template <bool HALF = false>
 __device__ __forceinline__ v16f mma(v4u a, v4u b, v16f c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a),
-                                                 __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+  if constexpr (HALF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
 }
 
 // Place of 16-byte chunk `chunk` of row `row` in an LDS tile of D-wide rows:
@@ -38,11 +43,18 @@ __device__ __forceinline__ void wait_loads() {
 #endif
 }
 
-// Two softmax weights as bf16, rounded to nearest even (half a step, 2^-8: the
-// operand type of the second product), and their sum added to l -- of the
+// Two softmax weights in the operand type of the second product, rounded to
+// nearest even (half a step: 2^-8, fp16 2^-11), and their sum added to l -- of the
 // rounded weights, so that rounding does not shift a row's mean.
+template <bool HALF>
 __device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
   typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+  if constexpr (HALF) {
+    const v2h w = {(_Float16)a, (_Float16)b}, one = {(_Float16)1.0f, (_Float16)1.0f};
+    *l = __builtin_amdgcn_fdot2(w, one, *l, false);
+    return __builtin_bit_cast(uint32_t, w);
+  }
   const v2b w = {(__bf16)a, (__bf16)b};
   const v2b one = {(__bf16)1.0f, (__bf16)1.0f};
   *l = __builtin_amdgcn_fdot2_f32_bf16(w, one, *l, false);
@@ -61,7 +73,7 @@ __device__ __forceinline__ void each(F&& f) {
 
 // What a wave carries for 32 query rows: a lane column is one row, its accumulators and
 // statistics the lane's own.
-template <int D>
+template <int D, bool HALF = false>
 struct TileRows {
   static constexpr int KS = D / 16, NJ = D / 32;
   v4u qf[KS];
@@ -112,7 +124,7 @@ struct TileRows {
   __device__ __forceinline__ void weight(v16f (&x)[2], float c, v4u (&p)[4], int v) {
     const int t = v >> 4, i = v & 15;
     x[t][i] = __builtin_amdgcn_exp2f(fmaf(x[t][i], c, -m));
-    if (i & 1) p[v >> 3][(i & 7) >> 1] = weight_pair(x[t][i - 1], x[t][i], &l);
+    if (i & 1) p[v >> 3][(i & 7) >> 1] = weight_pair<HALF>(x[t][i - 1], x[t][i], &l);
   }
   // The scores y of one tile and the weighted values of the tile before (scores x), as one
   // stream: a matrix instruction, then a piece of the softmax in its shadow, and
@@ -145,10 +157,10 @@ struct TileRows {
         v16f zero;
 #pragma unroll
         for (int k = 0; k < 16; ++k) zero[k] = 0.0f;
-        y[i / KS] = mma(f[i % kRing], qf[i % KS], i % KS ? y[i / KS] : zero);
+        y[i / KS] = mma<HALF>(f[i % kRing], qf[i % KS], i % KS ? y[i / KS] : zero);
       } else {
         constexpr int s = (i - N1) / NJ, j = (i - N1) % NJ;
-        o[j] = mma(f[i % kRing], p[s], o[j]);
+        o[j] = mma<HALF>(f[i % kRing], p[s], o[j]);
       }
 #pragma unroll
       for (int v = weights_by(i - 1); v < weights_by(i); ++v) weight(x, c, p, v);

@@ -4,7 +4,7 @@ layer uses them: block_forward and attention_forward's chunk steps, each stage a
 decode steps, eager and captured.
 
 Bounds: codes, sums and normed rows bit for bit; products within mx_ref.product_bound;
-attention within attn_ref.attend_bound (decode) or test_gpu_chunk.weight_bound (chunks); the
+attention within attn_ref.attend_bound (decode) or test_gpu_chunk.chunk_bound (chunks); the
 experts bit for bit what layer_forward gives for the same rows."""
 import math
 
@@ -19,7 +19,7 @@ import quantized_expert_ffn_router_amd as q
 from attn_ref import BF16, NVFP4, Q8_0
 from mx_ref import MXFP4, MXFP8
 from test_gpu_attention import FMT, bits, i32, to_dev
-from test_gpu_chunk import weight_bound
+from test_gpu_chunk import chunk_bound
 from test_gpu_norm_linear import tops
 
 pytestmark = pytest.mark.gpu
@@ -103,14 +103,11 @@ def check_stages(m, l, x, rows, T, chunk, out):
                 lim = m.lens[i] - n + r
                 span = slice(start[i], start[i + 1])
                 want, pv, qk = ref.attend(qs[t, col], k[span, kvh], v[span, kvh], lim, scale)
-                if chunk:  # (the keys and values read back are Q8_0's as they meet the units)
-                    w = weight_bound(m.fmt, qk, D, lim + 1)
-                    bound = np.abs(want) * 2.0 ** -8 * (1 + w) + pv * w * (1 + 2.0 ** -8) + 1e-30
-                else:  # (Q8_0: the read back is rounded to bf16, 2^-8, where the kernel rounds to fp16)
-                    vmax = float(np.abs(v[span, kvh]).max())
-                    bound = ref.attend_bound(want, pv, qk, lim + 1, vmax, D, m.fmt)
-                    if m.fmt == Q8_0:
-                        bound = bound + pv * (2.0 ** -8 + 2 * math.expm1(min(qk * 2.0 ** -8, 1.0))) * (1 + 2.0 ** -6)
+                vmax = float(np.abs(v[span, kvh]).max())
+                bound = (chunk_bound(m.fmt, want, pv, qk, D, lim + 1, vmax) if chunk
+                         else ref.attend_bound(want, pv, qk, lim + 1, vmax, D, m.fmt))
+                if m.fmt == Q8_0:  # (what is read back is rounded to bf16, 2^-8: the values and, in the scores, the keys)
+                    bound = bound + pv * (2.0 ** -8 + 2 * math.expm1(min(qk * 2.0 ** -8, 1.0))) * (1 + 2.0 ** -6)
                 assert (np.abs(o[t, col] - want) <= bound).all(), (i, r, h)
             t += 1
     c, s = mx_ref.quantise(fmt, host(m.attn.out))
@@ -247,8 +244,9 @@ def test_chunk_steps_of_attention_forward(fmt):
             lens.append(kv)
     one, two = torch.cat(outs[:3]), torch.cat(outs[3:])
     v = lens[-1][1].double().view(150, N_KV, 1, D).abs().amax(0).expand(-1, n_q // N_KV, -1).reshape(-1)
-    # each rounds its weights to bf16 (2^-8, in numerator and denominator) and the result (2^-8);
-    # scores of normed keys and queries: |s| <= D^1/2, fp32 sums of D products, D 2^-24 of it;
-    # sum p|v| is at most the largest |v|
-    w = 2.0 ** -7 + 2 * math.expm1(D ** 0.5 * 1.02 * D * 2.0 ** -24) + 2.0 ** -20 + 150 * 2.0 ** -24
+    # each rounds its weights to 2^-8 or finer, in numerator and denominator, and the result
+    # (2^-8); scores of normed keys and queries: |s| <= D^1/2, fp32 sums of D products, D 2^-24
+    # of it; Q8_0 keys and values: rounded to 2^-8 or finer; sum p|v| is at most the largest |v|
+    e_kv = 2.0 ** -8 if fmt == Q8_0 else 0.0
+    w = 2.0 ** -7 + e_kv + 2 * math.expm1(D ** 0.5 * 1.02 * (D * 2.0 ** -24 + e_kv)) + 2.0 ** -20 + 150 * 2.0 ** -24
     assert ((one - two).abs() <= 2 * (w + 2.0 ** -8 * (1 + w)) * v).all()
