@@ -636,9 +636,11 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
       }
       finish(t, c, y);
     };
+    // (waves without a row, in tiles of few, only decode)
+    const int all = hi_wave < 0 ? first : full;
     int t = first;
 #pragma unroll 1
-    for (; t + 2 < full; t += 2) {
+    for (; t + 2 < all; t += 2) {
       step(t, c_even, k_even, k_odd, v_even, v_odd, wild_odd);
       step(t + 1, c_odd, k_odd, k_even, v_odd, v_even, wild_even);
     }
