@@ -44,6 +44,7 @@ __device__ __forceinline__ int units_of_table(const SeqView& s) {
 struct LaneSeq {
   int start, end, len;
   int tiles, units;
+  bool light;  // a single tile, a quarter of it or less filled
   __device__ __forceinline__ LaneSeq(const SeqView& s, int i0, int64_t T, int G, int size) {
     const int i = min(i0 + lane_id(), s.n_seq - 1);
     start = max(s.row_start[i], 0);
@@ -51,6 +52,7 @@ struct LaneSeq {
     len = s.kv_len[i];
     const int64_t n = i0 + lane_id() < s.n_seq ? min((int64_t)end, T) - start : 0;
     tiles = n > 0 ? (int)((uint32_t)((int)n * G + size - 1) / (uint32_t)size) : 0;
+    light = n * G <= size / 4;
     units = n > 0 && len > 0 ? min((len - 1) / 32 + 1, units_of_table(s)) : 0;
   }
 };
@@ -67,11 +69,16 @@ constexpr int kWhole = 4 * kWaves;
 // lasts as long as its longest item, a chunk and what a workgroup needs before and behind
 // it, about kStart units; joining costs as much again.
 constexpr int kStart = 8;
-__device__ __forceinline__ int fit_chunk(const LaneSeq& q, float work, int most, int room, int rounds,
-                                         int least) {
+// Units go faster where most waves only decode (8 slots of one row behind 16000 tokens 70 us,
+// of 85 rows 116; over NVFP4 48 and 90): chunks of such sequences are half as long again, and
+// those of a sequence as even as they come (512 mixed rows over Q8_0 119 -> 98 us; 1.75 times
+// as long, and uneven, 103, and 513 rows beside 7 slots of one behind 8000 tokens 156, not 141).
+__device__ __forceinline__ int chunk_of(int chunk, bool light) { return light ? (chunk + chunk / 2) & ~1 : chunk; }
+__device__ __forceinline__ int fit_chunk(const LaneSeq& q, int most, int room, int rounds, int least) {
   const auto items = [&](int c) {
-    return wave_sum((float)q.tiles * (float)(q.units ? (int)((uint32_t)(q.units - 1) / (uint32_t)c) + 1 : 1));
+    return wave_sum((float)q.tiles * (float)(q.units ? (int)((uint32_t)(q.units - 1) / (uint32_t)chunk_of(c, q.light)) + 1 : 1));
   };
+  const float work = wave_sum((float)q.tiles * (float)q.units * (q.light ? 2.0f / 3.0f : 1.0f));
   const int whole = max((most + 1) & ~1, 2);
   const float tiles = items(whole);
   int chunk = whole;
@@ -103,6 +110,7 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
   r.b = -1;
   r.chunk = INT32_MAX;
   const LaneSeq first(s, 0, T, G, size);
+  const bool fit = FIT && S > 1 && s.n_seq <= 64;
   if (S > 1) {
     float work = 0.0f;
     int most = 0;
@@ -113,8 +121,8 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
     }
     work = wave_sum(work);
     most = wave_max(most);
-    if (FIT && s.n_seq <= 64) {
-      r.chunk = __builtin_amdgcn_readfirstlane(fit_chunk(first, work, most, room, rounds, ((most + S - 1) / S + 1) & ~1));
+    if (fit) {
+      r.chunk = __builtin_amdgcn_readfirstlane(fit_chunk(first, most, room, rounds, ((most + S - 1) / S + 1) & ~1));
     } else {
       // (a sequence has less than 2^27 units: held to 2^30, it stays an int)
       int chunk = (int)fminf(ceilf(work / (float)room), 0x1p30f);
@@ -127,7 +135,15 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
   for (int i0 = 0; i0 < s.n_seq; i0 += 64) {
     const LaneSeq q = i0 ? LaneSeq(s, i0, T, G, size) : first;
     // (a row without tokens is answered too)
-    const int splits = S > 1 && q.units ? (int)((uint32_t)(q.units - 1) / (uint32_t)r.chunk) + 1 : 1;
+    const auto parts = [&](int chunk) {
+      return S > 1 && q.units ? (int)((uint32_t)(q.units - 1) / (uint32_t)chunk) + 1 : 1;
+    };
+    int chunk = r.chunk, splits = parts(chunk);
+    if (fit) {  // (as even as they come)
+      splits = parts(chunk_of(chunk, q.light));
+      chunk = max(((int)((uint32_t)(q.units + splits - 1) / (uint32_t)splits) + 1) & ~1, 2);
+      splits = parts(chunk);
+    }
     const int sum = wave_incl_scan(q.tiles * splits * n_kv);
     const uint64_t past = __ballot(i0 + lane_id() < s.n_seq && before + sum > id);
     if (!past) {
@@ -143,6 +159,7 @@ __device__ __forceinline__ Item find_item(const SeqView& s, int64_t T, int G, in
     r.len = __builtin_amdgcn_readlane(q.len, l);
     r.inside = (int)min(rows, T - r.r0);
     r.splits = __builtin_amdgcn_readlane(splits, l);
+    r.chunk = __builtin_amdgcn_readlane(chunk, l);
     const int at = (int)((uint32_t)(id - before) / (uint32_t)r.splits);
     r.sp = id - before - at * r.splits;
     r.tile = (int)((uint32_t)at / (uint32_t)n_kv);
