@@ -730,8 +730,10 @@ Shape shape_of(int D, int n_kv, int n_q, int n_seq, int64_t T, int64_t max_len) 
   const bool whole = n_seq == 1 && tiles <= r.room && units + kStart <= once;
   r.S = T * n_q > kChunkPairs || S < 2 || (n_seq == 1 && base >= 512) || units <= 8 || whole ? 1 : (int)S;
   r.likely = (int)std::min({std::max(units / kWaves, (int64_t)1), std::max(256 / base, (int64_t)1), (int64_t)r.S});
-  // (workgroups without an item take their place on a CU too: no more than may be needed)
-  r.rounds = tiles <= r.room ? 1 : 2;
+  // Workgroups without an item take their place on a CU too, 5 to 7 us for a round of them: a
+  // second one only where it may save more (900 rows beside 6 slots of one, behind 11000 to
+  // 17000 tokens, 326 us, with it 281; 130 rows over five slots behind 5000 46, with it 52).
+  r.rounds = tiles <= r.room && tiles * units < (int64_t)240 * r.room ? 1 : 2;
   r.items = r.S == 1 ? tiles : n_seq > 64 ? tiles + r.room + 1 : std::max(tiles, (int64_t)r.rounds * r.room);
   return r;
 }
