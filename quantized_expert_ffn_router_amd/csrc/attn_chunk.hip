@@ -745,6 +745,14 @@ void launch_chunk(const SplitArgs& a, int D, unsigned grid, hipStream_t stream) 
   else k_attn_chunk<FMT, 256, chunk_waves(256)><<<grid, 64 * chunk_waves(256), 0, stream>>>(a);
 }
 
+// A few splits are joined by a wave (512 mixed rows of 24 heads, 4 to 6 splits each: 90 us with
+// both launches; a workgroup for each row and head, 97).
+template <int D>
+void join(const SplitArgs& a, hipStream_t stream) {
+  if (a.likely > 16) launch_join<D>(a, stream);
+  else k_attn_join_heads<D, D == 64 ? 4 : 8><<<(unsigned)((a.T * a.n_q + 3) / 4), 256, 0, stream>>>(a);
+}
+
 }  // namespace
 
 size_t attn_chunk_ws_bytes(int n_kv, int D, int n_q, int n_seq, int64_t T, int64_t max_len) {
@@ -779,9 +787,9 @@ hipError_t launch_attn_chunk(const moe_kv_cache* c, const moe_seq_batch* s, int 
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.S == 1) return e;
   switch (c->D) {
-    case 64: launch_join<64>(a, stream); break;
-    case 128: launch_join<128>(a, stream); break;
-    default: launch_join<256>(a, stream);
+    case 64: join<64>(a, stream); break;
+    case 128: join<128>(a, stream); break;
+    default: join<256>(a, stream);
   }
   return hipGetLastError();
 }

@@ -284,6 +284,72 @@ void launch_join(const SplitArgs& a, hipStream_t stream) {
   else k_attn_join<D, 32, kMaxSplit / 32><<<heads * (D / 32), 256, 0, stream>>>(a);
 }
 
+// The same with a wave for a row and head, four of them a workgroup: D / 4 lanes hold the
+// elements, 256 / D groups of them the splits, PER at a time.
+template <int D, int PER>
+__global__ __launch_bounds__(256) void k_attn_join_heads(SplitArgs a) {
+  constexpr int LW = D / 4, NG = 64 / LW;
+  const int lane = lane_id(), x = lane % LW, grp = lane / LW;
+  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= a.T * a.n_q) return;
+  const int t = (int)((uint32_t)id / (uint32_t)a.n_q), h = (int)((uint32_t)id % (uint32_t)a.n_q);
+  const int64_t at = id * a.S;
+  int ns = a.part_n[id];
+  float2 ml[PER];
+  float4 v[PER];
+  const auto load = [&](int i, int s) {
+    ml[i] = a.part_ml[at + s];
+    v[i] = *reinterpret_cast<const float4*>(a.part_o + (at + s) * D + 4 * x);
+  };
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (grp + NG * i < a.likely) load(i, grp + NG * i);
+  const RowSeq q = find_row(a.s, t, &ns);
+  ns = __builtin_amdgcn_readfirstlane(min(ns, a.S));
+  if (q.b < 0 || ns == 1) return;
+  float M = kNone, L = 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = grp; s0 < ns; s0 += NG * PER) {
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int s = s0 + NG * i;
+      if (s >= ns) ml[i] = make_float2(kNone, 0.0f);
+      else if (s >= a.likely || s0 != grp) load(i, s);
+      top = fmaxf(top, ml[i].x);
+    }
+    const float down = __builtin_amdgcn_exp2f(M - top);
+    o.x *= down; o.y *= down; o.z *= down; o.w *= down;
+    L *= down;
+    M = top;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (ml[i].x == kNone && ml[i].y == 0.0f) continue;  // nothing there
+      const float f = __builtin_amdgcn_exp2f(ml[i].x - M);
+      o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
+      L += f * ml[i].y;
+    }
+  }
+  float all = M;
+#pragma unroll
+  for (int d = LW; d < 64; d <<= 1) all = fmaxf(all, __shfl_xor(all, d));
+  const float down = __builtin_amdgcn_exp2f(M - all);
+  o.x *= down; o.y *= down; o.z *= down; o.w *= down;
+  L *= down;
+#pragma unroll
+  for (int d = LW; d < 64; d <<= 1) {
+    o.x += __shfl_xor(o.x, d); o.y += __shfl_xor(o.y, d);
+    o.z += __shfl_xor(o.z, d); o.w += __shfl_xor(o.w, d);
+    L += __shfl_xor(L, d);
+  }
+  if (grp == 0) {
+    const float inv = (int64_t)q.len - q.rows + (t - q.r0) < 0 ? 0.0f : 1.0f / L, ts = a.v_ts;
+    uint16_t* d = a.out + t * a.out_stride + (int64_t)h * D + 4 * x;
+    *reinterpret_cast<uint2*>(d) = make_uint2(bf16_pair(o.x * inv * ts, o.y * inv * ts),
+                                              bf16_pair(o.z * inv * ts, o.w * inv * ts));
+  }
+}
+
 }  // namespace
 
 }  // namespace moe
