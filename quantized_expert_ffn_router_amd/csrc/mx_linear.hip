@@ -14,6 +14,7 @@
 // (0, 1) and (2, 3) of a 128-element step (16x16x128) or of both blocks of a 64-element
 // one: lane group g holds elements 16 g.. of each half, and the scale of block g.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx.h"
 
@@ -84,6 +85,15 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   typedef __bf16 v2b __attribute__((ext_vector_type(2)));
   const v2b r = {(__bf16)a, (__bf16)b};
   return __builtin_bit_cast(uint32_t, r);
+}
+
+// f of the numbers I .. N - 1, each as a type.
+template <int I, int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each<I + 1, N>(f);
+  }
 }
 
 struct LinearArgs {
@@ -346,18 +356,26 @@ struct Gemm {
   }
   // (Of a step behind the last one nothing is read: its loads are there so that as many are
   // always on their way, without a branch, past which the matrix instructions would move.)
-  __device__ __forceinline__ void load(uint8_t* lds, int ks) const {
+  struct Step {
+    Rsrc x, w, s;
+    int k;
+  };
+  __device__ __forceinline__ Step step(int ks) const {
     const bool in = ks < a.steps;
-    const Rsrc x = buffer_of(rows, in ? row_bytes : 0), w = buffer_of(weights, in ? weight_bytes : 0);
-    const Rsrc s = buffer_of(scales, in ? scale_bytes : 0);
-    const int k = in ? ks : 0;
+    return Step{buffer_of(rows, in ? row_bytes : 0), buffer_of(weights, in ? weight_bytes : 0),
+                buffer_of(scales, in ? scale_bytes : 0), in ? ks : 0};
+  }
+  // Load i of PER.
+  __device__ __forceinline__ void load(const Step& f, uint8_t* lds, int i) const {
+    const int u = i * WAVES + wave;
+    if (i == PER - 1) load_lds<4>(f.s, lds + OS + (wave % NS) * 256, at[PER - 1], f.k * scale_step);
+    else if (i < NA / WAVES) load_lds<16>(f.x, lds + OA + u * 1024, at[i], f.k * CB);
+    else load_lds<16>(f.w, lds + OB + (u - NA) * 1024, at[i], f.k * 1024);
+  }
+  __device__ __forceinline__ void load(uint8_t* lds, int ks) const {
+    const Step f = step(ks);
 #pragma unroll
-    for (int i = 0; i < PER - 1; ++i) {
-      const int u = i * WAVES + wave;
-      if (i < NA / WAVES) load_lds<16>(x, lds + OA + u * 1024, at[i], k * CB);
-      else load_lds<16>(w, lds + OB + (u - NA) * 1024, at[i], k * 1024);
-    }
-    load_lds<4>(s, lds + OS + (wave % NS) * 256, at[PER - 1], k * scale_step);
+    for (int i = 0; i < PER; ++i) load(f, lds, i);
   }
   __device__ __forceinline__ v8i row_part(const uint8_t* lds, int f, int j) const {
     const int row = (wt * FT + f) * 32 + r;
@@ -386,33 +404,43 @@ struct Gemm {
   struct Parts {
     v8i p[FT], q[FN];
   };
-  __device__ __forceinline__ void parts(const uint8_t* lds, int j, Parts& f) const {
-#pragma unroll
-    for (int n = 0; n < FN; ++n) f.q[n] = weight_part(lds, n, j);
-#pragma unroll
-    for (int t = 0; t < FT; ++t) f.p[t] = row_part(lds, t, j);
+  // Part i of FN + FT, in the order of their use.
+  __device__ __forceinline__ void part(const uint8_t* lds, int j, Parts& f, int i) const {
+    if (i < FN) f.q[i] = weight_part(lds, i, j);
+    else f.p[i - FN] = row_part(lds, i - FN, j);
   }
-  // The step's scales: that of block 2 J + h of a row is byte 2 J of its word shifted by h
-  // bytes.
+  // The step's scales, as they lie: that of block 2 J + h of a row is byte 2 J of its word
+  // shifted by h bytes.
   struct Scales {
-    int p[FT], q[FN];
+    uint32_t p[FT], q[FN];
   };
   __device__ __forceinline__ void scales_of(const uint8_t* lds, Scales& s) const {
 #pragma unroll
-    for (int t = 0; t < FT; ++t)
-      s.p[t] = (int)(*reinterpret_cast<const uint32_t*>(lds + OS + ((wt * FT + t) * 32 + r) * 4) >> (8 * h));
-#pragma unroll
     for (int n = 0; n < FN; ++n)
-      s.q[n] = (int)(*reinterpret_cast<const uint32_t*>(lds + OS + (BT + (wn * FN + n) * 32 + r) * 4) >> (8 * h));
-  }
-  template <int J>
-  __device__ __forceinline__ void product(const Parts& f, const Scales& s, v16f (&o)[FT][FN]) const {
+      s.q[n] = *reinterpret_cast<const uint32_t*>(lds + OS + (BT + (wn * FN + n) * 32 + r) * 4);
 #pragma unroll
     for (int t = 0; t < FT; ++t)
+      s.p[t] = *reinterpret_cast<const uint32_t*>(lds + OS + ((wt * FT + t) * 32 + r) * 4);
+  }
+  __device__ __forceinline__ void shift(Scales& s) const {
 #pragma unroll
-      for (int n = 0; n < FN; ++n)
-        o[t][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.q[n], f.p[t], o[t][n], kFp4, kOperand<FMT>,
-                                                                  2 * J, s.q[n], 2 * J, s.p[t]);
+    for (int n = 0; n < FN; ++n) s.q[n] >>= 8 * h;
+#pragma unroll
+    for (int t = 0; t < FT; ++t) s.p[t] >>= 8 * h;
+  }
+  // The FT * FN matrix instructions of half a step; beside them the caller's pieces
+  // 0 .. PIECES - 1 (a type each), all but the last instruction's time for them.  Kept in
+  // this order: left to the compiler, the loads and the wait for the next scales stood before
+  // the instructions (16384 x 5120 x 2048, 8 bits: 168 us, so 165).
+  template <int J, int PIECES, typename P>
+  __device__ __forceinline__ void product(const Parts& f, const Scales& s, v16f (&o)[FT][FN], P piece) const {
+    each<0, FT * FN>([&](auto I) {
+      constexpr int i = I(), t = i / FN, n = i % FN, M = FT * FN - 1;
+      o[t][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.q[n], f.p[t], o[t][n], kFp4, kOperand<FMT>,
+                                                                2 * J, (int)s.q[n], 2 * J, (int)s.p[t]);
+      if constexpr (i < M) each<PIECES * i / M, PIECES * (i + 1) / M>(piece);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   }
 };
 
@@ -452,17 +480,20 @@ __global__ __launch_bounds__(64 * WT * WN) void k_mx_gemm(LinearArgs a, int tile
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  // Step ks: its first half's operands and its scales are there.
+  // Step ks: its first half's operands and its scales are there, or on their way.
   const auto turn = [&](int ks, uint8_t* now, uint8_t* next) {
-    m.parts(now, 1, f1);
-    m.template product<0>(f0, sc, o);
+    const typename G::Step ahead = m.step(ks + 3);
+    m.shift(sc);
+    m.template product<0, FN + FT>(f0, sc, o, [&](auto i) { m.part(now, 1, f1, i()); });
     wait_loads<G::PER>();  // the next step's, of those that are on their way
     meet();
-    m.load(now, ks + 3);
     typename G::Scales after;  // (behind the last step: of nothing that is used)
-    m.scales_of(next, after);
-    m.parts(next, 0, f0);
-    m.template product<1>(f1, sc, o);
+    m.template product<1, G::PER + 1 + FN + FT>(f1, sc, o, [&](auto i) {
+      constexpr int k = i() - G::PER - 1;
+      if constexpr (k < -1) m.load(ahead, now, i());
+      else if constexpr (k == -1) m.scales_of(next, after);
+      else m.part(next, 0, f0, k);
+    });
     sc = after;
   };
   m.load(b0, 0);
@@ -471,7 +502,8 @@ __global__ __launch_bounds__(64 * WT * WN) void k_mx_gemm(LinearArgs a, int tile
   wait_loads<2 * G::PER>();
   meet();
   m.scales_of(b0, sc);
-  m.parts(b0, 0, f0);
+#pragma unroll
+  for (int i = 0; i < FN + FT; ++i) m.part(b0, 0, f0, i);
 #pragma unroll 1
   for (int ks = 0; ks < steps; ks += 3) {
     turn(ks, b0, b1);
@@ -545,15 +577,21 @@ void linear(const LinearArgs& a, hipStream_t stream) {
     return;
   }
   // The tile whose rounds over the 256 CUs take the least, with the time of a round of each
-  // kind as measured (8 bits, K 4096: 64 us of 256 x 256, 38 of 128 x 256, 26 of 128 x 128, 16
-  // of 64 x 128).  16384 x 5120 x 2048: 170, 205, 220, 254 us; 4096 rows 58, 53, 56, 64; 1024
-  // rows 30, 18, 23, 21; 2048 x 2048 x 4096 55, 32, 26, 27; 256 x 5120 x 2048 28, 16, 14, 9.5.
+  // kind as measured (8 bits, K 4096: 60 us of 256 x 256, 38 of 128 x 256, 26 of 128 x 128, 15
+  // of 64 x 128).  8 bits, tiles in that order: 16384 x 5120 x 2048 167, 206, 217, 249 us; 4096
+  // rows 54, 54, 55, 63; 1024 rows 29, 17, 23, 22; 2048 x 2048 x 4096 54, 32, 26, 26; 256 x
+  // 5120 x 2048 28, 16, 14, 9.5.
   const auto rounds = [&](int bt, int bn) {
     return (((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn) + 255) / 256;
   };
   const int64_t cost[4] = {100 * rounds(256, 256), 60 * rounds(128, 256), 41 * rounds(128, 128), 26 * rounds(64, 128)};
   switch (std::min_element(cost, cost + 4) - cost) {
-    case 0: launch_gemm<FMT, 2, 4, 4, 2>(a, stream); break;
+    case 0:
+      // (8-bit rows: a wave reads 64 of them and 128 outputs, not 128 and 64, a fifth less of
+      // LDS: 171 us, so 167)
+      if constexpr (FMT == MOE_FMT_MXFP8) launch_gemm<FMT, 4, 2, 2, 4>(a, stream);
+      else launch_gemm<FMT, 2, 4, 4, 2>(a, stream);
+      break;
     case 1: launch_gemm<FMT, 2, 4, 2, 2>(a, stream); break;
     case 2: launch_gemm<FMT, 2, 2, 2, 2>(a, stream); break;
     default: launch_gemm<FMT, 1, 4, 2, 1>(a, stream);
