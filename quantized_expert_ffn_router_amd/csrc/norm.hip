@@ -8,7 +8,11 @@
 // codes must not hang on the order of a sum, so the norm is in fp64 (as many fp64 as
 // plain fp32 operations run per cycle here); the codes are those of z.
 //
-// Bound by memory.
+// Bound by memory: 16384 rows of 2048 with a residual, both 16-bit outputs and 8-bit codes
+// 55 us (5.5 TB/s, above a large copy's 4.9), 16384 rows of 4096 into 8 bits 36 us (5.6); 8
+// rows are a launch, 2.4 and 1.7 us in a graph.  A row to a workgroup's waves, as many as
+// hold it 16 or 32 bytes a lane: no loop over rows, in which the loads of the next row would
+// take the registers that the widened values need (155 us, with spills).
 #include <algorithm>
 
 #include "mx.h"
