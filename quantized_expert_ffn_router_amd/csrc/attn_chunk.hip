@@ -473,7 +473,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
   const uint16_t* qp = a.q + at * a.q_stride + (int64_t)head * D + 8 * (lane >> 5);
 #pragma unroll
   for (int s = 0; s < KS; ++s) w.qf[s] = *reinterpret_cast<const v4u*>(qp + 16 * s);
-  const float c_log2 = DECODED ? a.scale_log2 * w.halve() : a.scale_log2;
+  // (above 0, where masked scores, -inf, would become NaN; scores that far down are 0)
+  const float c_log2 = DECODED ? fmaxf(a.scale_log2 * w.halve(), 0x1p-126f) : a.scale_log2;
   w.places(lane);
   w.clear();
   // last token that some row of the wave sees

@@ -250,3 +250,16 @@ def test_chunk_steps_of_attention_forward(fmt):
     e_kv = 2.0 ** -8 if fmt == Q8_0 else 0.0
     w = 2.0 ** -7 + e_kv + 2 * math.expm1(D ** 0.5 * 1.02 * (D * 2.0 ** -24 + e_kv)) + 2.0 ** -20 + 150 * 2.0 ** -24
     assert ((one - two).abs() <= 2 * (w + 2.0 ** -8 * (1 + w)) * v).all()
+
+
+def test_a_step_without_rows_changes_nothing():
+    m = Model(NVFP4, MXFP8)
+    x = torch.zeros(4, H, dtype=torch.bfloat16, device=dev)
+    for chunk in (False, True):
+        q.attention_forward(m.caches[0], m.attn, m.buf.qkv, 0, 0.125, chunk=chunk)
+    pool, m.buf.qkv[:] = m.caches[0].pool.clone(), 7.0
+    q.moe_add_norm(H, 0, x, H, None, 0, m.blocks[0].attn_norm, 1e-5, None, 0, x, H)
+    q.moe_mx_linear_rows(m.blocks[0].out.mat, MXFP8, m.attn.out, m.n_q * m.D, 0, m.buf.qkv, m.buf.qkv.shape[1],
+                         q.MOE_DTYPE_BF16, m.buf.ws, m.buf.ws_bytes)
+    torch.cuda.synchronize()
+    assert torch.equal(m.caches[0].pool, pool) and (m.buf.qkv == 7.0).all() and (x == 0).all()

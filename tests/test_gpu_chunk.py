@@ -350,3 +350,82 @@ def test_chunk_in_a_captured_graph_and_on_another_stream():
     for i in (1, 3, 0, 2, 1):
         assert torch.equal(run(graph.replay, i), want[i]), i
         assert torch.equal(run(call, (i + 1) % 4), want[(i + 1) % 4])
+
+
+# ------------------------------------------------------------------ the ends of the ranges
+
+@pytest.mark.parametrize("fmt,G,D,lens,rows", [(NVFP4, 96, 128, [70, 33], [5, 1]), (Q8_0, 300, 64, [100, 3], [3, 2]),
+                                               (BF16, 1024, 64, [66, 1], [2, 1]), (NVFP4, 130, 256, [40], [3])])
+def test_chunk_groups_wider_than_a_tile(fmt, G, D, lens, rows):
+    """A tile ends within a row's heads; in place, too."""
+    s = Setup(fmt, 1, D, 32, lens, rows, seed=G)
+    qv = ref.bf16_bits(1.5 * s.rng.standard_normal((s.T, G * D)))
+    for m in (None, 1, 1 << 20):
+        got = run_chunk(s, G, qv, max_len=m)
+        check_chunk(s, G, qv, got)
+    end = int(s.start[-1])
+    assert np.array_equal(run_chunk(s, G, qv, max_len=1 << 20, out="q")[:end], got[:end])
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+@pytest.mark.parametrize("B", [64, 65, 150])
+def test_chunk_of_many_sequences(fmt, B):
+    """More sequences than lanes, some without rows, some without tokens."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(0, 90, B)]
+    rows = [int(n) for n in rng.integers(0, 4, B)]
+    lens[B - 1], rows[B - 1], lens[3] = 400, 40, 0
+    s = Setup(fmt, 1, 64, 32, lens, rows, seed=B)
+    qv = ref.bf16_bits(s.rng.standard_normal((s.T, 3 * 64)))
+    for m in (None, 1, 1 << 20):
+        print("sequences", FMT[fmt], B, m, flush=True)
+        got = run_chunk(s, 3, qv, max_len=m)
+        check_chunk(s, 3, qv, got)
+        assert (got[int(s.start[-1]):] == ref.bf16_bits([7.0])[0]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunk_values_at_the_end_of_fp16(D):
+    """Q8_0 values up to 65024, whose scale is 512, in tokens that some rows do not see: those are
+    as if the token were not there, and the others right."""
+    s = Setup(Q8_0, 1, D, 32, [150, 45], [40, 1], seed=5)
+    qv = ref.bf16_bits(s.rng.standard_normal((s.T, 4 * D)))
+    before = run_chunk(s, 4, qv)
+    x = np.zeros(D)
+    x[17], x[40] = 65024.0, -6e4
+    s.ref.put(1, s.table[0, 130 // 32], 130 % 32, 0, ref.bf16_bits(x))
+    s.ref.put(1, s.table[0, 2], 7, 0, ref.bf16_bits(s.rng.standard_normal(D) * 2e4))
+    s.to_device()
+    got = run_chunk(s, 4, qv)
+    check_chunk(s, 4, qv, got)
+    assert np.isfinite(ref.bf16_val(got[:41])).all() and np.array_equal(got[40], before[40])
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+def test_chunk_queries_near_nothing(fmt):
+    """Queries far below one, of zero, and a cache's small scale: rows still see only their own."""
+    s = Setup(fmt, 2, 128, 32, [100, 70], [40, 3], seed=6, k_ts=1e-30 if fmt == NVFP4 else 1.0)
+    qv = ref.bf16_bits(1e-36 * s.rng.standard_normal((s.T, 4 * 128)))
+    qv[5] = 0
+    got = run_chunk(s, 4, qv)
+    check_chunk(s, 4, qv, got)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, Q8_0, BF16], ids=FMT.get)
+def test_chunk_pages_beyond_32_bit_offsets(fmt):
+    """A pool of more than 4 GiB: the same answers from its last pages as from a small one's."""
+    n_kv, D, P, n_q = 8, 256, 256, 8
+    far = (1 << 32) // q.moe_kv_page_bytes(fmt, n_kv, D, P) + 3
+    qkv = torch.randn(600, (n_q + 2 * n_kv) * D, generator=torch.Generator(device=dev).manual_seed(6), device=dev).bfloat16()
+    got = []
+    for n_pages, pages in ((3, [2, 0, 1]), (far, [far - 1, far - 3, far - 2])):
+        print("pool", FMT[fmt], n_pages, flush=True)
+        cache = q.KvCache(fmt, n_q, n_kv, D, P, n_pages)
+        buf = q.AttnBuffers(cache, 1, 600, 3, chunk=True)
+        buf.page_table.copy_(i32([pages]))
+        buf.row_start.copy_(i32([0, 600]))
+        buf.kv_len.copy_(i32([600]))
+        got.append(q.attention_forward(cache, buf, qkv, 600, 1 / 16, chunk=True).clone())
+        torch.cuda.synchronize()
+        del cache, buf
+    assert torch.isfinite(got[0].float()).all() and torch.equal(*got)
