@@ -332,6 +332,10 @@ struct Gemm {
   int wave, lane, r, h, wt, wn, scale_step;
   uint32_t at[PER];
 
+  // What the chunks of a row are permuted by in LDS.
+  __device__ __forceinline__ static int place(int row) {
+    return FMT == MOE_FMT_MXFP8 ? (row >> 1) & 7 : (row >> 2) & 3;
+  }
   __device__ __forceinline__ Gemm(const LinearArgs& args, int64_t t0, int tile0, int w) : a(args), wave(w), lane(lane_id()) {
     r = lane & 31;
     h = lane >> 5;
@@ -347,12 +351,17 @@ struct Gemm {
     for (int i = 0; i < PER - 1; ++i) {
       const int u = i * WAVES + wave;
       if (i < NA / WAVES) {
-        // 8 bits: 8 rows of 8 chunks, the chunks of every other 8 rows swapped in pairs,
-        // so that 16 lanes read all banks; 4 bits: 16 rows of 4 chunks
-        if constexpr (FMT == MOE_FMT_MXFP8)
-          at[i] = (uint32_t)((u * 8 + (lane & 7)) * pitch + (((lane >> 3) ^ (u & 1)) * 16));
-        else
-          at[i] = (uint32_t)((u * 16 + (lane & 15)) * pitch + (lane >> 4) * 16);
+        // 8 bits: 8 rows of 8 chunks of 16 bytes, 4 bits: 16 rows of 4.  Neighbouring lanes
+        // take chunks of one row, permuted so that 16 rows' reads of a chunk meet all banks.
+        // (Lanes of different rows are looked up one by one: 64 x 2048 x 4096 of 8 bits 13.7
+        // us, so 9.0; 8192 rows 58, so 53.)
+        if constexpr (FMT == MOE_FMT_MXFP8) {
+          const int row = u * 8 + (lane >> 3);
+          at[i] = (uint32_t)(row * pitch + ((lane & 7) ^ place(row)) * 16);
+        } else {
+          const int row = u * 16 + (lane >> 2);
+          at[i] = (uint32_t)(row * pitch + ((lane & 3) ^ place(row)) * 16);
+        }
       } else {
         at[i] = (uint32_t)((u - NA) * a.steps * 1024 + lane * 16);
       }
@@ -394,9 +403,9 @@ struct Gemm {
     if constexpr (FMT == MOE_FMT_MXFP8) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        q[k] = *reinterpret_cast<const v4u*>(lds + OA + (row >> 3) * 1024 + (((4 * j + 2 * k + h) ^ ((row >> 3) & 1)) * 128) + (row & 7) * 16);
+        q[k] = *reinterpret_cast<const v4u*>(lds + OA + row * 128 + ((4 * j + 2 * k + h) ^ place(row)) * 16);
     } else {
-      q[0] = *reinterpret_cast<const v4u*>(lds + OA + (row >> 4) * 1024 + (2 * j + h) * 256 + (row & 15) * 16);
+      q[0] = *reinterpret_cast<const v4u*>(lds + OA + row * 64 + ((2 * j + h) ^ place(row)) * 16);
     }
     v8i v;
 #pragma unroll
@@ -446,7 +455,7 @@ struct Gemm {
   template <int J, int PIECES, typename P>
   __device__ __forceinline__ void product(const Parts& f, const Scales& s, v16f (&o)[FT][FN], P piece) const {
     each<0, FT * FN>([&](auto I) {
-      constexpr int i = I(), t = i / FN, n = i % FN, M = FT * FN - 1;
+      constexpr int i = I(), t = i / FN, n = i % FN, M = FT * FN > 1 ? FT * FN - 1 : 1;
       o[t][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.q[n], f.p[t], o[t][n], kFp4, kOperand<FMT>,
                                                                 2 * J, (int)s.q[n], 2 * J, (int)s.p[t]);
       if constexpr (i < M) each<PIECES * i / M, PIECES * (i + 1) / M>(piece);
@@ -595,8 +604,9 @@ void linear(const LinearArgs& a, hipStream_t stream) {
   const auto rounds = [&](int bt, int bn) {
     return (((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn) + 255) / 256;
   };
-  const int64_t cost[4] = {100 * rounds(256, 256), 60 * rounds(128, 256), 41 * rounds(128, 128), 26 * rounds(64, 128)};
-  switch (std::min_element(cost, cost + 4) - cost) {
+  const int64_t cost[5] = {100 * rounds(256, 256), 60 * rounds(128, 256), 41 * rounds(128, 128), 26 * rounds(64, 128),
+                           20 * rounds(64, 64)};
+  switch (std::min_element(cost, cost + 5) - cost) {
     case 0:
       // (8-bit rows: a wave reads 64 of them and 128 outputs, not 128 and 64, a fifth less of
       // LDS: 171 us, so 167)
@@ -605,7 +615,8 @@ void linear(const LinearArgs& a, hipStream_t stream) {
       break;
     case 1: launch_gemm<FMT, 2, 4, 2, 2>(a, stream); break;
     case 2: launch_gemm<FMT, 2, 2, 2, 2>(a, stream); break;
-    default: launch_gemm<FMT, 1, 4, 2, 1>(a, stream);
+    case 3: launch_gemm<FMT, 1, 4, 2, 1>(a, stream); break;
+    default: launch_gemm<FMT, 2, 2, 1, 1>(a, stream);
   }
 }
 
