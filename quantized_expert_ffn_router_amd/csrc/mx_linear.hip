@@ -312,11 +312,11 @@ void launch_few(const LinearArgs& a, hipStream_t stream) {
 // are in registers by then, those of the next step's first half are read beside it, so
 // that the matrix units do not wait for LDS.
 //
-// 16384 x 5120 x 2048 of 8-bit rows 165 us (2.1 PFLOP/s), of 4-bit rows 134 (2.6); 8192 x
-// 2048 x 4096 58.6 and 41.4 (2.3 and 3.3), where a bf16 library product reaches 1.2.  The
-// matrix units are 47 % busy at 2.07 GHz.  Codes that are all zero take 14 % less (power);
-// steps whose loads read nothing, a quarter less than that: the way into LDS beside the
-// reads of it, a third of LDS's cycles, and the barrier that both wait at.
+// 16384 x 5120 x 2048 of 8-bit rows 154 to 158 us (2.2 PFLOP/s), of 4-bit rows 130 (2.6); 8192
+// x 2048 x 4096 53 and 40.5 (2.6 and 3.4), where a bf16 library product reaches 1.2.  The
+// matrix units are half of the time busy at the 2.1 GHz they hold: codes that are all zero
+// took 14 % less (power), steps whose loads read nothing a quarter less than that: loads into
+// LDS beside the reads of it.  Two groups of waves that take every other step: no gain.
 template <int FMT, int WT, int WN, int FT, int FN>
 struct Gemm {
   static constexpr int WAVES = WT * WN, BT = WT * FT * 32, BN = WN * FN * 32;
@@ -597,15 +597,15 @@ void linear(const LinearArgs& a, hipStream_t stream) {
     return;
   }
   // The tile whose rounds over the 256 CUs take the least, with the time of a round of each
-  // kind as measured (8 bits, K 4096: 60 us of 256 x 256, 38 of 128 x 256, 26 of 128 x 128, 15
-  // of 64 x 128).  8 bits, tiles in that order: 16384 x 5120 x 2048 167, 206, 217, 249 us; 4096
-  // rows 54, 54, 55, 63; 1024 rows 29, 17, 23, 22; 2048 x 2048 x 4096 54, 32, 26, 26; 256 x
-  // 5120 x 2048 28, 16, 14, 9.5.
-  const auto rounds = [&](int bt, int bn) {
-    return (((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn) + 255) / 256;
-  };
-  const int64_t cost[5] = {100 * rounds(256, 256), 60 * rounds(128, 256), 41 * rounds(128, 128), 26 * rounds(64, 128),
-                           20 * rounds(64, 64)};
+  // kind as measured (8 bits, K 4096: 39 us of 256 x 256, 24 of 128 x 256, 17 of 128 x 128, 12
+  // of 64 x 128); 64 x 64 where tiles of 64 x 128 leave half of the CUs without (it reads
+  // more).  8 bits, tiles in that order: 16384 x 5120 x 2048 154, 183, 176, 197, 260 us; 4096
+  // rows 50, 43, 43, 48, 63; 1024 rows 24, 15, 16, 15, 19; 2048 x 2048 x 4096 40, 25, 20, 20,
+  // 26; 256 x 5120 x 2048 23, 14, 10, 7.8, 8.9; 64 rows 21, 13, 9.5, 6.6, 5.9.
+  const auto tiles = [&](int bt, int bn) { return ((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn); };
+  const auto rounds = [&](int bt, int bn) { return (tiles(bt, bn) + 255) / 256; };
+  const int64_t cost[5] = {100 * rounds(256, 256), 62 * rounds(128, 256), 43 * rounds(128, 128), 30 * rounds(64, 128),
+                           tiles(64, 128) < 128 ? 27 : INT64_MAX};
   switch (std::min_element(cost, cost + 5) - cost) {
     case 0:
       // (8-bit rows: a wave reads 64 of them and 128 outputs, not 128 and 64, a fifth less of
