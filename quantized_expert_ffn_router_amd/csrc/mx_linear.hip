@@ -136,72 +136,68 @@ __device__ __forceinline__ void store_4(const LinearArgs& a, int64_t t, int n, v
 
 // ------------------------------------------------------------------ few rows
 
-// Up to NT * 16 rows.  A tile of 16 outputs a workgroup at a time, its waves taking KS
+// Up to 16 rows.  A tile of 16 outputs a workgroup at a time, its waves taking KS
 // steps of K each (in several passes, if K is longer) and adding up in LDS; the next
 // tile's weights are on their way while one is worked on.  The rows' codes stay in
 // registers while there is one pass; ROWS: they are made here from 16-bit rows.
-template <int FMT, bool ROWS, int NT, int KS>
-__global__ __launch_bounds__(NT == 1 ? 1024 : 512) void k_mx_few(LinearArgs a, int passes) {
-  extern __shared__ v4f part[];  // [2][waves][NT][64]
+template <int FMT, bool ROWS, int KS>
+__global__ __launch_bounds__(1024) void k_mx_few(LinearArgs a, int passes) {
+  extern __shared__ v4f part[];  // [2][waves][64]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int lane = lane_id(), r = lane & 15, g = lane >> 4;
-  v8i b[NT][KS];
-  int bs[NT][KS];
+  v8i b[KS];
+  int bs[KS];
 
   const auto rows = [&](int pass) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int64_t t = n * 16 + r;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int ks = (pass * waves + wave) * KS + s;
-        const bool in = t < a.T && ks < a.steps;
-        v4u q[2] = {v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}};
-        uint32_t sc = 0;
-        if constexpr (!ROWS) {
-          if (in) {
-            const uint8_t* p = a.codes + t * mx_bytes<FMT>(a.K) + mx_bytes<FMT>(ks * kMxStep) + 16 * g;
-            q[0] = *reinterpret_cast<const v4u*>(p);
-            if constexpr (FMT == MOE_FMT_MXFP8) q[1] = *reinterpret_cast<const v4u*>(p + 64);
-            sc = a.scales[t * (a.K / kMxBlock) + ks * 4 + g];
-          }
-        } else {
-          // 32 elements: those of block g, or 16 of each half
-          uint4 x[4];
-          const uint16_t* p = a.x + t * a.x_stride + ks * kMxStep + (FMT == MOE_FMT_MXFP4 ? 32 : 16) * g;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = in ? *reinterpret_cast<const uint4*>(p + 8 * i + (FMT == MOE_FMT_MXFP8 && i > 1 ? 48 : 0))
-                      : make_uint4(0, 0, 0, 0);
-          if constexpr (FMT == MOE_FMT_MXFP4) {
-            sc = mx_scale<FMT>(max(max(mx_top(x[0]), mx_top(x[1])), max(mx_top(x[2]), mx_top(x[3]))));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[0][i] = mx_codes<FMT>(x[i], sc).x;
-          } else {
-            // a block's other 16 elements are in the neighbouring lane group, and block
-            // g's scale in another
-            uint32_t s2[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t top = max(mx_top(x[2 * h]), mx_top(x[2 * h + 1]));
-              const auto m = __builtin_amdgcn_permlane16_swap(top, top, false, false);
-              s2[h] = mx_scale<FMT>(max((uint32_t)m[0], (uint32_t)m[1]));
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint2 c = mx_codes<FMT>(x[2 * h + i], s2[h]);
-                q[h][2 * i] = c.x;
-                q[h][2 * i + 1] = c.y;
-              }
-            }
-            const int from = (g & 1) * 32 + r;
-            const uint32_t s0 = __shfl((int)s2[0], from), s1 = __shfl((int)s2[1], from);
-            sc = g < 2 ? s0 : s1;
-          }
+    for (int s = 0; s < KS; ++s) {
+      const int ks = (pass * waves + wave) * KS + s;
+      const bool in = r < a.T && ks < a.steps;
+      v4u q[2] = {v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}};
+      uint32_t sc = 0;
+      if constexpr (!ROWS) {
+        if (in) {
+          const uint8_t* p = a.codes + (int64_t)r * mx_bytes<FMT>(a.K) + mx_bytes<FMT>(ks * kMxStep) + 16 * g;
+          q[0] = *reinterpret_cast<const v4u*>(p);
+          if constexpr (FMT == MOE_FMT_MXFP8) q[1] = *reinterpret_cast<const v4u*>(p + 64);
+          sc = a.scales[(int64_t)r * (a.K / kMxBlock) + ks * 4 + g];
         }
+      } else {
+        // 32 elements: those of block g, or 16 of each half
+        uint4 x[4];
+        const uint16_t* p = a.x + (int64_t)r * a.x_stride + ks * kMxStep + (FMT == MOE_FMT_MXFP4 ? 32 : 16) * g;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[n][s][i] = (int)q[i >> 2][i & 3];
-        bs[n][s] = (int)sc;
+        for (int i = 0; i < 4; ++i)
+          x[i] = in ? *reinterpret_cast<const uint4*>(p + 8 * i + (FMT == MOE_FMT_MXFP8 && i > 1 ? 48 : 0))
+                    : make_uint4(0, 0, 0, 0);
+        if constexpr (FMT == MOE_FMT_MXFP4) {
+          sc = mx_scale<FMT>(max(max(mx_top(x[0]), mx_top(x[1])), max(mx_top(x[2]), mx_top(x[3]))));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[0][i] = mx_codes<FMT>(x[i], sc).x;
+        } else {
+          // a block's other 16 elements are in the neighbouring lane group, and block
+          // g's scale in another
+          uint32_t s2[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t top = max(mx_top(x[2 * h]), mx_top(x[2 * h + 1]));
+            const auto m = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+            s2[h] = mx_scale<FMT>(max((uint32_t)m[0], (uint32_t)m[1]));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint2 c = mx_codes<FMT>(x[2 * h + i], s2[h]);
+              q[h][2 * i] = c.x;
+              q[h][2 * i + 1] = c.y;
+            }
+          }
+          const int from = (g & 1) * 32 + r;
+          const uint32_t s0 = __shfl((int)s2[0], from), s1 = __shfl((int)s2[1], from);
+          sc = g < 2 ? s0 : s1;
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[s][i] = (int)q[i >> 2][i & 3];
+      bs[s] = (int)sc;
     }
   };
 
@@ -222,9 +218,7 @@ __global__ __launch_bounds__(NT == 1 ? 1024 : 512) void k_mx_few(LinearArgs a, i
   int tile = blockIdx.x, pass = 0, turn = 0;
   weights(tile, 0);
   rows(0);
-  v4f o[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) o[n] = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f o = v4f{0.f, 0.f, 0.f, 0.f};
   while (true) {
     v4u c[KS];
     uint32_t cs[KS];
@@ -238,29 +232,24 @@ __global__ __launch_bounds__(NT == 1 ? 1024 : 512) void k_mx_few(LinearArgs a, i
       v8i m;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = i < 4 ? (int)c[s][i] : 0;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        o[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(m, b[n][s], o[n], kFp4, kOperand<FMT>, 0,
-                                                                (int)(cs[s] >> (8 * g)), 0, bs[n][s]);
+      o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(m, b[s], o, kFp4, kOperand<FMT>, 0,
+                                                           (int)(cs[s] >> (8 * g)), 0, bs[s]);
     }
     if (last) {
-      v4f* const p = part + turn * waves * NT * 64;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) p[(wave * NT + n) * 64 + lane] = o[n];
+      v4f* const p = part + turn * waves * 64;
+      p[wave * 64 + lane] = o;
       __syncthreads();
-      for (int i = threadIdx.x; i < NT * 64; i += blockDim.x) {
-        v4f sum = p[i];
-        for (int k = 1; k < waves; ++k) sum += p[k * NT * 64 + i];
-        const int64_t t = (i >> 6) * 16 + (i & 15);
-        const int n = tile * kMxTile + 4 * ((i & 63) >> 4);
+      if (wave == 0) {
+        v4f sum = p[lane];
+        for (int k = 1; k < waves; ++k) sum += p[k * 64 + lane];
+        const int n = tile * kMxTile + 4 * g;
         if (a.bias)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum[e] += n + e < a.N ? a.bias[n + e] : 0.0f;
-        if (t < a.T) store_4(a, t, n, sum);
+        if (r < a.T) store_4(a, r, n, sum);
       }
       turn ^= 1;  // (the other half is free once all have passed this barrier)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) o[n] = v4f{0.f, 0.f, 0.f, 0.f};
+      o = v4f{0.f, 0.f, 0.f, 0.f};
     }
     if (next >= a.tiles) break;
     tile = next;
@@ -270,19 +259,17 @@ __global__ __launch_bounds__(NT == 1 ? 1024 : 512) void k_mx_few(LinearArgs a, i
 }
 
 struct Few {
-  int nt, ks, waves, passes;
+  int ks, waves, passes;
 };
-// How a product of few rows is cut, by the steps of K and the tiles of N.  (N 5120, K 2048,
-// 8 bits: 16 rows 4.9 us, 32 rows 7.5; as tiles of 64 rows 7.0 and 7.1, and 64 rows 8.6
-// where this kernel took 13.)
-constexpr int64_t kFewRows = 32;
-Few few_of(int64_t T, int steps, int tiles) {
+// How a product of few rows is cut, by the steps of K and the tiles of N.  (5120 x 2048, 8 bits:
+// 16 rows 4.9 us; 17 as two tiles of 16 rows here 5.6, as a tile of 64 below 5.7, and 32 rows
+// 7.7 and 5.7; 32 x 20000 x 2048 17.7 and 8.1.)
+constexpr int64_t kFewRows = 16;
+Few few_of(int steps, int tiles) {
   Few f;
-  f.nt = T <= 16 ? 1 : 2;
-  const int most = f.nt == 1 ? 16 : 8;
-  // two steps of K a wave while the waves of a workgroup reach over all of it (20 x 30000 x
-  // 1024, 8 bits: 8.3 us, with four 12.7), four for many outputs of a longer K (5 x 100003 x
-  // 2048 20.9 us, with two 22.3)
+  const int most = 16;
+  // two steps of K a wave while the waves of a workgroup reach over all of it, four for many
+  // outputs of a longer K (5 x 100003 x 2048 20.9 us, with two 22.3)
   f.ks = steps <= 8 || (steps <= 2 * most && tiles < 1024) ? 2 : 4;
   f.waves = std::min((steps + f.ks - 1) / f.ks, most);
   f.passes = (steps + f.ks * f.waves - 1) / (f.ks * f.waves);
@@ -291,16 +278,14 @@ Few few_of(int64_t T, int steps, int tiles) {
 
 template <int FMT>
 void launch_few(const LinearArgs& a, hipStream_t stream) {
-  const Few f = few_of(a.T, a.steps, a.tiles);
+  const Few f = few_of(a.steps, a.tiles);
   // (what runs at once: 16 waves a CU)
   const unsigned grid = (unsigned)std::min(a.tiles, 256 * std::max(16 / f.waves, 1));
   const unsigned block = 64 * f.waves;
-  const size_t lds = (size_t)2 * f.waves * f.nt * 1024;
-  if (a.x) k_mx_few<FMT, true, 1, 2><<<grid, block, lds, stream>>>(a, f.passes);
-  else if (f.nt == 1 && f.ks == 2) k_mx_few<FMT, false, 1, 2><<<grid, block, lds, stream>>>(a, f.passes);
-  else if (f.nt == 1) k_mx_few<FMT, false, 1, 4><<<grid, block, lds, stream>>>(a, f.passes);
-  else if (f.ks == 2) k_mx_few<FMT, false, 2, 2><<<grid, block, lds, stream>>>(a, f.passes);
-  else k_mx_few<FMT, false, 2, 4><<<grid, block, lds, stream>>>(a, f.passes);
+  const size_t lds = (size_t)2 * f.waves * 1024;
+  if (a.x) k_mx_few<FMT, true, 2><<<grid, block, lds, stream>>>(a, f.passes);
+  else if (f.ks == 2) k_mx_few<FMT, false, 2><<<grid, block, lds, stream>>>(a, f.passes);
+  else k_mx_few<FMT, false, 4><<<grid, block, lds, stream>>>(a, f.passes);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -648,13 +633,13 @@ hipError_t launch_mx_pack(int N, int K, const uint8_t* codes, const uint8_t* sca
   return hipGetLastError();
 }
 
-// Up to 16 rows whose codes a workgroup's waves hold: each workgroup makes them again (16 x
-// 5120 x 2048, 8 bits: 6.2 us, where a launch of its own takes 1.8 beside the product's 4.9
-// and a gap; 32 rows 11.6 against 1.8 and 7.5; 5 x 100003 24.9 against 1.8 and 20.9).
+// Few rows whose codes a workgroup's waves hold: each workgroup makes them again (16 x 5120 x
+// 2048, 8 bits: 6.2 us, where a launch of its own takes 1.8 beside the product's 4.9 and a
+// gap; 5 x 100003 24.9 against 1.8 and 20.9).
 bool mx_linear_takes_rows(int64_t N, int64_t K, int64_t T) {
   const MxLayout l = mx_layout(N, K);
-  const Few f = few_of(T, (int)l.steps, (int)std::min(l.tiles, (int64_t)INT32_MAX));
-  return T <= 16 && f.ks == 2 && f.passes == 1;
+  const Few f = few_of((int)l.steps, (int)std::min(l.tiles, (int64_t)INT32_MAX));
+  return T <= kFewRows && f.ks == 2 && f.passes == 1;
 }
 
 hipError_t launch_mx_linear(const moe_mx_matrix* w, int fmt, const uint16_t* x, int64_t x_stride,
