@@ -700,12 +700,17 @@ class MxLinear:
         if not _launches_on(dev, stream):
             raise bad(f"weight is on {dev}, not the current GPU")
         self.N, self.K, self.device = N, K, dev
-        codes = weight
-        if scales is None:
+        self.packed = torch.empty(nb, dtype=torch.uint8, device=dev)
+        codes, quantise = weight, scales is None
+        if quantise:
             codes = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
             scales = torch.empty((N, K // 32), dtype=torch.uint8, device=dev)
+        # The current stream may still be writing weight, and using the memory that its allocator
+        # has just handed out again.
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream(dev))
+        if quantise:
             moe_mx_quant(MOE_FMT_MXFP4, K, N, weight, K, codes, scales, stream)
-        self.packed = torch.empty(nb, dtype=torch.uint8, device=dev)
         moe_mx_pack(N, K, codes, scales, self.packed, stream)
         torch.cuda.current_stream().synchronize() if stream is None else stream.synchronize()
         self.bias = bias

@@ -1,0 +1,47 @@
+"""In which order MxLinear launches, and on which stream: a CPU test with stand-ins for the streams
+and the calls."""
+import types
+
+import pytest
+import torch
+
+import quantized_expert_ffn_router_amd as q
+
+
+class Stream:
+    def __init__(self, name, log):
+        self.name, self.log, self.cuda_stream = name, log, id(self)
+
+    def wait_stream(self, other):
+        if other is not self:
+            self.log.append(f"{self.name} waits for {other.name}")
+
+    def synchronize(self):
+        self.log.append(f"host waits for {self.name}")
+
+
+@pytest.fixture
+def log(monkeypatch):
+    """What happens, in order; tensors stay on the CPU, where nothing is launched."""
+    out = []
+    current = Stream("current", out)
+    call = lambda name: lambda *a: out.append(f"{name} on {current.name if a[-1] is None else a[-1].name}")  # noqa: E731
+    monkeypatch.setattr(q, "_launches_on", lambda device, stream: True)
+    monkeypatch.setattr(q, "moe_mx_quant", call("quant"))
+    monkeypatch.setattr(q, "moe_mx_pack", call("pack"))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    return types.SimpleNamespace(out=out, current=current)
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_another_stream_waits_for_the_current_one(log, codes):
+    """The weights may still be written there, and the allocator's memory still be read."""
+    weight = torch.zeros(16, 64, dtype=torch.uint8) if codes else torch.zeros(16, 128, dtype=torch.bfloat16)
+    q.MxLinear(weight, torch.zeros(16, 4, dtype=torch.uint8) if codes else None, stream=Stream("side", log.out))
+    quant = [] if codes else ["quant on side"]
+    assert log.out == ["side waits for current", *quant, "pack on side", "host waits for side"]
+
+
+def test_without_a_stream_it_is_the_current_one(log):
+    q.MxLinear(torch.zeros(16, 128, dtype=torch.bfloat16))
+    assert log.out == ["quant on current", "pack on current", "host waits for current"]
