@@ -230,6 +230,17 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _stream_object(stream, device):
+    """torch's object for a stream that may be given as a raw handle, or None: the current one."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if not isinstance(stream, int):
+        return stream
+    # (torch takes a handle of 0 for no handle, and makes a stream)
+    return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+
+
 # ---------------------------------------------------------------- raw ABI
 
 def moe_abi_version() -> int:
@@ -463,7 +474,7 @@ class DeviceLayer:
         refs["tu"] = w.up_ts
         refs["td"] = w.down_ts if w.down_ts is not None else 1.0
         self.refs = t(refs.view(np.uint8))
-        torch.cuda.current_stream().synchronize() if stream is None else stream.synchronize()
+        _stream_object(stream, dev).synchronize()
         del canon
         self.desc = LayerDesc(self.E, self.k, self.H, self.I, MOE_FMT_NVFP4, self.fmt_down,
                               w.renormalize, ffn_mode, self.refs.data_ptr(), self.w_router.data_ptr(),
@@ -707,12 +718,12 @@ class MxLinear:
             scales = torch.empty((N, K // 32), dtype=torch.uint8, device=dev)
         # The current stream may still be writing weight, and using the memory that its allocator
         # has just handed out again.
-        if stream is not None:
-            stream.wait_stream(torch.cuda.current_stream(dev))
+        stream = _stream_object(stream, dev)
+        stream.wait_stream(torch.cuda.current_stream(dev))
         if quantise:
             moe_mx_quant(MOE_FMT_MXFP4, K, N, weight, K, codes, scales, stream)
         moe_mx_pack(N, K, codes, scales, self.packed, stream)
-        torch.cuda.current_stream().synchronize() if stream is None else stream.synchronize()
+        stream.synchronize()
         self.bias = bias
         self.mat = MxMatrix(N, K, self.packed.data_ptr(), None if bias is None else bias.data_ptr())
 

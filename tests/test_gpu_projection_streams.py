@@ -50,3 +50,14 @@ def test_memory_that_is_still_being_used():
     m = q.MxLinear(src, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(m.packed, want)
+
+
+def test_raw_handles():
+    src = rows(3)
+    want, side = plain(src), torch.cuda.Stream()
+    for handle in (side.cuda_stream, torch.cuda.current_stream().cuda_stream, 0):
+        weight = torch.zeros_like(src)
+        torch.cuda.synchronize()
+        keep_busy()
+        weight.copy_(src)
+        assert torch.equal(q.MxLinear(weight, stream=handle).packed, want)

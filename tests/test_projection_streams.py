@@ -1,10 +1,11 @@
-"""In which order MxLinear launches, and on which stream: a CPU test with stand-ins for the streams
-and the calls."""
+"""In which order MxLinear launches, and on which stream, and DeviceLayer's streams: a CPU test with
+stand-ins for the streams and the calls."""
 import types
 
 import pytest
 import torch
 
+import moegen
 import quantized_expert_ffn_router_amd as q
 
 
@@ -25,11 +26,13 @@ def log(monkeypatch):
     """What happens, in order; tensors stay on the CPU, where nothing is launched."""
     out = []
     current = Stream("current", out)
-    call = lambda name: lambda *a: out.append(f"{name} on {current.name if a[-1] is None else a[-1].name}")  # noqa: E731
+    call = lambda name: lambda *a: out.append(f"{name} on {(a[-1] or current).name}")  # noqa: E731
     monkeypatch.setattr(q, "_launches_on", lambda device, stream: True)
     monkeypatch.setattr(q, "moe_mx_quant", call("quant"))
     monkeypatch.setattr(q, "moe_mx_pack", call("pack"))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream("default", out))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(f"stream {handle}", out))
     return types.SimpleNamespace(out=out, current=current)
 
 
@@ -45,3 +48,18 @@ def test_another_stream_waits_for_the_current_one(log, codes):
 def test_without_a_stream_it_is_the_current_one(log):
     q.MxLinear(torch.zeros(16, 128, dtype=torch.bfloat16))
     assert log.out == ["quant on current", "pack on current", "host waits for current"]
+
+
+@pytest.mark.parametrize("handle,name", [(4096, "stream 4096"), (0, "default")])
+def test_raw_handles(log, handle, name):
+    """As every call takes them; 0 is the device's default stream."""
+    q.MxLinear(torch.zeros(16, 128, dtype=torch.bfloat16), stream=handle)
+    assert log.out == [f"{name} waits for current", f"quant on {name}", f"pack on {name}", f"host waits for {name}"]
+
+
+@pytest.mark.parametrize("handle,name", [(4096, "stream 4096"), (0, "default"), (None, "current")])
+def test_raw_handles_of_a_layer(log, monkeypatch, handle, name):
+    monkeypatch.setattr(q, "moe_pack_experts", lambda *a: log.out.append(a[-1]))
+    w = moegen.make_layer(moegen.Workload("streams", E=4, k=2, H=128, I=128, T=1))
+    q.DeviceLayer(w, device="cpu", stream=handle)
+    assert log.out == [handle, f"host waits for {name}"]
