@@ -624,12 +624,14 @@ def _check_rows(t, numel, device, name, call="attention_forward", other="the cac
 
 
 def _launches_on(device, stream):
-    """Whether a call's kernels run on this device: on the current one, if no
-    stream is given."""
+    """Whether a call's kernels run on this device: the stream's, or the current
+    one if no stream is given.  (A raw handle does not tell.)"""
     import torch
     if device.type != "cuda":
         return False
-    return stream is not None or device.index == torch.cuda.current_device()
+    if stream is None:
+        return device.index == torch.cuda.current_device()
+    return getattr(stream, "device", device) == device
 
 
 def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: float, prompt=None,
@@ -669,7 +671,7 @@ def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: floa
     if buf.q.device != dev:
         raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: buffers on {buf.q.device}, the cache on {dev}")
     if T > 0 and not _launches_on(dev, stream):
-        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: the cache is on {dev}, not the current GPU")
+        raise MoeError(MOE_ERR_INVALID_ARG, f"attention_forward: the cache is on {dev}, not the current GPU or the stream's")
     moe_kv_append(c, cache.qkv_desc, buf.seqs, qkv, qw + 2 * kw, T, None, buf.q, qw, buf.k, kw, stream)
     if chunk:
         moe_attn_chunk(c, buf.seqs, cache.n_q, buf.q, qw, T, max_len, scale, buf.out, qw, buf.ws,
@@ -709,7 +711,7 @@ class MxLinear:
                                  not bias.is_contiguous() or bias.device != dev):
             raise bad(f"bias must be float32 [{N}] on {dev}")
         if not _launches_on(dev, stream):
-            raise bad(f"weight is on {dev}, not the current GPU")
+            raise bad(f"weight is on {dev}, not the current GPU or the stream's")
         self.N, self.K, self.device = N, K, dev
         self.packed = torch.empty(nb, dtype=torch.uint8, device=dev)
         codes, quantise = weight, scales is None
@@ -792,7 +794,7 @@ def block_forward(w: BlockWeights, layer: DeviceLayer, cache: KvCache, buf: Bloc
             raise bad(f"the {name} are on {d}, the cache on {dev}")
     _check_rows(x, T * H, dev, "x", call)
     if T > 0 and not _launches_on(dev, stream):
-        raise bad(f"the cache is on {dev}, not the current GPU")
+        raise bad(f"the cache is on {dev}, not the current GPU or the stream's")
     moe_add_norm(H, T, x, H, None, 0, w.attn_norm, w.eps, None, 0, None, 0, w.fmt, buf.codes, buf.scales, stream)
     moe_mx_linear(w.qkv.mat, w.fmt, buf.codes, buf.scales, T, buf.qkv, width, MOE_DTYPE_BF16, stream)
     a = attention_forward(cache, attn, buf.qkv, T, scale, prompt, max_len, stream, chunk)

@@ -1,4 +1,4 @@
-"""In which order MxLinear launches, and on which stream, and DeviceLayer's streams: a CPU test with
+"""In which order MxLinear launches, and on which stream, and DeviceLayer's streams: CPU tests with
 stand-ins for the streams and the calls."""
 import types
 
@@ -63,3 +63,11 @@ def test_raw_handles_of_a_layer(log, monkeypatch, handle, name):
     w = moegen.make_layer(moegen.Workload("streams", E=4, k=2, H=128, I=128, T=1))
     q.DeviceLayer(w, device="cpu", stream=handle)
     assert log.out == [handle, f"host waits for {name}"]
+
+
+def test_a_stream_of_another_gpu():
+    """Its kernels would run there, on memory that may not be reachable from it."""
+    here = torch.device("cuda:0")
+    stream = lambda index: types.SimpleNamespace(cuda_stream=1, device=torch.device("cuda", index))  # noqa: E731
+    assert q._launches_on(here, stream(0)) and q._launches_on(here, 4096)
+    assert not q._launches_on(here, stream(1)) and not q._launches_on(torch.device("cpu"), stream(0))
