@@ -607,6 +607,7 @@ class AttnBuffers:
         self.ws_bytes = moe_attn_workspace_bytes(cache.desc, cache.n_q, n_seq, T_max, self.max_len)
         self.chunk_bytes = moe_attn_chunk_workspace_bytes(cache.desc, cache.n_q, n_seq, T_max, self.max_len) if chunk else None
         self.ws = torch.empty(max(self.ws_bytes, self.chunk_bytes or 0, 1), dtype=torch.uint8, device=dev)
+        self.spans = _spans(self.q, self.k, self.out, self.ws)
 
 
 def _check_rows(t, numel, device, name, call="attention_forward", other="the cache"):
@@ -621,6 +622,11 @@ def _check_rows(t, numel, device, name, call="attention_forward", other="the cac
         raise MoeError(MOE_ERR_INVALID_ARG, f"{call}: {name} has {t.numel()} elements of {numel}")
     if t.device != device:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{call}: {name} is on {t.device}, {other} on {device}")
+
+
+def _spans(*tensors):
+    """The addresses that contiguous tensors lie at: (first, past the last) of each."""
+    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors]
 
 
 def _launches_on(device, stream):
@@ -764,6 +770,7 @@ class BlockBuffers:
         self.qkv, self.proj, self.sum, self.z = bf16(w.qkv.N), bf16(w.H), bf16(w.H), bf16(w.H)
         self.ws_bytes = moe_mx_workspace_bytes(w.fmt, w.out.K, T_max)
         self.ws = u8(max(self.ws_bytes, 1))
+        self.spans = _spans(self.qkv, self.proj, self.ws)
 
 
 def block_forward(w: BlockWeights, layer: DeviceLayer, cache: KvCache, buf: BlockBuffers, attn: AttnBuffers,
@@ -771,8 +778,11 @@ def block_forward(w: BlockWeights, layer: DeviceLayer, cache: KvCache, buf: Bloc
                   **layer_options):
     """One layer from residual to residual over the step's rows x (bf16 [T][H]):
       a = attention_forward(qkv(norm(x))), h = x + out(a), h + layer_forward(norm(h)),
-    the norms' rows going to the projection as codes.  attn, prompt, max_len and
-    chunk as for attention_forward, step and layer_options as for layer_forward.
+    the norms' rows going to the projection as codes.  x is read twice: it may
+    be step.out (a layer's rows from the one before), but not lie in a buffer that
+    the step writes in between (buf.qkv, proj and ws, attn's, prompt's k and v).
+    attn, prompt, max_len and chunk as for attention_forward, step and
+    layer_options as for layer_forward.
     Returns step.out (bf16 bits [T_max][H]; the first T rows are the step's)."""
     call = "block_forward"
     bad = lambda msg: MoeError(MOE_ERR_INVALID_ARG, f"{call}: {msg}")  # noqa: E731
@@ -793,6 +803,11 @@ def block_forward(w: BlockWeights, layer: DeviceLayer, cache: KvCache, buf: Bloc
         if d != dev:
             raise bad(f"the {name} are on {d}, the cache on {dev}")
     _check_rows(x, T * H, dev, "x", call)
+    lo = _ptr(x)
+    hi = lo + 2 * T * H
+    for a, b in buf.spans + attn.spans + ([] if prompt is None else _spans(*prompt[2:])):
+        if a < hi and lo < b:
+            raise bad("x lies in a buffer that the step writes before it reads x again")
     if T > 0 and not _launches_on(dev, stream):
         raise bad(f"the cache is on {dev}, not the current GPU or the stream's")
     moe_add_norm(H, T, x, H, None, 0, w.attn_norm, w.eps, None, 0, None, 0, w.fmt, buf.codes, buf.scales, stream)
