@@ -30,35 +30,11 @@ namespace moe {
 
 namespace {
 
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-
 #if defined(__HIP_DEVICE_COMPILE__)  // (the host pass does not know the builtins)
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 #else
 typedef const void* Rsrc;
 #endif
-
-__device__ __forceinline__ uint32_t bits(v2h v) { return __builtin_bit_cast(uint32_t, v); }
-__device__ __forceinline__ v2h halves(uint32_t w) { return __builtin_bit_cast(v2h, w); }
-__device__ __forceinline__ v2h fp4_pair(uint32_t w, int k) {  // byte k: two E2M1 codes
-  switch (k) {
-    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
-    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
-    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
-    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
-  }
-}
-__device__ __forceinline__ v2h fp8_pair(uint32_t w, int k) {  // half-word k: two E4M3 scales
-  return k ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
-           : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
-}
-// int8 codes 2k, 2k + 1 of a word whose sign bits are flipped: byte b + 128 under the
-// exponent byte of 1024 is 1024 + 128 + b in fp16, exactly.
-__device__ __forceinline__ v2h i8_pair(uint32_t biased, int k) {
-  const uint32_t w = __builtin_amdgcn_perm(0x64646464u, biased, k ? 0x07030702u : 0x05010400u);
-  const v2h c = {(_Float16)1152.0f, (_Float16)1152.0f};
-  return halves(w) - c;
-}
 
 // Place of 16-byte chunk `chunk` (2 elements of 4 tokens) of a quad's values in LDS:
 // permuted within 16 chunks so that neither the 16 lanes of a write, whose chunks lie
@@ -523,13 +499,14 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
     __syncthreads();
   };
 
-      const auto is_wild = [&](const uint8_t* vt, const int* found) {
-        if constexpr (!DECODED) return wild<D>(vt, lane);
-        int any = 0;
-  #pragma unroll
-        for (int i = 0; i < W; ++i) any |= found[i];
-        return any != 0;
-      };
+  // Whether a tile of values holds an infinity or a NaN.
+  const auto is_wild = [&](const uint8_t* vt, const int* found) {
+    if constexpr (!DECODED) return wild<D>(vt, lane);
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) any |= found[i];
+    return any != 0;
+  };
   bool some_wild = false;
   typedef Codes<FMT, D, W> C;
   const auto put_all = [&](const C& c, uint8_t* kt, uint8_t* vt) {

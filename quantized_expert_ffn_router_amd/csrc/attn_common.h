@@ -12,18 +12,37 @@
 #include <type_traits>
 
 #include "gate_common.h"
+#include "pairs.h"
 
 namespace moe {
 
 constexpr float kNone = -3.0e38f;  // running maximum before any token
 constexpr float kGrow = 8.0f;      // log2 headroom before the accumulators are rescaled
 
-// Two values as bf16, rounded to nearest even.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
-  const v2b r = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, r);
+// The cache's codes and scales as fp16, two at a time.
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v2h fp4_pair(uint32_t w, int k) {  // byte k: two E2M1 codes
+  switch (k) {
+    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
+  }
 }
+__device__ __forceinline__ v2h fp8_pair(uint32_t w, int k) {  // half-word k: two E4M3 scales
+  return k ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
+           : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
+}
+// int8 codes 2k, 2k + 1 of a word whose sign bits are flipped: byte b + 128 under
+// the exponent byte of 1024 is 1024 + 128 + b in fp16, exactly; one packed
+// subtraction leaves b.
+__device__ __forceinline__ v2h i8_pair(uint32_t biased, int k) {
+  const uint32_t w = __builtin_amdgcn_perm(0x64646464u, biased, k ? 0x07030702u : 0x05010400u);
+  const v2h c = {(_Float16)1152.0f, (_Float16)1152.0f};
+  return __builtin_bit_cast(v2h, w) - c;
+}
+__device__ __forceinline__ uint32_t bits(v2h v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ v2h halves(uint32_t w) { return __builtin_bit_cast(v2h, w); }
 
 // Byte offsets inside one (page, head) block; head = bytes of the block.
 struct KvLayout {

@@ -28,7 +28,6 @@ namespace moe {
 
 namespace {
 
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -45,28 +44,6 @@ constexpr int kStreamed = 2;         // cache policy of loads that are read once
 // weights have fp32's exponents.
 template <int FMT>
 constexpr float kRaise = FMT == MOE_FMT_BF16 ? 0.0f : 7.0f;
-
-__device__ __forceinline__ v2h fp4_pair(uint32_t w, int k) {  // byte k: two E2M1 codes
-  switch (k) {
-    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
-    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
-    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
-    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
-  }
-}
-__device__ __forceinline__ v2h fp8_pair(uint32_t w, int k) {  // half-word k: two E4M3 scales
-  return k ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
-           : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
-}
-// int8 codes: byte b + 128 under the exponent byte of 1024 is 1024 + 128 + b
-// in fp16, exactly; one packed subtraction leaves b.
-__device__ __forceinline__ v2h i8_pair(uint32_t biased, int k) {
-  const uint32_t w = __builtin_amdgcn_perm(0x64646464u, biased, k ? 0x07030702u : 0x05010400u);
-  const v2h c = {(_Float16)1152.0f, (_Float16)1152.0f};
-  return __builtin_bit_cast(v2h, w) - c;
-}
-__device__ __forceinline__ uint32_t bits(v2h v) { return __builtin_bit_cast(uint32_t, v); }
-__device__ __forceinline__ v2h halves(uint32_t w) { return __builtin_bit_cast(v2h, w); }
 
 // max / sum over the four 16-lane groups (a query row's lanes).
 __device__ __forceinline__ float groups_max(float v) {

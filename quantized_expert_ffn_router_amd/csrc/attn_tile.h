@@ -49,7 +49,6 @@ __device__ __forceinline__ void wait_loads() {
 template <bool HALF>
 __device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
   typedef __bf16 v2b __attribute__((ext_vector_type(2)));
-  typedef _Float16 v2h __attribute__((ext_vector_type(2)));
   if constexpr (HALF) {
     const v2h w = {(_Float16)a, (_Float16)b}, one = {(_Float16)1.0f, (_Float16)1.0f};
     *l = __builtin_amdgcn_fdot2(w, one, *l, false);
@@ -59,16 +58,6 @@ __device__ __forceinline__ uint32_t weight_pair(float a, float b, float* l) {
   const v2b one = {(__bf16)1.0f, (__bf16)1.0f};
   *l = __builtin_amdgcn_fdot2_f32_bf16(w, one, *l, false);
   return __builtin_bit_cast(uint32_t, w);
-}
-
-// f of the numbers I .. N - 1, each as a type: where more code depends on the number than a
-// loop's unrolling takes.
-template <int I, int N, typename F>
-__device__ __forceinline__ void each(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>());
-    each<I + 1, N>(f);
-  }
 }
 
 // What a wave carries for 32 query rows: a lane column is one row, its accumulators and

@@ -8,7 +8,7 @@
 // codes are the only rounding.
 #pragma once
 
-#include "common.h"
+#include "pairs.h"
 
 namespace moe {
 

@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t load_4(Rsrc r, uint32_t at, uint32_t base) {
 // the instruction itself: with the builtin the compiler, which does not tell the turns of a
 // ring of buffers apart at the head of their loop, waits there for every load (256 rows, K
 // 4096, 8 bits: 17.7 us, so 14.8).  It has no output but LDS; who reads that waits with
-// wait_loads and a barrier.
+// wait_loads_and_reads and a barrier.
 template <int N>
 __device__ __forceinline__ void load_lds(Rsrc r, uint8_t* lds, uint32_t at, uint32_t base) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -81,26 +81,11 @@ __device__ __forceinline__ void load_lds(Rsrc r, uint8_t* lds, uint32_t at, uint
 }
 // Waits until at most N of the wave's loads are on their way, and for all its LDS reads.
 template <int N>
-__device__ __forceinline__ void wait_loads() {
+__device__ __forceinline__ void wait_loads_and_reads() {
 #if defined(__HIP_DEVICE_COMPILE__)
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
 #endif
 }
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
-  const v2b r = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, r);
-}
-
-// f of the numbers I .. N - 1, each as a type.
-template <int I, int N, typename F>
-__device__ __forceinline__ void each(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>());
-    each<I + 1, N>(f);
-  }
-}
-
 struct LinearArgs {
   const uint8_t* w;         // packed codes
   const uint8_t* w_scales;  // packed scales
@@ -490,7 +475,7 @@ __global__ __launch_bounds__(64 * WT * WN) void k_mx_gemm(LinearArgs a, int tile
     const typename G::Step ahead = m.step(ks + 3);
     m.shift(sc);
     m.template product<0, FN + FT>(f0, sc, o, [&](auto i) { m.part(now, 1, f1, i()); });
-    wait_loads<G::PER>();  // the next step's, of those that are on their way
+    wait_loads_and_reads<G::PER>();  // the next step's, of those that are on their way
     meet();
     typename G::Scales after;  // (behind the last step: of nothing that is used)
     m.template product<1, G::PER + 1 + FN + FT>(f1, sc, o, [&](auto i) {
@@ -504,7 +489,7 @@ __global__ __launch_bounds__(64 * WT * WN) void k_mx_gemm(LinearArgs a, int tile
   m.load(b0, 0);
   m.load(b1, 1);
   m.load(b2, 2);
-  wait_loads<2 * G::PER>();
+  wait_loads_and_reads<2 * G::PER>();
   meet();
   m.scales_of(b0, sc);
 #pragma unroll
@@ -515,7 +500,7 @@ __global__ __launch_bounds__(64 * WT * WN) void k_mx_gemm(LinearArgs a, int tile
     if (ks + 1 < steps) turn(ks + 1, b1, b2);
     if (ks + 2 < steps) turn(ks + 2, b2, b0);
   }
-  wait_loads<0>();
+  wait_loads_and_reads<0>();
 
   if (a.f32) {
 #pragma unroll

@@ -37,13 +37,6 @@ __device__ __forceinline__ double wave_sum(double v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
-  const v2b r = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, r);
-}
 
 struct NormArgs {
   const uint16_t* x;
