@@ -666,7 +666,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_chunk(SplitAr
   }
   w.finish();
   if (slot > last_slot) return;
-  if (n == slot - (it.tile * W + wave) * 32 && lane < 32 && sp == 0 && a.S > 1) a.part_n[at * a.n_q + head] = it.splits;
+  if (lane < 32 && sp == 0 && a.S > 1) a.part_n[at * a.n_q + head] = it.splits;
   if (it.splits == 1) {
     const float inv = w.limit < 0 ? 0.0f : 1.0f / w.l, ts = a.v_ts;
     // A lane holds 4 of every 8 elements, its partner in the other half of the wave the
