@@ -651,7 +651,13 @@ def attention_forward(cache: KvCache, buf: AttnBuffers, qkv, T: int, scale: floa
     that every chunk of a prompt attends to what the cache holds.  chunk, in
     place of prompt: the same straight over the cache, without k and v
     (buffers made with chunk=True; decode rows of other slots may be among the
-    step's)."""
+    step's).  The answers are the same but for rounding.  Time (32 query and 4
+    key/value heads of 128, NVFP4): with neither, a few rows a sequence, up to
+    some 128 behind 8192 tokens, are the fastest (8 slots of one row behind 16000
+    22 us, chunk 51, prompt 301); chunk is for more rows behind a long cache (512
+    behind 8192: 99 us, else 118, prompt 133), alone or among decode rows; prompt
+    for thousands of rows (4096 behind 12288: 775 us, chunk 897; 2048 behind none:
+    53 us, else 67, chunk 86)."""
     c, D = cache.desc, cache.D
     qw, kw = cache.n_q * D, cache.n_kv * D
     if chunk and prompt is not None:

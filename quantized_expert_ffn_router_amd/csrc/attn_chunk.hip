@@ -11,10 +11,12 @@
 // registers.  Where the tiles are fewer than the CUs hold, sequences are split along the
 // tokens and the parts joined, as in a decode step.
 //
-// 32 query and 4 key/value heads of 128 over NVFP4: 4096 rows behind 12288 tokens 863 to 907
-// us (1.07 to 1.13 PFLOP/s; a bf16 library product 1.2), 64 rows behind 32768 tokens 55 us
-// (the join of 33 MB of parts 7 of it); 512 rows of 8 slots, 505 of them one's, over Q8_0
-// with heads of 64 90 us.  In the first the matrix units are half of the time busy at the
+// 32 query and 4 key/value heads of 128 over NVFP4: 4096 rows behind 12288 tokens 863 to 930
+// us (1.03 to 1.11 PFLOP/s; a bf16 library product 1.2; over Q8_0 954, 16 bits 844), 64 rows
+// behind 32768 tokens 55 to 63 us (the join of 33 MB of parts 7 of it; Q8_0 62, 16 bits 57);
+// 512 rows of 8 slots, 505 of them one's, over Q8_0 with heads of 64 85 to 91 us.  Beside
+// the other calls, 512 rows behind 8192: 99 us, k_attn_decode 118, read back and k_attn_prompt
+// 133; 64 rows behind 8192 37, 29 and 126; 4096 behind 12288 897, - and 775.  In the first the matrix units are half of the time busy at the
 // 2.1 GHz they hold, the vector units (exponentials, maxima, rounding, decoding) as long and
 // LDS as well (256 KB of fragments a turn): 256 rows a workgroup is what the registers hold,
 // and it halves the decoding and the reads of the cache against 128 (1222 us).  Reading the

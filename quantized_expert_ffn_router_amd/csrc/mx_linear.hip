@@ -14,10 +14,10 @@
 // (0, 1) and (2, 3) of a 128-element step (16x16x128) or of both blocks of a 64-element
 // one: lane group g holds elements 16 g.. of each half, and the scale of block g.
 //
-// A few rows are bound by reading the weights (5 x 100003 x 2048: 20.9 us, 5.2 TB/s, above a
-// large copy's 4.9), and below some 10 MB of them by the launch and the chain of loads,
-// products and the waves' sum (1 x 5120 x 2048 3.0 us, 8 x 2048 x 4096 3.6).  Many rows: see
-// there.
+// A few rows are bound by reading the weights (5 x 100003 x 2048: 22.3 us, 4.9 TB/s, a large
+// copy's rate), and below some 10 MB of them by the launch and the chain of loads, products
+// and the waves' sum (1 x 5120 x 2048 3.5 us, 8 x 2048 x 4096 4.4; out of the caches 4.2 and
+// 4.7).  Many rows: see there.
 #include <algorithm>
 #include <type_traits>
 
@@ -254,7 +254,7 @@ Few few_of(int steps, int tiles) {
   Few f;
   const int most = 16;
   // two steps of K a wave while the waves of a workgroup reach over all of it, four for many
-  // outputs of a longer K (5 x 100003 x 2048 20.9 us, with two 22.3)
+  // outputs of a longer K (5 x 100003 x 2048 23.0 us, with two 24.3)
   f.ks = steps <= 8 || (steps <= 2 * most && tiles < 1024) ? 2 : 4;
   f.waves = std::min((steps + f.ks - 1) / f.ks, most);
   f.passes = (steps + f.ks * f.waves - 1) / (f.ks * f.waves);
@@ -282,8 +282,10 @@ void launch_few(const LinearArgs& a, hipStream_t stream) {
 // are in registers by then, those of the next step's first half are read beside it, so
 // that the matrix units do not wait for LDS.
 //
-// 16384 x 5120 x 2048 of 8-bit rows 154 to 158 us (2.2 PFLOP/s), of 4-bit rows 130 (2.6); 8192
-// x 2048 x 4096 53 and 40.5 (2.6 and 3.4), where a bf16 library product reaches 1.2.  The
+// 16384 x 5120 x 2048 of 8-bit rows 154 to 169 us (2.0 to 2.2 PFLOP/s), of 4-bit rows 138 (2.5);
+// 8192 x 2048 x 4096 62 and 45 (2.2 and 3.1), 53 and 39 where rows and results stay in the last
+// cache; a bf16 library product reaches 1.2, the instructions themselves, from registers, 4.7
+// and 8.2.  32-bit results take longer to store: 236 and 211 us, 75 and 71.  The
 // matrix units are half of the time busy at the 2.1 GHz they hold: codes that are all zero
 // took 14 % less (power), steps whose loads read nothing a quarter less than that: loads into
 // LDS beside the reads of it.  Two groups of waves that take every other step: no gain.
@@ -619,8 +621,8 @@ hipError_t launch_mx_pack(int N, int K, const uint8_t* codes, const uint8_t* sca
 }
 
 // Few rows whose codes a workgroup's waves hold: each workgroup makes them again (16 x 5120 x
-// 2048, 8 bits: 6.2 us, where a launch of its own takes 1.8 beside the product's 4.9 and a
-// gap; 5 x 100003 24.9 against 1.8 and 20.9).
+// 2048, 8 bits: 6.8 us, where a launch of its own takes 2.3 beside the product's 5.4; 5 x
+// 100003 x 2048, 512 workgroups, 25.5 against 24.2 for the two launches).
 bool mx_linear_takes_rows(int64_t N, int64_t K, int64_t T) {
   const MxLayout l = mx_layout(N, K);
   const Few f = few_of((int)l.steps, (int)std::min(l.tiles, (int64_t)INT32_MAX));

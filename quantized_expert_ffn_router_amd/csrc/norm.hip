@@ -9,10 +9,12 @@
 // plain fp32 operations run per cycle here); the codes are those of z.
 //
 // Bound by memory: 16384 rows of 2048 with a residual, both 16-bit outputs and 8-bit codes
-// 55 us (5.5 TB/s, above a large copy's 4.9), 16384 rows of 4096 into 8 bits 36 us (5.6); 8
-// rows are a launch, 2.4 and 1.7 us in a graph.  A row to a workgroup's waves, as many as
-// hold it 16 or 32 bytes a lane: no loop over rows, in which the loads of the next row would
-// take the registers that the widened values need (155 us, with spills).
+// 54 to 57 us (5.3 to 5.6 TB/s, above a large copy's 4.9), 16384 rows of 4096 into 8 bits 36 to
+// 38 us (5.4); over the same buffers again and again, which the last cache holds in part, 4-bit
+// codes 50 against 56 and 26 against 30, the sum and codes alone 34 (4 bits) and 36.  8 rows are
+// a launch, 2.9 and 2.3 us in a graph.  A row to a workgroup's waves, as many as hold it 16 or
+// 32 bytes a lane: no loop over rows, in which the loads of the next row would take the
+// registers that the widened values need (155 us, with spills).
 #include <algorithm>
 
 #include "mx.h"
