@@ -149,3 +149,17 @@ def test_norm_over_norm_of_8_bit_rows():
             err[fmt, T] = float((run(m, rows, True) - y).norm() / y.norm())
     print(err, flush=True)
     assert max(err[MXFP8, 16], err[MXFP8, 300]) <= 2e-5 and max(err[MXFP4, 16], err[MXFP4, 300]) <= 2e-6
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_a_nan_code(T):
+    """E4M3 has codes for NaN, too: a row that holds one is NaN, no other."""
+    gen = torch.Generator(dev).manual_seed(T)
+    m, w, _, bias = matrix(77, 1152, gen, True)
+    rows = Rows(MXFP8, T, 1152, gen)
+    want = run(m, rows, True)
+    rows.codes[1, 700], rows.codes[2, 3] = 0x7F, 0xFF
+    got = run(m, rows, True)
+    assert bool(got[1:3].isnan().all())
+    keep = torch.arange(T, device=dev).sub(1.5).abs() > 1
+    assert torch.equal(got[keep], want[keep])
